@@ -18,7 +18,11 @@ __all__ = [
     "attn_bwd_finalize", "attn_bwd_noalloc", "attn_device_status", "attn_strerror",
     "attn_selftest_wait_timeout", "attn_bwd_dq_partials_bytes", "attn_bwd_deterministic",
     "attn_bwd_finalize_partials", "attn_fwd_ref_dropout", "attn_bwd_dropout", "attn_fwd_local",
-    "attn_fwd_ref_local", "attn_bwd_local", "attn_fwd_dropout",
+    "attn_fwd_ref_local", "attn_bwd_local", "attn_fwd_dropout", "attn_rotary_frequencies",
+    "attn_rotary", "attn_bwd_finalize_rotary", "attn_layer_norm", "attn_layer_norm_bwd",
+    "attn_layer_norm_bwd_workspace_bytes", "attn_dropout_add", "attn_dropout_add_norm",
+    "attn_dropout_add_norm_bwd", "ATTN_BF16", "ATTN_FP16", "ATTN_FP32", "ATTN_ROTARY_PLAIN",
+    "ATTN_ROTARY_LINEAR", "ATTN_ROTARY_BASE", "ATTN_ROTARY_RAMP",
     "ATTN_OK", "ATTN_ERR_NULL", "ATTN_ERR_SHAPE", "ATTN_ERR_UNSUPPORTED", "ATTN_ERR_ALIGN",
     "ATTN_ERR_LAUNCH", "ATTN_ERR_DEVICE_TIMEOUT", "ATTN_ERR_DEVICE", "ATTN_ERR_TOO_LARGE",
 ]
@@ -33,9 +37,21 @@ ATTN_ERR_DEVICE_TIMEOUT = -6
 ATTN_ERR_DEVICE = -7
 ATTN_ERR_TOO_LARGE = -8
 
+ATTN_BF16 = 0
+ATTN_FP16 = 1
+ATTN_FP32 = 2
+
+ATTN_ROTARY_PLAIN = 0
+ATTN_ROTARY_LINEAR = 1
+ATTN_ROTARY_BASE = 2
+ATTN_ROTARY_RAMP = 3
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_D = ctypes.c_double
+_L = ctypes.c_longlong
+_U = ctypes.c_ulonglong
 
 _SIGNATURES = {
     "attn_fwd_ref": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _P],
@@ -59,6 +75,17 @@ _SIGNATURES = {
     "attn_fwd_ref_local": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _I, _I, _P],
     "attn_bwd_local": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _P,
                        _I, _I, _P],
+    "attn_rotary_frequencies": [ctypes.POINTER(_U), ctypes.POINTER(_F), _I, _D, _I, _D, _I, _D,
+                                _D],
+    "attn_rotary": [_P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P, _P],
+    "attn_bwd_finalize_rotary": [_P, _P, _P, _P, _F, _P, _P, _L, _I, _I, _I, _I, _I, _I, _F, _I,
+                                 _P, _P],
+    "attn_layer_norm": [_P, _P, _P, _P, _P, _P, _L, _I, _F, _I, _I, _P],
+    "attn_layer_norm_bwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _P],
+    "attn_dropout_add": [_P, _P, _P, _L, _F, _U, _I, _P],
+    "attn_dropout_add_norm": [_P, _P, _P, _P, _P, _P, _P, _P, _L, _I, _F, _F, _U, _I, _I, _P],
+    "attn_dropout_add_norm_bwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _L, _I, _F, _U, _I,
+                                  _I, _P],
 }
 
 _lib = None
@@ -85,6 +112,8 @@ def library():
             fn.restype = ctypes.c_int
         lib.attn_bwd_dq_partials_bytes.argtypes = [_I, _I, _I, _I, _I]
         lib.attn_bwd_dq_partials_bytes.restype = ctypes.c_longlong
+        lib.attn_layer_norm_bwd_workspace_bytes.argtypes = [_L, _I]
+        lib.attn_layer_norm_bwd_workspace_bytes.restype = ctypes.c_longlong
         lib.attn_strerror.argtypes = [ctypes.c_int]
         lib.attn_strerror.restype = ctypes.c_char_p
         _lib = lib
@@ -205,6 +234,80 @@ def attn_bwd_deterministic(q, k, v, o, dO, lse, dq_partials, dk, dv, B, H, H_kv,
 def attn_bwd_finalize_partials(dq_partials, dq, scale, B, H, N, d, causal, stream=None):
     return library().attn_bwd_finalize_partials(_ptr(dq_partials), _ptr(dq), scale, B, H, N, d,
                                                 int(causal), _stream(stream))
+
+
+def attn_rotary_frequencies(rot, base=10000.0, scaling=ATTN_ROTARY_PLAIN, factor=1.0,
+                            original_length=0, low_turns=1.0, high_turns=32.0):
+    """Returns (rc, turns, magnitude): turns is a list of rot / 2 integers,
+    turns per position in units of 2^-64 turn (computed on the host)."""
+    n = max(int(rot) // 2, 0)
+    turns, magnitude = (_U * max(n, 1))(), _F(0.0)
+    rc = library().attn_rotary_frequencies(turns, ctypes.byref(magnitude), int(rot), base,
+                                           int(scaling), factor, int(original_length), low_turns,
+                                           high_turns)
+    return rc, list(turns[:n]), magnitude.value
+
+
+def _strides(values, count):
+    """A C array of `count` element strides, or NULL."""
+    if values is None:
+        return None
+    if len(values) != count:
+        raise ValueError("expected %d strides, got %d" % (count, len(values)))
+    return (_L * count)(*values)
+
+
+def attn_rotary(q, k, q_out, k_out, turns, positions, pos_stride, B, H, H_kv, N, d, rot, magnitude,
+                interleaved, adjoint, dtype, strides=None, stream=None):
+    return library().attn_rotary(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(turns),
+                                 _ptr(positions), pos_stride, B, H, H_kv, N, d, rot, magnitude,
+                                 int(interleaved), int(adjoint), dtype, _strides(strides, 12),
+                                 _stream(stream))
+
+
+def attn_bwd_finalize_rotary(dq_accum, dq, dk, dk_out, scale, turns, positions, pos_stride, B, H,
+                             H_kv, N, d, rot, magnitude, interleaved, strides=None, stream=None):
+    return library().attn_bwd_finalize_rotary(
+        _ptr(dq_accum), _ptr(dq), _ptr(dk), _ptr(dk_out), scale, _ptr(turns), _ptr(positions),
+        pos_stride, B, H, H_kv, N, d, rot, magnitude, int(interleaved), _strides(strides, 6),
+        _stream(stream))
+
+
+def attn_layer_norm(x, gamma, beta, y, mean, rstd, rows, C, eps, dtype, wdtype, stream=None):
+    return library().attn_layer_norm(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean),
+                                     _ptr(rstd), rows, C, eps, dtype, wdtype, _stream(stream))
+
+
+def attn_layer_norm_bwd_workspace_bytes(rows, C):
+    return library().attn_layer_norm_bwd_workspace_bytes(rows, C)
+
+
+def attn_layer_norm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, rows, C, dtype,
+                        wdtype, stream=None):
+    return library().attn_layer_norm_bwd(
+        _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dgamma),
+        _ptr(dbeta), _ptr(workspace), rows, C, dtype, wdtype, _stream(stream))
+
+
+def attn_dropout_add(x, residual, y, n, p_drop, seed, dtype, stream=None):
+    return library().attn_dropout_add(_ptr(x), _ptr(residual), _ptr(y), n, p_drop,
+                                      int(seed) & 0xFFFFFFFFFFFFFFFF, dtype, _stream(stream))
+
+
+def attn_dropout_add_norm(x, residual, gamma, beta, z, y, mean, rstd, rows, C, eps, p_drop, seed,
+                          dtype, wdtype, stream=None):
+    return library().attn_dropout_add_norm(
+        _ptr(x), _ptr(residual), _ptr(gamma), _ptr(beta), _ptr(z), _ptr(y), _ptr(mean),
+        _ptr(rstd), rows, C, eps, p_drop, int(seed) & 0xFFFFFFFFFFFFFFFF, dtype, wdtype,
+        _stream(stream))
+
+
+def attn_dropout_add_norm_bwd(dy, dz_in, z, gamma, mean, rstd, dx, dresidual, dgamma, dbeta,
+                              workspace, rows, C, p_drop, seed, dtype, wdtype, stream=None):
+    return library().attn_dropout_add_norm_bwd(
+        _ptr(dy), _ptr(dz_in), _ptr(z), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
+        _ptr(dresidual), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), rows, C, p_drop,
+        int(seed) & 0xFFFFFFFFFFFFFFFF, dtype, wdtype, _stream(stream))
 
 
 def attn_device_status(clear=True, stream=None):

@@ -1,13 +1,24 @@
 """Convenience wrappers that allocate device memory with torch and call the
 C ABI in stream order: forward (O, LSE), then preprocess -> attn_bwd ->
-finalize. No arithmetic happens here; torch provides memory and streams.
+finalize, and the operators around them (rotary positions, layer norm,
+dropout with a residual). No arithmetic happens here; torch provides memory
+and streams.
 """
 import torch
 
-from . import (attn_bwd, attn_bwd_deterministic, attn_bwd_dq_partials_bytes, attn_bwd_dropout,
-               attn_bwd_finalize, attn_bwd_finalize_partials, attn_bwd_local, attn_bwd_preprocess,
-               attn_fwd, attn_fwd_dropout, attn_fwd_local, attn_fwd_ref, attn_fwd_ref_dropout,
-               attn_fwd_ref_local, check)
+from . import (ATTN_BF16, ATTN_FP16, ATTN_FP32, ATTN_ROTARY_BASE, ATTN_ROTARY_LINEAR,
+               ATTN_ROTARY_PLAIN, ATTN_ROTARY_RAMP, attn_bwd, attn_bwd_deterministic,
+               attn_bwd_dq_partials_bytes, attn_bwd_dropout, attn_bwd_finalize,
+               attn_bwd_finalize_partials, attn_bwd_finalize_rotary, attn_bwd_local,
+               attn_bwd_preprocess, attn_dropout_add, attn_dropout_add_norm,
+               attn_dropout_add_norm_bwd, attn_fwd, attn_fwd_dropout, attn_fwd_local,
+               attn_fwd_ref, attn_fwd_ref_dropout, attn_fwd_ref_local, attn_layer_norm,
+               attn_layer_norm_bwd, attn_layer_norm_bwd_workspace_bytes, attn_rotary,
+               attn_rotary_frequencies, check)
+
+_DTYPES = {torch.bfloat16: ATTN_BF16, torch.float16: ATTN_FP16, torch.float32: ATTN_FP32}
+_SCALINGS = {"plain": ATTN_ROTARY_PLAIN, "linear": ATTN_ROTARY_LINEAR, "base": ATTN_ROTARY_BASE,
+             "ramp": ATTN_ROTARY_RAMP}
 
 
 def _dims(q, k, *others):
@@ -84,39 +95,54 @@ class BackwardBuffers:
 
 
 def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=None,
-             deterministic=False, dropout=None, window=None):
+             deterministic=False, dropout=None, window=None, rotary=None, positions=None):
     """dQ, dK, dV (bf16) via preprocess -> attn_bwd -> finalize, or, with
     deterministic=True, preprocess -> attn_bwd_deterministic ->
     finalize_partials (dQ identical bit for bit from run to run). window =
-    (left, right) runs attn_bwd_local in place of attn_bwd."""
+    (left, right) runs attn_bwd_local in place of attn_bwd. rotary = the
+    Rotary that q and k came from (with the same positions): dQ and dK are
+    then the gradients of what went into it (attn_bwd_finalize_rotary in
+    place of attn_bwd_finalize)."""
     B, H, H_kv, N, d = _dims(q, k, v, o, do)
     if v.shape != k.shape or o.shape != q.shape or do.shape != q.shape:
         raise ValueError("v must have the shape of k, and o, dO that of q")
     _check_lse(lse, B, H, N, q.device)
+    if rotary is not None:
+        positions, pos_stride = _check_rotary(rotary, positions, B, N, d, q.device)
+    elif positions is not None:
+        raise ValueError("positions are those of a rotary")
     s = _stream(stream)
     if bufs is None:
         bufs = BackwardBuffers(q, k)
+
+    def finalize():
+        if rotary is None:
+            check(attn_bwd_finalize(bufs.dq_accum, bufs.dq, scale, B, H, N, d, s))
+        else:
+            check(attn_bwd_finalize_rotary(bufs.dq_accum, bufs.dq, bufs.dk, bufs.dk, scale,
+                                           rotary.turns, positions, pos_stride, B, H, H_kv, N, d,
+                                           rotary.rot, rotary.magnitude, rotary.interleaved, None,
+                                           s))
+        return bufs.dq, bufs.dk, bufs.dv
+
     if dropout is not None:
         check(attn_bwd_preprocess(o, do, bufs.dpsum, bufs.dq_accum, B, H, N, d, s))
         check(attn_bwd_dropout(q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv, B, H, H_kv,
                                N, d, scale, causal, softcap, bufs.dpsum, dropout[0], dropout[1],
                                s))
-        check(attn_bwd_finalize(bufs.dq_accum, bufs.dq, scale, B, H, N, d, s))
-        return bufs.dq, bufs.dk, bufs.dv
+        return finalize()
     if window is not None:
         if deterministic:
             raise ValueError("the local window has no deterministic variant")
         check(attn_bwd_preprocess(o, do, bufs.dpsum, bufs.dq_accum, B, H, N, d, s))
         check(attn_bwd_local(q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv, B, H, H_kv, N,
                              d, scale, causal, softcap, bufs.dpsum, window[0], window[1], s))
-        check(attn_bwd_finalize(bufs.dq_accum, bufs.dq, scale, B, H, N, d, s))
-        return bufs.dq, bufs.dk, bufs.dv
+        return finalize()
     if not deterministic:
         check(attn_bwd_preprocess(o, do, bufs.dpsum, bufs.dq_accum, B, H, N, d, s))
         check(attn_bwd(q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv, B, H, H_kv, N, d,
                        scale, causal, softcap, bufs.dpsum, s))
-        check(attn_bwd_finalize(bufs.dq_accum, bufs.dq, scale, B, H, N, d, s))
-        return bufs.dq, bufs.dk, bufs.dv
+        return finalize()
     nbytes = attn_bwd_dq_partials_bytes(B, H, N, d, causal)
     if nbytes < 0:
         check(int(nbytes))
@@ -126,4 +152,221 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
     check(attn_bwd_deterministic(q, k, v, o, do, lse, bufs.dq_partials, bufs.dk, bufs.dv, B, H,
                                  H_kv, N, d, scale, causal, softcap, bufs.dpsum, s))
     check(attn_bwd_finalize_partials(bufs.dq_partials, bufs.dq, scale, B, H, N, d, causal, s))
+    if rotary is not None:
+        check(attn_rotary(bufs.dq, bufs.dk, bufs.dq, bufs.dk, rotary.turns, positions, pos_stride,
+                          B, H, H_kv, N, d, rotary.rot, rotary.magnitude, rotary.interleaved, True,
+                          ATTN_BF16, None, s))
     return bufs.dq, bufs.dk, bufs.dv
+
+
+# ------------------------------------------------ around the attention call
+def _stream_of(stream, device):
+    """The caller's stream, or the current one of the tensors' device."""
+    return stream if stream is not None else torch.cuda.current_stream(device)
+
+
+def _check_cuda(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (t.device != device or t.device.type != "cuda"):
+            raise ValueError("%s must be on the same CUDA device as the other tensors" % name)
+
+
+def _check_like(like, **tensors):
+    """Contiguous tensors of like's shape and type."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.shape != like.shape or t.dtype != like.dtype:
+            raise ValueError("%s must have the shape and dtype %s, %s" % (name, tuple(like.shape),
+                                                                          like.dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+class Rotary:
+    """Rotary frequencies on a device: rot columns of each row turn, in pairs
+    (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved=True. scaling is
+    "plain", "linear", "base" or "ramp" (attn_rotary_frequencies)."""
+
+    def __init__(self, rot, device, base=10000.0, scaling="plain", factor=1.0, original_length=0,
+                 low_turns=1.0, high_turns=32.0, interleaved=False):
+        if scaling not in _SCALINGS:
+            raise ValueError("scaling must be one of %s" % ", ".join(sorted(_SCALINGS)))
+        rc, turns, self.magnitude = attn_rotary_frequencies(
+            rot, base, _SCALINGS[scaling], factor, original_length, low_turns, high_turns)
+        check(rc)
+        self.rot, self.interleaved = int(rot), bool(interleaved)
+        self.turns = torch.tensor(turns or [0], dtype=torch.int64, device=device)
+
+
+def _check_rotary(plan, positions, B, N, d, device):
+    """(positions, their batch stride) after checking them and the plan."""
+    if plan.rot > d:
+        raise ValueError("rot = %d exceeds the head dimension %d" % (plan.rot, d))
+    _check_cuda(device, turns=plan.turns, positions=positions)
+    if positions is None:
+        return None, 0
+    if positions.dtype != torch.int64 or tuple(positions.shape) not in ((N,), (B, N)):
+        raise ValueError("positions must be an int64 tensor of shape [N] or [B, N]")
+    if N > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions must be contiguous along N")
+    return positions, positions.stride(0) if positions.dim() == 2 else 0
+
+
+def rotary(q, k, plan, positions=None, adjoint=False, out=None, stream=None):
+    """(q, k) rotated (attn_rotary), contiguous [B, heads, N, d]. q
+    [B,H,N,d] and k [B,H_kv,N,d] (or None) may be strided as long as their
+    rows are contiguous, e.g. parts of a packed [B, N, H + 2 H_kv, d]
+    projection transposed. positions: int64 [N] or [B, N], default 0 .. N - 1.
+    out = (q_out, k_out): written in place of new tensors (they may be strided
+    too, and may be q and k)."""
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be 4-D ([B, heads, N, d])")
+    B, H, N, d = q.shape
+    if k is not None and (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
+        raise ValueError("k has shape %s, expected [%d, heads, %d, %d]" % (tuple(k.shape), B, N, d))
+    if q.dtype not in _DTYPES or (k is not None and k.dtype != q.dtype):
+        raise ValueError("q and k must both be bfloat16, float16 or float32")
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    for x, y in ((q, out[0]), (k, out[1])):
+        if x is None:
+            continue
+        if y is None or y.shape != x.shape or y.dtype != x.dtype:
+            raise ValueError("out must have the shapes and dtype of q and k")
+        if d > 1 and (x.stride(3) != 1 or y.stride(3) != 1):
+            raise ValueError("rows must be contiguous")
+    _check_cuda(q.device, q=q, k=k, q_out=out[0], k_out=out[1])
+    positions, pos_stride = _check_rotary(plan, positions, B, N, d, q.device)
+    parts = [q, q if k is None else k, out[0], out[0] if k is None else out[1]]
+    strides = [v for t in parts for v in t.stride()[:3]]
+    with torch.cuda.device(q.device):
+        check(attn_rotary(q, k, out[0], out[1], plan.turns, positions, pos_stride, B, H,
+                          0 if k is None else k.shape[1], N, d, plan.rot, plan.magnitude,
+                          plan.interleaved, adjoint, _DTYPES[q.dtype], strides,
+                          _stream_of(stream, q.device)))
+    return out
+
+
+def _norm_dims(x, gamma, beta):
+    """(rows, C, dtype code, weight dtype code) of x [..., C]."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("expected a tensor [..., C] with C >= 1")
+    if x.dtype not in _DTYPES:
+        raise ValueError("expected a bfloat16, float16 or float32 tensor, got %s" % x.dtype)
+    if not x.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    C = x.shape[-1]
+    wd = None
+    for name, w in (("gamma", gamma), ("beta", beta)):
+        if w is None:
+            continue
+        if tuple(w.shape) != (C,) or not w.is_contiguous():
+            raise ValueError("%s must be a contiguous [%d] tensor" % (name, C))
+        if w.dtype not in _DTYPES or (wd is not None and w.dtype != wd):
+            raise ValueError("gamma and beta must share one of the types bfloat16, float16, "
+                             "float32")
+        wd = w.dtype
+    _check_cuda(x.device, x=x, gamma=gamma, beta=beta)
+    return x.numel() // C, C, _DTYPES[x.dtype], _DTYPES[wd or x.dtype]
+
+
+def _row_stats(x):
+    return tuple(torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+                 for _ in range(2))
+
+
+def layer_norm(x, gamma=None, beta=None, eps=1e-5, stream=None):
+    """(y, mean, rstd) of x [..., C] (attn_layer_norm)."""
+    rows, C, code, wcode = _norm_dims(x, gamma, beta)
+    y = torch.empty_like(x)
+    mean, rstd = _row_stats(x)
+    with torch.cuda.device(x.device):
+        check(attn_layer_norm(x, gamma, beta, y, mean, rstd, rows, C, eps, code, wcode,
+                              _stream_of(stream, x.device)))
+    return y, mean, rstd
+
+
+def _check_stats(x, mean, rstd):
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous float32 %s tensor"
+                             % (name, list(x.shape[:-1])))
+    _check_cuda(x.device, mean=mean, rstd=rstd)
+
+
+def _weight_grads(x, gamma, want, rows, C, wdtype):
+    """(dgamma, dbeta, workspace): None where not wanted."""
+    if not want:
+        return None, None, None
+    nbytes = attn_layer_norm_bwd_workspace_bytes(rows, C)
+    if nbytes < 0:
+        check(int(nbytes))
+    dt = gamma.dtype if gamma is not None else wdtype
+    grads = [torch.empty(C, dtype=dt, device=x.device) for _ in range(2)]
+    return grads[0], grads[1], torch.empty(nbytes // 4, dtype=torch.float32, device=x.device)
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, weight_grads=True, stream=None):
+    """(dx, dgamma, dbeta) of layer_norm (attn_layer_norm_bwd); dgamma and
+    dbeta have gamma's type (x's if gamma is None), or are None with
+    weight_grads=False."""
+    rows, C, code, wcode = _norm_dims(x, gamma, None)
+    _check_like(x, dy=dy)
+    _check_cuda(x.device, dy=dy)
+    _check_stats(x, mean, rstd)
+    dx = torch.empty_like(x)
+    dgamma, dbeta, workspace = _weight_grads(x, gamma, weight_grads, rows, C, x.dtype)
+    with torch.cuda.device(x.device):
+        check(attn_layer_norm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, rows, C,
+                                  code, wcode, _stream_of(stream, x.device)))
+    return dx, dgamma, dbeta
+
+
+def dropout_add(x, residual=None, dropout=(0.0, 0), stream=None):
+    """residual + dropout(x) (attn_dropout_add), dropout = (p_drop, seed); the
+    adjoint is the call on dy without a residual."""
+    if x.dtype not in _DTYPES:
+        raise ValueError("expected a bfloat16, float16 or float32 tensor, got %s" % x.dtype)
+    _check_like(x, x=x, residual=residual)
+    _check_cuda(x.device, x=x, residual=residual)
+    y = torch.empty_like(x)
+    with torch.cuda.device(x.device):
+        check(attn_dropout_add(x, residual, y, x.numel(), dropout[0], dropout[1],
+                               _DTYPES[x.dtype], _stream_of(stream, x.device)))
+    return y
+
+
+def dropout_add_norm(x, residual, gamma=None, beta=None, eps=1e-5, dropout=(0.0, 0), stream=None):
+    """(z, y, mean, rstd): z = residual + dropout(x), y its layer norm
+    (attn_dropout_add_norm)."""
+    rows, C, code, wcode = _norm_dims(x, gamma, beta)
+    _check_like(x, residual=residual)
+    _check_cuda(x.device, residual=residual)
+    z, y = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = _row_stats(x)
+    with torch.cuda.device(x.device):
+        check(attn_dropout_add_norm(x, residual, gamma, beta, z, y, mean, rstd, rows, C, eps,
+                                    dropout[0], dropout[1], code, wcode,
+                                    _stream_of(stream, x.device)))
+    return z, y, mean, rstd
+
+
+def dropout_add_norm_backward(dy, dz, z, gamma, mean, rstd, dropout=(0.0, 0), weight_grads=True,
+                              stream=None):
+    """(dx, dresidual, dgamma, dbeta) of dropout_add_norm
+    (attn_dropout_add_norm_bwd); dz is the gradient that reaches z by its
+    other uses, or None. Without dropout dx is dresidual."""
+    rows, C, code, wcode = _norm_dims(z, gamma, None)
+    _check_like(z, dy=dy, dz=dz)
+    _check_cuda(z.device, dy=dy, dz=dz)
+    _check_stats(z, mean, rstd)
+    dres = torch.empty_like(z)
+    dx = torch.empty_like(z) if dropout[0] != 0 else None
+    dgamma, dbeta, workspace = _weight_grads(z, gamma, weight_grads, rows, C, z.dtype)
+    with torch.cuda.device(z.device):
+        check(attn_dropout_add_norm_bwd(dy, dz, z, gamma, mean, rstd, dx, dres, dgamma, dbeta,
+                                        workspace, rows, C, dropout[0], dropout[1], code, wcode,
+                                        _stream_of(stream, z.device)))
+    return (dres if dx is None else dx), dres, dgamma, dbeta

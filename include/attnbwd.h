@@ -55,7 +55,7 @@ extern "C" {
 #define ATTN_OK 0
 #define ATTN_ERR_NULL (-1)           /* a required pointer is NULL */
 #define ATTN_ERR_SHAPE (-2)          /* negative size, H % H_kv != 0, bad scale ... */
-#define ATTN_ERR_UNSUPPORTED (-3)    /* head dimension not supported by this call */
+#define ATTN_ERR_UNSUPPORTED (-3)    /* head dimension or element type not supported */
 #define ATTN_ERR_ALIGN (-4)          /* a pointer is not 16-byte aligned */
 #define ATTN_ERR_LAUNCH (-5)         /* CUDA reported an error at launch */
 #define ATTN_ERR_DEVICE_TIMEOUT (-6) /* a kernel gave up waiting (device status) */
@@ -259,6 +259,166 @@ int attn_bwd_finalize(const float* dq_accum, void* dq, float scale, int B, int H
 int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, const void* dO,
                      const float* lse, void* dq, void* dk, void* dv, int B, int H, int H_kv,
                      int N, int d, float scale, int causal, float softcap, void* stream);
+
+/*
+ * Operators around the attention call: rotary positions on Q and K, layer
+ * norm, and dropout with a residual. They take bf16, fp16 or fp32 elements
+ * (`dtype`; norm weights, biases and their gradients have a type of their
+ * own, `wdtype`; row statistics are fp32), compute in fp32 and round each
+ * output once. An unknown type code returns ATTN_ERR_UNSUPPORTED. Pointers of
+ * an empty problem (no rows) may be NULL.
+ */
+#define ATTN_BF16 0
+#define ATTN_FP16 1
+#define ATTN_FP32 2
+
+/*
+ * attn_rotary_frequencies: HOST function (no launch): fills turns[rot / 2]
+ * (host memory) with the rotary frequencies, as turns per position in units
+ * of 2^-64 turn, and *magnitude with the factor on cosine and sine.
+ *   w_i = base^(-2 i / rot) radians per position, i = 0 .. rot / 2 - 1;
+ *   ATTN_ROTARY_PLAIN   w_i as it is (factor and what follows are ignored);
+ *   ATTN_ROTARY_LINEAR  w_i / factor (positions interpolated; Chen et al.,
+ *                       "Extending context window of large language models
+ *                       via positional interpolation", 2023);
+ *   ATTN_ROTARY_BASE    base := base * factor^(rot / (rot - 2)): the highest
+ *                       frequency stays, the lowest is divided by factor;
+ *   ATTN_ROTARY_RAMP    w_i keeps its value where it makes high_turns turns
+ *                       or more over original_length positions, is divided
+ *                       by factor below low_turns turns, and goes over
+ *                       linearly in the number of turns between; magnitude
+ *                       is 1 + 0.1 ln(factor), else 1 (Peng et al., "YaRN:
+ *                       efficient context window extension", 2023).
+ * rot even, base >= 1, factor >= 1 (ATTN_ERR_SHAPE otherwise).
+ */
+#define ATTN_ROTARY_PLAIN 0
+#define ATTN_ROTARY_LINEAR 1
+#define ATTN_ROTARY_BASE 2
+#define ATTN_ROTARY_RAMP 3
+int attn_rotary_frequencies(unsigned long long* turns, float* magnitude, int rot, double base,
+                            int scaling, double factor, int original_length, double low_turns,
+                            double high_turns);
+
+/*
+ * attn_rotary: rotary positions on q and k in one launch. Column pair i of
+ * a row at position p turns by theta = 2 pi p turns[i] / 2^64 (reduced
+ * exactly, in integers, for any 64-bit p) and is multiplied by magnitude:
+ *   a' = m (a cos theta - b sin theta),  b' = m (a sin theta + b cos theta),
+ * (a, b) being columns (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved != 0.
+ * Columns rot .. d - 1 are copied. adjoint != 0 applies the transposed map
+ * (theta -> -theta): it takes gradients of q_out, k_out to those of q, k.
+ * In:  q [B,H,N,d], k [B,H_kv,N,d] of type dtype; turns [rot/2], DEVICE
+ *      memory; positions: DEVICE, element b * pos_stride + n is the position
+ *      of row n of batch b (pos_stride 0: one row of positions for all), or
+ *      NULL: position n. positions must be 8-byte aligned only.
+ * Out: q_out, k_out (overwritten), of the same type.
+ * strides: HOST array of 12 element strides, (batch, head, row) of q, k,
+ *      q_out and k_out; NULL: all contiguous. They let q and k be parts of a
+ *      packed [B, N, H + 2 H_kv, d] projection. A row's d elements are
+ *      contiguous. Outputs must not overlap each other; q_out may be q (k_out
+ *      k) with the same strides, otherwise outputs must not overlap inputs.
+ * H_kv = 0 leaves k out (k, k_out may be NULL), H = 0 leaves q out. H need
+ * not be a multiple of H_kv. 0 <= rot <= d, rot even; rot = 0 copies (turns
+ * may be NULL); any d >= 1. Whole 16-byte groups (d and every stride a
+ * multiple of 16 bytes, and rot one of 32 bytes) run faster than others.
+ */
+int attn_rotary(const void* q, const void* k, void* q_out, void* k_out,
+                const unsigned long long* turns, const long long* positions, long long pos_stride,
+                int B, int H, int H_kv, int N, int d, int rot, float magnitude, int interleaved,
+                int adjoint, int dtype, const long long* strides, void* stream);
+
+/*
+ * attn_bwd_finalize_rotary: attn_bwd_finalize for a backward whose q and k
+ * came out of attn_rotary, with the adjoint of that call, in one launch:
+ *   dq = bf16(R^T (scale * dq_accum)),  dk_out = bf16(R^T dk).
+ * In:  dq_accum [B,H,N,d] fp32, dk [B,H_kv,N,d] bf16 (from attn_bwd and its
+ *      forms), both contiguous; turns, positions, pos_stride, rot, magnitude,
+ *      interleaved as given to attn_rotary.
+ * Out: dq, dk_out bf16; dk_out may be dk if it is contiguous. strides: HOST
+ *      array of 6 element strides, (batch, head, row) of dq and dk_out; NULL:
+ *      contiguous.
+ * H_kv = 0 leaves dk out. Any d >= 1.
+ */
+int attn_bwd_finalize_rotary(const float* dq_accum, void* dq, const void* dk, void* dk_out,
+                             float scale, const unsigned long long* turns,
+                             const long long* positions, long long pos_stride, int B, int H,
+                             int H_kv, int N, int d, int rot, float magnitude, int interleaved,
+                             const long long* strides, void* stream);
+
+/*
+ * attn_layer_norm: layer norm over the C columns of each row,
+ *   mu = mean(x), r = (mean((x - mu)^2) + eps)^(-1/2),
+ *   y = gamma (x - mu) r + beta.
+ * In:  x [rows, C] dtype; gamma, beta [C] wdtype (either may be NULL: 1, 0).
+ * Out: y [rows, C] dtype (may be x); mean, rstd [rows] fp32 (mu and r, which
+ *      the backward reads; either may be NULL).
+ * C >= 1, eps >= 0. Rows of heads ([B,H,N,d] with C = d) and of hidden
+ * states are the same to it.
+ */
+int attn_layer_norm(const void* x, const void* gamma, const void* beta, void* y, float* mean,
+                    float* rstd, long long rows, int C, float eps, int dtype, int wdtype,
+                    void* stream);
+
+/*
+ * attn_layer_norm_bwd: with h = (x - mean) rstd and g = dy gamma,
+ *   dx = rstd (g - mean(g) - h mean(g h)),
+ *   dgamma = sum over rows of dy h, dbeta = sum over rows of dy.
+ * In:  dy, x [rows, C] dtype; gamma [C] wdtype or NULL (1); mean, rstd [rows].
+ * Out: dx [rows, C] dtype (may be dy or x); dgamma, dbeta [C] wdtype,
+ *      overwritten (either may be NULL: not wanted). They are summed in an
+ *      order that depends on rows, C and the GPU's SM count alone: the same
+ *      bits every time. rows = 0 gives zeros.
+ * workspace: attn_layer_norm_bwd_workspace_bytes(rows, C) bytes of device
+ *      memory, whose contents need no preparation and mean nothing after; may
+ *      be NULL if dgamma and dbeta are. Calls that may run at the same time
+ *      (two streams, two captured graphs) need one each.
+ */
+long long attn_layer_norm_bwd_workspace_bytes(long long rows, int C);
+int attn_layer_norm_bwd(const void* dy, const void* x, const void* gamma, const float* mean,
+                        const float* rstd, void* dx, void* dgamma, void* dbeta, float* workspace,
+                        long long rows, int C, int dtype, int wdtype, void* stream);
+
+/*
+ * attn_dropout_add: y = residual + x Z / (1 - p_drop), elementwise over n
+ * elements. Element e is kept (Z = 1) iff word (e mod 4) of
+ * Philox4x32-10(counter = (floor(e / 4) mod 2^32, floor(e / 2^34), 0, 1),
+ * key = (seed mod 2^32, seed >> 32)) is >= round(p_drop * 2^32): the
+ * generator of attn_fwd_dropout at counters that it does not use, so one seed
+ * may serve both. The mask is never stored: the call's adjoint is the call
+ * itself on dy with residual = NULL and the same seed (the residual's
+ * gradient is dy). A dropped element contributes 0 whatever its value.
+ * In:  x [n], residual [n] or NULL (0). Out: y [n] (may be x or residual).
+ * p_drop in [0, 1) (0 = none); the seed is taken at the call, so a captured
+ * graph draws the same mask at each replay.
+ */
+int attn_dropout_add(const void* x, const void* residual, void* y, long long n, float p_drop,
+                     unsigned long long seed, int dtype, void* stream);
+
+/*
+ * attn_dropout_add_norm: attn_dropout_add and attn_layer_norm in one pass,
+ *   z = residual + x Z / (1 - p_drop), y = gamma (z - mu) r + beta,
+ * over [rows, C] (e = row C + column). mu, r and y are those of z before it
+ * is rounded to its type. p_drop = 0 is the serving form.
+ * Out: z, y [rows, C] dtype (z may be x or residual, y may be x or residual;
+ *      z and y distinct); mean, rstd [rows] fp32 or NULL.
+ *
+ * attn_dropout_add_norm_bwd: dz = (attn_layer_norm_bwd's dx for input z)
+ *   + dz_in, dresidual = dz, dx = dz Z / (1 - p_drop).
+ * In:  dy, z [rows, C]; dz_in [rows, C] or NULL (0): the gradient that
+ *      reaches z by its other uses (the next residual).
+ * Out: dresidual, dx [rows, C], distinct, each may be one of the inputs; with
+ *      p_drop = 0 the two are equal and dx may be NULL. dgamma, dbeta,
+ *      workspace as for attn_layer_norm_bwd.
+ */
+int attn_dropout_add_norm(const void* x, const void* residual, const void* gamma,
+                          const void* beta, void* z, void* y, float* mean, float* rstd,
+                          long long rows, int C, float eps, float p_drop, unsigned long long seed,
+                          int dtype, int wdtype, void* stream);
+int attn_dropout_add_norm_bwd(const void* dy, const void* dz_in, const void* z, const void* gamma,
+                              const float* mean, const float* rstd, void* dx, void* dresidual,
+                              void* dgamma, void* dbeta, float* workspace, long long rows, int C,
+                              float p_drop, unsigned long long seed, int dtype, int wdtype,
+                              void* stream);
 
 /*
  * attn_device_status: waits for `stream`, then reads the library's device

@@ -14,9 +14,12 @@ Sources (web pages, cited by title and section):
     mask comes from Philox4x32-10 (Salmon et al., SC 2011), written out in
     ``oracle/philox.py`` from its published definition.
 
+  * Rotary positions, layer norm and dropout with a residual: written from
+    their formulas in ``oracle/rotary.py`` and ``oracle/norm.py``.
+
 Every function here is pinned by ``tests/test_oracle_pins.py`` (hand-derived
 N=2, d=2 example, finite differences against an independent scalar forward,
-invariants and special cases).
+invariants and special cases) and ``tests/test_oracle_block_pins.py``.
 """
 from .attention import (  # noqa: F401
     attention_forward,
@@ -24,4 +27,11 @@ from .attention import (  # noqa: F401
     head_forward,
     head_backward,
 )
+from .norm import (  # noqa: F401
+    dropout,
+    element_keep_mask,
+    layer_norm,
+    layer_norm_backward,
+)
 from .philox import dropout_keep_mask, keep_threshold, philox4x32_10  # noqa: F401
+from .rotary import angles, frequencies, rotate  # noqa: F401
