@@ -51,16 +51,61 @@ __device__ __forceinline__ bool kept(long long e, const Drop& d) {
   return w.w[e & 3] >= d.threshold;
 }
 
-template <typename T>
+// Keep words of the 4 NB elements from e (a multiple of 4) on.
+template <int NB>
+__device__ __forceinline__ void keep_words(long long e, const Drop& d, uint32_t (&w)[NB][4]) {
+#pragma unroll
+  for (int u = 0; u < NB; ++u) {
+    const long long c = (e >> 2) + u;
+    w[u][0] = static_cast<uint32_t>(c);
+    w[u][1] = static_cast<uint32_t>(c >> 32);
+    w[u][2] = 0u;
+    w[u][3] = 1u;
+  }
+  philox4x32_10_batch<NB, 10>(w, d.seed_lo, d.seed_hi);
+}
+
+// One thread per 16 bytes: a group of 16-byte loads is in flight on every
+// lane, and the mask words (two generator calls per 8 elements) are drawn
+// behind them.
+template <typename T, bool DROP>
 __global__ void __launch_bounds__(kThreads)
-    dropout_add_kernel(const T* __restrict__ x, const T* residual, T* y, long long n, Drop drop) {
-  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long e = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; e < n;
-       e += stride) {
-    float v = to_f32(x[e]);
-    if (drop.on) v = kept(e, drop) ? v * drop.inv_keep : 0.f;
-    if (residual != nullptr) v += to_f32(residual[e]);
-    y[e] = from_f32<T>(v);
+    dropout_add_kernel(const T* x, const T* residual, T* y, long long n, Drop drop) {
+  constexpr int E = Vec<T>::kElems;
+  const long long e = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) * E;
+  if (e >= n) return;
+  const bool whole = e + E <= n;
+  float v[E], r[E];
+  Vec<T> vx, vr;
+  if (whole) {
+    vx = load_vec(x + e);
+    if (residual != nullptr) vr = load_vec(residual + e);
+  }
+  uint32_t w[E / 4][4];
+  if (DROP) keep_words<E / 4>(e, drop, w);
+  if (whole) {
+    unpack(vx, v);
+    if (residual != nullptr) unpack(vr, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      v[i] = e + i < n ? to_f32(x[e + i]) : 0.f;
+      r[i] = residual != nullptr && e + i < n ? to_f32(residual[e + i]) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    if (DROP) v[i] = w[i / 4][i % 4] >= drop.threshold ? v[i] * drop.inv_keep : 0.f;
+    if (residual != nullptr) v[i] += r[i];
+  }
+  if (whole) {
+    Vec<T> o;
+    pack(v, o);
+    store_vec(y + e, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (e + i < n) y[e + i] = from_f32<T>(v[i]);
   }
 }
 
@@ -292,10 +337,15 @@ extern "C" int attn_dropout_add(const void* x, const void* residual, void* y, lo
   const norm::Drop drop = norm::make_drop(p_drop, seed);
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    norm::dropout_add_kernel<T>
-        <<<norm::grid_for((n + norm::kThreads - 1) / norm::kThreads), norm::kThreads, 0,
-           as_stream(stream)>>>(static_cast<const T*>(x), static_cast<const T*>(residual),
-                                static_cast<T*>(y), n, drop);
+    const T *xt = static_cast<const T*>(x), *rt = static_cast<const T*>(residual);
+    const long long per_block = norm::kThreads * static_cast<long long>(Vec<T>::kElems);
+    const unsigned grid = static_cast<unsigned>((n + per_block - 1) / per_block);
+    if (drop.on)
+      norm::dropout_add_kernel<T, true>
+          <<<grid, norm::kThreads, 0, as_stream(stream)>>>(xt, rt, static_cast<T*>(y), n, drop);
+    else
+      norm::dropout_add_kernel<T, false>
+          <<<grid, norm::kThreads, 0, as_stream(stream)>>>(xt, rt, static_cast<T*>(y), n, drop);
     return launch_status();
   });
 }

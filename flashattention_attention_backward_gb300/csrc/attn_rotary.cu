@@ -64,9 +64,10 @@ __device__ __forceinline__ void angle(long long p, unsigned long long f, float& 
   s = (quadrant & 2u) ? -b : b;
 }
 
-// One thread per column pair (or copied column) of a row.
+// Fallback for rows that 16-byte groups do not divide (odd d, strides or
+// rot): one thread per column pair (or copied column) of a row.
 template <typename TQ, typename TK, typename TO>
-__global__ void __launch_bounds__(256) rotary_kernel(Args p) {
+__global__ void __launch_bounds__(256) rotary_any_kernel(Args p) {
   const int items = p.half + (p.d - 2 * p.half);
   const int heads = p.side[0].heads + p.side[1].heads;
   const long long total = static_cast<long long>(p.B) * p.N * heads * items;
@@ -105,13 +106,190 @@ __global__ void __launch_bounds__(256) rotary_kernel(Args p) {
   }
 }
 
+constexpr int kThreads = 128;
+
+// E consecutive elements in fp32 from T (E = the output type's 16 bytes).
+template <typename T, int E>
+struct Group {
+  static constexpr int kVecs = E * static_cast<int>(sizeof(T)) / 16;
+  Vec<T> v[kVecs];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = load_vec(p + i * Vec<T>::kElems);
+  }
+  __device__ __forceinline__ void get(float (&f)[E]) const {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float part[Vec<T>::kElems];
+      unpack(v[i], part);
+#pragma unroll
+      for (int j = 0; j < Vec<T>::kElems; ++j) f[i * Vec<T>::kElems + j] = part[j];
+    }
+  }
+};
+
+// One thread keeps the cosines and sines of E column pairs of one token (two
+// 16-byte groups: the pairs' two halves, or two neighbouring groups where
+// interleaved) and takes them through `per` heads, U heads' loads in flight
+// at a time. The angles cost about as much as four heads' arithmetic, the
+// loads and stores are what bounds it.
+template <typename TI, typename TO, int U, bool INTERLEAVED>
+__device__ __forceinline__ void rotate_heads(const Args& p, const Side& s, int h0, int h1,
+                                             long long b, long long n, int item) {
+  constexpr int E = Vec<TO>::kElems;
+  const int turning = INTERLEAVED ? 0 : p.half / E;  // items that turn (half layout)
+  int ca, cb;
+  bool turn_a, turn_b;
+  if (!INTERLEAVED && item < turning) {
+    ca = item * E;
+    cb = ca + p.half;
+    turn_a = turn_b = true;
+  } else {
+    ca = (INTERLEAVED ? 0 : 2 * p.half) + (item - turning) * 2 * E;
+    cb = ca + E;
+    turn_a = ca < 2 * p.half;
+    turn_b = cb < 2 * p.half;
+  }
+  const bool has_b = cb < p.d;
+  const TI* in = static_cast<const TI*>(s.in) + b * s.in_stride[0] + h0 * s.in_stride[1] +
+                 n * s.in_stride[2];
+  TO* out = static_cast<TO*>(s.out) + b * s.out_stride[0] + h0 * s.out_stride[1] +
+            n * s.out_stride[2];
+  float cs[E], sn[E];
+  bool ready = false;
+  for (int h = h0; h < h1; h += U) {
+    Group<TI, E> ga[U], gb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (h + u < h1) {
+        ga[u].load(in + u * s.in_stride[1] + ca);
+        if (has_b) gb[u].load(in + u * s.in_stride[1] + cb);
+      }
+    }
+    if (!ready) {  // behind the first loads, so that their latency covers it
+      ready = true;
+      if (turn_a) {
+        const long long pos = p.positions != nullptr ? p.positions[b * p.pos_stride + n] : n;
+        const int first = INTERLEAVED ? ca / 2 : ca;
+        const int count = p.half - first < E ? p.half - first : E;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          cs[i] = sn[i] = 0.f;
+          if (i < count) angle(pos, p.turns[first + i], cs[i], sn[i]);
+          cs[i] *= p.magnitude * s.scale;
+          sn[i] *= p.magnitude * s.scale * p.sign;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (h + u >= h1) continue;
+      float a[E], v[E];
+      ga[u].get(a);
+      gb[u].get(v);
+      if (INTERLEAVED) {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          if (turn_a) {
+            const float x = a[i], y = a[i + 1];
+            a[i] = x * cs[i / 2] - y * sn[i / 2];
+            a[i + 1] = x * sn[i / 2] + y * cs[i / 2];
+          } else {
+            a[i] *= s.scale;
+            a[i + 1] *= s.scale;
+          }
+          if (turn_b) {
+            const float x = v[i], y = v[i + 1];
+            v[i] = x * cs[(E + i) / 2] - y * sn[(E + i) / 2];
+            v[i + 1] = x * sn[(E + i) / 2] + y * cs[(E + i) / 2];
+          } else {
+            v[i] *= s.scale;
+            v[i + 1] *= s.scale;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const float x = a[i], y = v[i];
+          a[i] = turn_a ? x * cs[i] - y * sn[i] : x * s.scale;
+          v[i] = turn_a ? x * sn[i] + y * cs[i] : y * s.scale;
+        }
+      }
+      Vec<TO> w;
+      pack(a, w);
+      store_vec(out + u * s.out_stride[1] + ca, w);
+      if (has_b) {
+        pack(v, w);
+        store_vec(out + u * s.out_stride[1] + cb, w);
+      }
+    }
+    in += U * s.in_stride[1];
+    out += U * s.out_stride[1];
+  }
+}
+
+template <typename TQ, typename TK, typename TO, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads)
+    rotary_kernel(Args p, int items, int per, int q_groups, long long tokens) {
+  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  const long long token = i / items;
+  if (token >= tokens) return;
+  const int item = static_cast<int>(i - token * items);
+  const long long b = token / p.N, n = token - b * p.N;
+  const int g = blockIdx.y;
+  // loads in flight per thread: 128 bytes
+  if (g < q_groups) {
+    const int h0 = g * per;
+    rotate_heads<TQ, TO, sizeof(TQ) == sizeof(TO) ? 4 : 2, INTERLEAVED>(
+        p, p.side[0], h0, min(h0 + per, p.side[0].heads), b, n, item);
+  } else {
+    const int h0 = (g - q_groups) * per;
+    rotate_heads<TK, TO, 4, INTERLEAVED>(p, p.side[1], h0, min(h0 + per, p.side[1].heads), b, n,
+                                         item);
+  }
+}
+
+// Whether rows and strides are whole 16-byte groups of the output's type (and
+// of the input's).
+template <typename TO>
+bool whole_groups(const Args& a) {
+  constexpr int E = Vec<TO>::kElems;
+  if (a.d % E != 0 || (a.interleaved ? 2 * a.half : a.half) % E != 0) return false;
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 3; ++j)
+      if (a.side[i].heads > 0 && (a.side[i].in_stride[j] % E != 0 || a.side[i].out_stride[j] % E != 0))
+        return false;
+  return true;
+}
+
 template <typename TQ, typename TK, typename TO>
 int launch(const Args& a, cudaStream_t stream) {
-  const long long total = static_cast<long long>(a.B) * a.N *
-                          (a.side[0].heads + a.side[1].heads) * (a.d - a.half);
-  const long long want = (total + 255) / 256;
-  const long long cap = static_cast<long long>(sm_count() > 0 ? sm_count() : 1) * 8;
-  rotary_kernel<TQ, TK, TO><<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream>>>(a);
+  const int sms = sm_count() > 0 ? sm_count() : 1;
+  const int heads = a.side[0].heads + a.side[1].heads;
+  if (!whole_groups<TO>(a)) {
+    const long long total = static_cast<long long>(a.B) * a.N * heads * (a.d - a.half);
+    const long long want = (total + 255) / 256, cap = sms * 8LL;
+    rotary_any_kernel<TQ, TK, TO>
+        <<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream>>>(a);
+    return launch_status();
+  }
+  constexpr int E = Vec<TO>::kElems;
+  const int items = a.interleaved ? (a.d + 2 * E - 1) / (2 * E)
+                                  : a.half / E + (a.d - 2 * a.half + 2 * E - 1) / (2 * E);
+  const long long tokens = static_cast<long long>(a.B) * a.N;
+  const long long blocks = (tokens * items + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffLL) return ATTN_ERR_TOO_LARGE;
+  // heads per thread: as many as leave every SM a few blocks
+  int per = 8;
+  while (per > 1 && blocks * ((a.side[0].heads + per - 1) / per + (a.side[1].heads + per - 1) / per) <
+                        sms * 8LL)
+    per /= 2;
+  const int qg = (a.side[0].heads + per - 1) / per, kg = (a.side[1].heads + per - 1) / per;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(qg + kg));
+  if (a.interleaved)
+    rotary_kernel<TQ, TK, TO, true><<<grid, kThreads, 0, stream>>>(a, items, per, qg, tokens);
+  else
+    rotary_kernel<TQ, TK, TO, false><<<grid, kThreads, 0, stream>>>(a, items, per, qg, tokens);
   return launch_status();
 }
 

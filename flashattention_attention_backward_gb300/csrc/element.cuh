@@ -46,6 +46,69 @@ __device__ __forceinline__ void store_as(void* p, long long i, int dtype, float 
     static_cast<__half*>(p)[i] = from_f32<__half>(v);
 }
 
+// 16 bytes of T in registers, and their elements in fp32.
+template <typename T>
+struct Vec {
+  static constexpr int kElems = 16 / sizeof(T);
+  uint4 w;
+};
+
+__device__ __forceinline__ void unpack(const Vec<float>& v, float (&f)[4]) {
+  f[0] = __uint_as_float(v.w.x);
+  f[1] = __uint_as_float(v.w.y);
+  f[2] = __uint_as_float(v.w.z);
+  f[3] = __uint_as_float(v.w.w);
+}
+__device__ __forceinline__ void unpack(const Vec<__nv_bfloat16>& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.w.x, v.w.y, v.w.z, v.w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const Vec<__half>& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.w.x, v.w.y, v.w.z, v.w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+__device__ __forceinline__ void pack(const float (&f)[4], Vec<float>& v) {
+  v.w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                   __float_as_uint(f[3]));
+}
+__device__ __forceinline__ void pack(const float (&f)[8], Vec<__nv_bfloat16>& v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  v.w = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void pack(const float (&f)[8], Vec<__half>& v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  v.w = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ Vec<T> load_vec(const T* p) {
+  Vec<T> v;
+  v.w = *reinterpret_cast<const uint4*>(p);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T>& v) {
+  *reinterpret_cast<uint4*>(p) = v.w;
+}
+
 inline bool known_dtype(int dtype) {
   return dtype == ATTN_BF16 || dtype == ATTN_FP16 || dtype == ATTN_FP32;
 }
