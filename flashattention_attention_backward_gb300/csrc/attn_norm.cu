@@ -18,22 +18,10 @@
 #include <cmath>
 #include <cstdint>
 
-#include "element.cuh"
-#include "philox.cuh"
+#include "norm_common.cuh"
 
 namespace attn {
 namespace norm {
-
-constexpr int kThreads = 256;
-// Row chunks of the weight gradients' first stage: the workspace holds two
-// fp32 sums a column for each.
-constexpr int kMaxChunks = 1024;
-
-struct Drop {
-  uint32_t seed_lo, seed_hi, threshold;
-  float inv_keep;
-  int on;
-};
 
 inline Drop make_drop(float p, unsigned long long seed) {
   Drop d;
@@ -43,26 +31,6 @@ inline Drop make_drop(float p, unsigned long long seed) {
   d.inv_keep = static_cast<float>(1.0 / (1.0 - static_cast<double>(p)));
   d.on = p > 0.0f;
   return d;
-}
-
-__device__ __forceinline__ bool kept(long long e, const Drop& d) {
-  const PhiloxOut w = philox4x32_10(static_cast<uint32_t>(e >> 2), static_cast<uint32_t>(e >> 34),
-                                    0u, 1u, d.seed_lo, d.seed_hi);
-  return w.w[e & 3] >= d.threshold;
-}
-
-// Keep words of the 4 NB elements from e (a multiple of 4) on.
-template <int NB>
-__device__ __forceinline__ void keep_words(long long e, const Drop& d, uint32_t (&w)[NB][4]) {
-#pragma unroll
-  for (int u = 0; u < NB; ++u) {
-    const long long c = (e >> 2) + u;
-    w[u][0] = static_cast<uint32_t>(c);
-    w[u][1] = static_cast<uint32_t>(c >> 32);
-    w[u][2] = 0u;
-    w[u][3] = 1u;
-  }
-  philox4x32_10_batch<NB, 10>(w, d.seed_lo, d.seed_hi);
 }
 
 // One thread per 16 bytes: a group of 16-byte loads is in flight on every
@@ -109,148 +77,24 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Sum over the block, the same value in every thread.
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float part[kThreads / 32];
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-  return s;
-}
-
-struct FwdArgs {
-  const void *x, *residual, *gamma, *beta;  // residual NULL: plain layer norm
-  void *z, *y;
-  float *mean, *rstd;
-  long long rows;
-  int C, wdtype;
-  float eps;
-  Drop drop;
-};
-
-// One block per row; the row is read three times.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(FwdArgs a) {
-  const T* x = static_cast<const T*>(a.x);
-  const T* res = static_cast<const T*>(a.residual);
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const long long base = row * a.C;
-    auto value = [&](int c) {
-      float v = to_f32(x[base + c]);
-      if (a.drop.on) v = kept(base + c, a.drop) ? v * a.drop.inv_keep : 0.f;
-      return res != nullptr ? v + to_f32(res[base + c]) : v;
-    };
-    float s = 0.f;
-    for (int c = threadIdx.x; c < a.C; c += kThreads) s += value(c);
-    const float mu = block_sum(s) / a.C;
-    float q = 0.f;
-    for (int c = threadIdx.x; c < a.C; c += kThreads) {
-      const float d = value(c) - mu;
-      q = fmaf(d, d, q);
-    }
-    const float r = 1.0f / sqrtf(block_sum(q) / a.C + a.eps);
-    for (int c = threadIdx.x; c < a.C; c += kThreads) {
-      const float v = value(c);
-      float o = (v - mu) * r;
-      if (a.gamma != nullptr) o *= load_as(a.gamma, c, a.wdtype);
-      if (a.beta != nullptr) o += load_as(a.beta, c, a.wdtype);
-      if (a.z != nullptr) static_cast<T*>(a.z)[base + c] = from_f32<T>(v);
-      static_cast<T*>(a.y)[base + c] = from_f32<T>(o);
-    }
-    if (threadIdx.x == 0) {
-      if (a.mean != nullptr) a.mean[row] = mu;
-      if (a.rstd != nullptr) a.rstd[row] = r;
-    }
-  }
-}
-
-struct BwdArgs {
-  const void *dy, *dz, *z, *gamma;  // dz NULL: nothing to add
-  const float *mean, *rstd;
-  void *dx, *dres;  // dx: behind the dropout, or NULL; dres: dz itself
-  void *dgamma, *dbeta;
-  float* workspace;
-  long long rows;
-  int C, wdtype;
-  Drop drop;
-};
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(BwdArgs a) {
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* dz = static_cast<const T*>(a.dz);
-  const T* z = static_cast<const T*>(a.z);
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const long long base = row * a.C;
-    const float mu = a.mean[row], r = a.rstd[row];
-    auto grad = [&](int c) {
-      const float g = to_f32(dy[base + c]);
-      return a.gamma != nullptr ? g * load_as(a.gamma, c, a.wdtype) : g;
-    };
-    float s = 0.f, t = 0.f;
-    for (int c = threadIdx.x; c < a.C; c += kThreads) {
-      const float g = grad(c), h = (to_f32(z[base + c]) - mu) * r;
-      s += g;
-      t = fmaf(g, h, t);
-    }
-    s = block_sum(s) / a.C;
-    t = block_sum(t) / a.C;
-    for (int c = threadIdx.x; c < a.C; c += kThreads) {
-      const float g = grad(c), h = (to_f32(z[base + c]) - mu) * r;
-      float v = r * (g - s - h * t);
-      if (dz != nullptr) v += to_f32(dz[base + c]);
-      if (a.dres != nullptr) static_cast<T*>(a.dres)[base + c] = from_f32<T>(v);
-      if (a.dx != nullptr) {
-        if (a.drop.on) v = kept(base + c, a.drop) ? v * a.drop.inv_keep : 0.f;
-        static_cast<T*>(a.dx)[base + c] = from_f32<T>(v);
-      }
-    }
-  }
-}
-
-// First stage of the weight gradients: 32 columns by a chunk of rows.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) weights_kernel(BwdArgs a, long long rows_per_chunk) {
-  __shared__ float part[2][8][32];
+// Second stage of the weight gradients: a block takes 32 columns, its 32
+// warps every 32nd partial sum of each, and adds the warps' sums in order.
+__global__ void __launch_bounds__(1024) weights_sum_kernel(BwdArgs a, int chunks) {
+  __shared__ float part[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + tx;
-  const long long first = blockIdx.y * rows_per_chunk;
-  const long long last = first + rows_per_chunk < a.rows ? first + rows_per_chunk : a.rows;
-  float s = 0.f, t = 0.f;
-  if (c < a.C) {
-    for (long long row = first + ty; row < last; row += 8) {
-      const float g = to_f32(static_cast<const T*>(a.dy)[row * a.C + c]);
-      const float h = (to_f32(static_cast<const T*>(a.z)[row * a.C + c]) - a.mean[row]) * a.rstd[row];
-      s += g;
-      t = fmaf(g, h, t);
-    }
-  }
-  part[0][ty][tx] = t;
-  part[1][ty][tx] = s;
-  __syncthreads();
-  if (ty < 2 && c < a.C) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v += part[ty][i][tx];
-    a.workspace[(static_cast<long long>(blockIdx.y) * 2 + ty) * a.C + c] = v;
-  }
-}
-
-// Second stage: the chunks of a column, in order.
-__global__ void __launch_bounds__(kThreads) weights_sum_kernel(BwdArgs a, int chunks) {
-  const int i = blockIdx.x * kThreads + threadIdx.x;
-  if (i >= 2 * a.C) return;
-  const int c = i < a.C ? i : i - a.C;
-  void* out = i < a.C ? a.dgamma : a.dbeta;
-  if (out == nullptr) return;
+  const int i = blockIdx.x * 32 + tx;
   float v = 0.f;
-  for (int k = 0; k < chunks; ++k) v += a.workspace[(2LL * k + (i < a.C ? 0 : 1)) * a.C + c];
-  store_as(out, c, a.wdtype, v);
+  if (i < 2 * a.C)
+    for (int k = ty; k < chunks; k += 32) v += a.workspace[2LL * k * a.C + i];
+  part[ty][tx] = v;
+  __syncthreads();
+  if (ty == 0 && i < 2 * a.C) {
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v += part[k][tx];
+    void* out = i < a.C ? a.dgamma : a.dbeta;
+    if (out != nullptr) store_as(out, i < a.C ? i : i - a.C, a.wdtype, v);
+  }
 }
 
 int check(long long rows, int C, int dtype, int wdtype) {
@@ -260,41 +104,29 @@ int check(long long rows, int C, int dtype, int wdtype) {
   return ATTN_OK;
 }
 
+// Partial sums a column that a backward over this many rows may leave.
+inline long long max_chunks(long long rows) {
+  const long long n = (rows + 7) / 8 * 8;  // blocks come in eights
+  return n < kMaxChunks ? (n > 0 ? n : 8) : kMaxChunks;
+}
+
 inline bool bad_p(float p) { return !(p >= 0.0f && p < 1.0f); }
 
-inline unsigned grid_for(long long want) {
-  const long long cap = static_cast<long long>(sm_count() > 0 ? sm_count() : 1) * 8;
-  return static_cast<unsigned>(want < cap ? want : cap);
-}
-
-int run_fwd(const FwdArgs& a, int dtype, cudaStream_t stream) {
+int forward(const FwdArgs& a, int dtype, cudaStream_t stream) {
   if (a.rows == 0) return ATTN_OK;
-  return with_dtype(dtype, [&](auto t) {
-    fwd_kernel<decltype(t)><<<grid_for(a.rows), kThreads, 0, stream>>>(a);
-    return launch_status();
-  });
+  return with_dtype(dtype, [&](auto t) { return run_fwd<decltype(t)>(a, stream); });
 }
 
-inline int chunks_for(long long rows) {
-  const long long n = (rows + 63) / 64;
-  return static_cast<int>(n < kMaxChunks ? (n > 0 ? n : 1) : kMaxChunks);
-}
-
-int run_bwd(const BwdArgs& a, int dtype, cudaStream_t stream) {
+int backward(const BwdArgs& a, int dtype, cudaStream_t stream) {
   const bool weights = a.dgamma != nullptr || a.dbeta != nullptr;
-  if (a.rows == 0 && !weights) return ATTN_OK;
-  const int chunks = chunks_for(a.rows);
-  return with_dtype(dtype, [&](auto t) {
-    using T = decltype(t);
-    if (weights) {
-      const long long per = (a.rows + chunks - 1) / chunks;
-      const dim3 grid(static_cast<unsigned>((a.C + 31) / 32), static_cast<unsigned>(chunks));
-      weights_kernel<T><<<grid, kThreads, 0, stream>>>(a, per);
-      weights_sum_kernel<<<(2 * a.C + kThreads - 1) / kThreads, kThreads, 0, stream>>>(a, chunks);
-    }
-    if (a.rows > 0) bwd_kernel<T><<<grid_for(a.rows), kThreads, 0, stream>>>(a);
-    return launch_status();
-  });
+  int chunks = 0;
+  if (a.rows > 0) {
+    chunks = with_dtype(dtype, [&](auto t) { return run_bwd<decltype(t)>(a, stream); });
+    if (chunks < 0) return chunks;
+  }
+  if (!weights) return ATTN_OK;
+  weights_sum_kernel<<<(2 * a.C + 31) / 32, 1024, 0, stream>>>(a, chunks);
+  return launch_status();
 }
 
 }  // namespace norm
@@ -323,7 +155,7 @@ extern "C" int attn_layer_norm(const void* x, const void* gamma, const void* bet
   a.C = C;
   a.wdtype = wdtype;
   a.eps = eps;
-  return norm::run_fwd(a, dtype, as_stream(stream));
+  return norm::forward(a, dtype, as_stream(stream));
 }
 
 extern "C" int attn_dropout_add(const void* x, const void* residual, void* y, long long n,
@@ -377,13 +209,13 @@ extern "C" int attn_dropout_add_norm(const void* x, const void* residual, const 
   a.wdtype = wdtype;
   a.eps = eps;
   a.drop = norm::make_drop(p_drop, seed);
-  return norm::run_fwd(a, dtype, as_stream(stream));
+  return norm::forward(a, dtype, as_stream(stream));
 }
 
 extern "C" long long attn_layer_norm_bwd_workspace_bytes(long long rows, int C) {
   const int rc = norm::check(rows, C, ATTN_BF16, ATTN_BF16);
   if (rc != ATTN_OK) return rc;
-  return static_cast<long long>(norm::chunks_for(rows)) * 2 * C *
+  return norm::max_chunks(rows) * 2 * C *
          static_cast<long long>(sizeof(float));
 }
 
@@ -412,7 +244,7 @@ extern "C" int attn_layer_norm_bwd(const void* dy, const void* x, const void* ga
   a.rows = rows;
   a.C = C;
   a.wdtype = wdtype;
-  return norm::run_bwd(a, dtype, as_stream(stream));
+  return norm::backward(a, dtype, as_stream(stream));
 }
 
 extern "C" int attn_dropout_add_norm_bwd(const void* dy, const void* dz, const void* z,
@@ -448,5 +280,5 @@ extern "C" int attn_dropout_add_norm_bwd(const void* dy, const void* dz, const v
   a.C = C;
   a.wdtype = wdtype;
   a.drop = norm::make_drop(p_drop, seed);
-  return norm::run_bwd(a, dtype, as_stream(stream));
+  return norm::backward(a, dtype, as_stream(stream));
 }
