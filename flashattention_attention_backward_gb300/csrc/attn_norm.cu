@@ -33,47 +33,67 @@ inline Drop make_drop(float p, unsigned long long seed) {
   return d;
 }
 
-// One thread per 16 bytes: a group of 16-byte loads is in flight on every
-// lane, and the mask words (two generator calls per 8 elements) are drawn
+// A thread takes two 16-byte groups a block apart: their loads are in flight
+// together, and the mask words (a generator call per 4 elements) are drawn
 // behind them.
 template <typename T, bool DROP>
 __global__ void __launch_bounds__(kThreads)
     dropout_add_kernel(const T* x, const T* residual, T* y, long long n, Drop drop) {
-  constexpr int E = Vec<T>::kElems;
-  const long long e = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) * E;
-  if (e >= n) return;
-  const bool whole = e + E <= n;
-  float v[E], r[E];
-  Vec<T> vx, vr;
-  if (whole) {
-    vx = load_vec(x + e);
-    if (residual != nullptr) vr = load_vec(residual + e);
-  }
-  uint32_t w[E / 4][4];
-  if (DROP) keep_words<E / 4>(e, drop, w);
-  if (whole) {
-    unpack(vx, v);
-    if (residual != nullptr) unpack(vr, r);
-  } else {
+  constexpr int E = Vec<T>::kElems, U = 2;
+  const long long e0 =
+      (static_cast<long long>(blockIdx.x) * (U * kThreads) + threadIdx.x) * E;
+  Vec<T> vx[U], vr[U];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      v[i] = e + i < n ? to_f32(x[e + i]) : 0.f;
-      r[i] = residual != nullptr && e + i < n ? to_f32(residual[e + i]) : 0.f;
+  for (int u = 0; u < U; ++u) {
+    const long long e = e0 + u * kThreads * E;
+    if (e + E <= n) {
+      vx[u] = load_vec(x + e);
+      if (residual != nullptr) vr[u] = load_vec(residual + e);
     }
   }
+  uint32_t w[U * E / 4][4];
+  if (DROP) {
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    if (DROP) v[i] = w[i / 4][i % 4] >= drop.threshold ? v[i] * drop.inv_keep : 0.f;
-    if (residual != nullptr) v[i] += r[i];
+    for (int u = 0; u < U * E / 4; ++u) {
+      const long long c = ((e0 + (u / (E / 4)) * (kThreads * E)) >> 2) + u % (E / 4);
+      w[u][0] = static_cast<uint32_t>(c);
+      w[u][1] = static_cast<uint32_t>(c >> 32);
+      w[u][2] = 0u;
+      w[u][3] = 1u;
+    }
+    philox4x32_10_batch<U * E / 4, 10>(w, drop.seed_lo, drop.seed_hi);
   }
-  if (whole) {
-    Vec<T> o;
-    pack(v, o);
-    store_vec(y + e, o);
-  } else {
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (e + i < n) y[e + i] = from_f32<T>(v[i]);
+  for (int u = 0; u < U; ++u) {
+    const long long e = e0 + u * kThreads * E;
+    if (e >= n) continue;
+    const bool whole = e + E <= n;
+    float v[E], r[E];
+    if (whole) {
+      unpack(vx[u], v);
+      if (residual != nullptr) unpack(vr[u], r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        v[i] = e + i < n ? to_f32(x[e + i]) : 0.f;
+        r[i] = residual != nullptr && e + i < n ? to_f32(residual[e + i]) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if (DROP)
+        v[i] = w[u * E / 4 + i / 4][i % 4] >= drop.threshold ? v[i] * drop.inv_keep : 0.f;
+      if (residual != nullptr) v[i] += r[i];
+    }
+    if (whole) {
+      Vec<T> o;
+      pack(v, o);
+      store_vec(y + e, o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (e + i < n) y[e + i] = from_f32<T>(v[i]);
+    }
   }
 }
 
@@ -170,7 +190,7 @@ extern "C" int attn_dropout_add(const void* x, const void* residual, void* y, lo
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const T *xt = static_cast<const T*>(x), *rt = static_cast<const T*>(residual);
-    const long long per_block = norm::kThreads * static_cast<long long>(Vec<T>::kElems);
+    const long long per_block = 2LL * norm::kThreads * Vec<T>::kElems;
     const unsigned grid = static_cast<unsigned>((n + per_block - 1) / per_block);
     if (drop.on)
       norm::dropout_add_kernel<T, true>
