@@ -102,20 +102,6 @@ __device__ __forceinline__ void drop_vec(float (&f)[E], long long e, const Drop&
   for (int i = 0; i < E; ++i) f[i] = w[i / 4][i % 4] >= d.threshold ? f[i] * d.inv_keep : 0.f;
 }
 
-// The vector of columns c .. c + E - 1 at p (16-byte aligned). RAGGED: it may
-// reach over the row's ends, and past `end`, the tensor's; then only its
-// elements inside the tensor are read.
-template <typename T, bool RAGGED>
-__device__ __forceinline__ Vec<T> load_row_vec(const T* p, const T* end) {
-  constexpr int E = Vec<T>::kElems;
-  if (!RAGGED || p + E <= end) return load_vec(p);
-  Vec<T> v;
-  T* e = reinterpret_cast<T*>(&v);
-#pragma unroll
-  for (int i = 0; i < E; ++i) e[i] = p + i < end ? p[i] : from_f32<T>(0.f);
-  return v;
-}
-
 // Writes the vector's elements that lie in the row.
 template <typename T, bool RAGGED, int E>
 __device__ __forceinline__ void store_row_vec(T* p, const float (&f)[E], int c, int C) {
@@ -130,11 +116,8 @@ __device__ __forceinline__ void store_row_vec(T* p, const float (&f)[E], int c, 
   }
 }
 
-__device__ __forceinline__ void copy_async16(void* smem, const void* global) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(smem))),
-               "l"(global)
-               : "memory");
+__device__ __forceinline__ void copy_async16(uint32_t smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(global) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -146,82 +129,111 @@ __device__ __forceinline__ void copy_wait() {
 // rows a grid apart, so that a thread's columns are the same in all of its
 // rows (RAGGED: the grid is a multiple of 8 blocks, so all of a thread's rows
 // start at the same offset within a vector), and its weights, or its sums of
-// the weights' gradients, stay in registers. Rows come through a ring of
-// STAGES in shared memory, filled by asynchronous copies: a thread reads back
-// only what it copied itself, so the ring needs no barrier, and the next
-// rows' loads run while this one is reduced.
-template <typename T, typename S, int STAGES, int TENSORS, bool RAGGED>
+// the weights' gradients, stay in registers. Rows of NT tensors come through
+// a ring of STAGES in shared memory, filled by asynchronous copies: a thread
+// reads back only what it copied itself, so the ring needs no barrier, and
+// the next rows' loads run while this one is reduced. A row's slots stay for
+// LAG turns more. Vectors outside the row read as zeros.
+template <typename T, typename S, int STAGES, int LAG, int NT, bool RAGGED>
 struct Walk {
+  static constexpr int kAhead = STAGES - 1 - LAG;  // rows being copied
   static constexpr int E = Vec<T>::kElems;
-  uint4* ring;               // [STAGES][tensors][VECS][BLOCK], this thread's slots
-  const T* src[TENSORS];     // absent tensors come last and are not counted
-  int tensors, C;
-  long long rows, total, step, row, e;  // e: element of the row's first vector
-  int t, shift;
-  int stage;
+  static constexpr int kStageBytes = NT * S::VECS * S::BLOCK * 16;
+  uint4* ring;          // this thread's slots: [STAGES][NT][VECS], BLOCK apart
+  const T* from[NT];    // vector 0 of the next row to copy
+  const T* end[NT];     // behind the tensors (RAGGED)
+  long long stride;     // elements between this thread's rows
+  long long e;          // element of the current row's vector 0
+  long long row, step, left, to_copy;  // left: this thread's rows still to come
+  int t, shift, C;
+  int fill, take;       // stages
 
-  __device__ __forceinline__ Walk(uint4* smem, const T* const (&from)[TENSORS], int n,
-                                  long long rows_, int C_)
-      : ring(smem + threadIdx.x), tensors(n), C(C_), rows(rows_), total(rows_ * C_), stage(0) {
-#pragma unroll
-    for (int q = 0; q < TENSORS; ++q) src[q] = from[q];
+  __device__ __forceinline__ Walk(uint4* smem, const void* const (&src)[NT], long long rows, int C_)
+      : ring(smem + threadIdx.x), C(C_), fill(0), take(0) {
     t = threadIdx.x % S::TPR;
     row = static_cast<long long>(blockIdx.x) * S::ROWS + threadIdx.x / S::TPR;
     step = static_cast<long long>(gridDim.x) * S::ROWS;
     shift = RAGGED ? static_cast<int>((row * C) % E) : 0;
-    e = row * C - shift;
+    e = row * C - shift + t * E;
+    stride = step * C;
+    left = row < rows ? (rows - row + step - 1) / step : 0;
+    to_copy = left;
 #pragma unroll
-    for (int k = 0; k < STAGES - 1; ++k) fetch(k, k);
+    for (int q = 0; q < NT; ++q) {
+      from[q] = static_cast<const T*>(src[q]) + e;
+      end[q] = static_cast<const T*>(src[q]) + rows * C;
+    }
+#pragma unroll
+    for (int j = 0; j < S::VECS; ++j)
+      if (!inside(j))
+        for (int k = 0; k < STAGES * NT; ++k)
+          ring[(k * S::VECS + j) * S::BLOCK] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) copy_next();
   }
-  // the first column of this thread's vector j; below 0 and up to the row's
-  // end it reaches over the row's ends (RAGGED)
+  // the first column of this thread's vector j; below 0, or less than a
+  // vector from the row's end, it reaches over the row's ends (RAGGED)
   __device__ __forceinline__ int column(int j) const { return (t + j * S::TPR) * E - shift; }
-  __device__ __forceinline__ bool active() const { return row < rows; }
-  __device__ __forceinline__ long long element(int j) const { return e + (t + j * S::TPR) * E; }
-  __device__ __forceinline__ uint4* slot(int at, int q, int j) const {
-    return ring + ((at * tensors + q) * S::VECS + j) * S::BLOCK;
-  }
-  // starts the copies of the row `ahead` steps on
-  __device__ __forceinline__ void fetch(int ahead, int at) {
-    if (row + ahead * step < rows) {
-      const long long first = e + ahead * step * C;
+  __device__ __forceinline__ bool inside(int j) const { return column(j) < C; }
+  // element of vector j, less that of vector 0
+  __device__ __forceinline__ static constexpr int offset(int j) { return j * S::TPR * E; }
+  __device__ __forceinline__ bool active() const { return left > 0; }
+
+  __device__ __forceinline__ void copy_next() {
+    uint4* to = ring + fill * (kStageBytes / 16);
+    if (to_copy > 0) {
 #pragma unroll
       for (int j = 0; j < S::VECS; ++j) {
-        if (column(j) < C) {
-          const long long i = first + (t + j * S::TPR) * E;
+        if (inside(j)) {
 #pragma unroll
-          for (int q = 0; q < TENSORS; ++q) {
-            if (q < tensors) {
-              if (!RAGGED || i + E <= total)
-                copy_async16(slot(at, q, j), src[q] + i);
-              else
-                *reinterpret_cast<Vec<T>*>(slot(at, q, j)) =
-                    load_row_vec<T, RAGGED>(src[q] + i, src[q] + total);
+          for (int q = 0; q < NT; ++q) {
+            uint4* slot = to + (q * S::VECS + j) * S::BLOCK;
+            const T* p = from[q] + offset(j);
+            if (!RAGGED || p + E <= end[q]) {
+              copy_async16(ptx::smem_u32(slot), p);
+            } else {  // the tensor's last vector is no whole one
+              T* v = reinterpret_cast<T*>(slot);
+              for (int i = 0; i < E; ++i) v[i] = p + i < end[q] ? p[i] : from_f32<T>(0.f);
             }
           }
         }
       }
+    } else if (S::ROWS > 1) {  // other rows of the block go on: no stale values
+#pragma unroll
+      for (int k = 0; k < NT * S::VECS; ++k) to[k * S::BLOCK] = make_uint4(0u, 0u, 0u, 0u);
     }
     copy_commit();
+    --to_copy;
+#pragma unroll
+    for (int q = 0; q < NT; ++q) from[q] += stride;
+    fill = fill == STAGES - 1 ? 0 : fill + 1;
   }
   // starts the next copies and waits for the current row's
   __device__ __forceinline__ void arrive() {
-    fetch(STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-    copy_wait<STAGES - 1>();
+    copy_next();
+    copy_wait<kAhead>();
   }
-  __device__ __forceinline__ void get(int q, int j, float (&f)[E]) const {
-    unpack(*reinterpret_cast<const Vec<T>*>(slot(stage, q, j)), f);
+  __device__ __forceinline__ void get(int stage, int q, int j, float (&f)[E]) const {
+    Vec<T> v;
+    v.w = ring[stage * (kStageBytes / 16) + (q * S::VECS + j) * S::BLOCK];
+    unpack(v, f);
   }
   __device__ __forceinline__ void next() {
     row += step;
-    e += step * C;
-    stage = stage == STAGES - 1 ? 0 : stage + 1;
-  }
-  // the block's first row is still one: the same for all of its threads
-  __device__ __forceinline__ bool more() const {
-    return row - threadIdx.x / S::TPR < rows;
+    e += stride;
+    --left;
+    take = take == STAGES - 1 ? 0 : take + 1;
   }
 };
+
+// Rows of the block's first group of threads: as many turns as the block
+// takes, the same for all of its threads.
+template <typename S>
+__device__ __forceinline__ long long block_turns(long long rows) {
+  const long long first = static_cast<long long>(blockIdx.x) * S::ROWS;
+  const long long step = static_cast<long long>(gridDim.x) * S::ROWS;
+  return first < rows ? (rows - first + step - 1) / step : 0;
+}
 
 // Sum over groups of W lanes, the same value in each.
 template <int W>
@@ -231,12 +243,15 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// Weights of all of a thread's columns in fp32 pairs (a null array: `fill`).
+// Weights of columns c .. c + E - 1 in fp32 pairs (a null array: `fill`).
 template <int E, bool RAGGED>
 __device__ __forceinline__ void weight_pairs(const void* p, int c, int C, int wdtype, float fill,
                                              uint64_t (&g)[E / 2]) {
   float f[E];
-  if (RAGGED) {
+  if (c >= C) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[i] = 0.f;
+  } else if (RAGGED) {
     load_weights_ragged<E>(p, c, C, wdtype, fill, f);
   } else {
     Weights<E> w;
@@ -247,177 +262,255 @@ __device__ __forceinline__ void weight_pairs(const void* p, int c, int C, int wd
   for (int i = 0; i < E / 2; ++i) g[i] = ptx::f2_make(f[2 * i], f[2 * i + 1]);
 }
 
-// Forward: the row (its sum with the residual, behind the dropout) is held in
-// fp32 registers, in pairs (one instruction for two columns). A warp takes
-// the mean of its part and the squares about that; parts of n_w elements are
-// joined by
+// What a row leaves for the second half of its turn.
+struct Mark {
+  long long e, row;
+  int stage;
+  bool active;
+};
+
+// Forward, a row in two halves.
+// First half: its sum with the residual, behind the dropout, goes to fp32
+// registers, in pairs (one instruction for two columns); a warp takes the mean
+// of its part and the squares about that. Second half: parts of n_w elements
+// are joined by
 //   mu = sum n_w mu_w / C,  sum of squares = sum (q_w + n_w (mu_w - mu)^2),
-// which loses nothing to cancellation and costs one barrier a row.
-template <typename T, typename S, int STAGES, bool DROP, bool RAGGED>
-__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 768 / S::BLOCK : 1)
+// which loses nothing to cancellation and costs one barrier a row, and the
+// output is written. LAG = 1: a row's second half runs in one turn with the
+// next row's first, so that the reductions of one are covered by the
+// arithmetic of the other. ADD: with a residual, and z written.
+template <typename T, typename S, int STAGES, int LAG, bool ADD, bool DROP, bool RAGGED>
+__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 512 / S::BLOCK : 1)
     fwd_kernel(FwdArgs a) {
-  constexpr int E = Vec<T>::kElems, TPR = S::TPR, VECS = S::VECS, P = E / 2;
+  constexpr int E = Vec<T>::kElems, TPR = S::TPR, VECS = S::VECS, P = E / 2, NT = ADD ? 2 : 1;
   constexpr bool kKeep = VECS * E <= 16;  // weights stay in registers
   constexpr int kLanes = TPR < 32 ? TPR : 32, kWarps = TPR / kLanes;
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float2 part[2][kWarps];
   __shared__ float counts[kWarps];
-  const T* const src[2] = {static_cast<const T*>(a.x), static_cast<const T*>(a.residual)};
-  const bool add = a.residual != nullptr;
-  Walk<T, S, STAGES, 2, RAGGED> w(ring, src, add ? 2 : 1, a.rows, a.C);
+  const void* src[NT];
+  src[0] = a.x;
+  if (ADD) src[NT - 1] = a.residual;
+  Walk<T, S, STAGES, 0, NT, RAGGED> w(ring, src, a.rows, a.C);
   const float inv_C = 1.0f / static_cast<float>(a.C);
   uint64_t gamma[kKeep ? VECS : 1][P], beta[kKeep ? VECS : 1][P];
   int mine = 0;  // this thread's columns inside the row
 #pragma unroll
   for (int j = 0; j < VECS; ++j) {
     const int c = w.column(j);
-    if (c < a.C) {
-      if (kKeep) {
-        weight_pairs<E, RAGGED>(a.gamma, c, a.C, a.wdtype, 1.f, gamma[j]);
-        weight_pairs<E, RAGGED>(a.beta, c, a.C, a.wdtype, 0.f, beta[j]);
-      }
-      mine += RAGGED ? min(c + E, a.C) - max(c, 0) : E;
+    if (kKeep) {
+      weight_pairs<E, RAGGED>(a.gamma, c, a.C, a.wdtype, 1.f, gamma[j]);
+      weight_pairs<E, RAGGED>(a.beta, c, a.C, a.wdtype, 0.f, beta[j]);
     }
+    if (w.inside(j)) mine += RAGGED ? min(c + E, a.C) - max(c, 0) : E;
   }
   const float count = lane_sum<kLanes>(static_cast<float>(mine));  // n_w
   const float inv_count = count > 0.f ? 1.0f / count : 0.f;
-  if (kWarps > 1 && (threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = count;
+  float other = count;  // n_w of the warp whose part this lane joins
+  if (kWarps > 1) {
+    if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = count;
+    __syncthreads();
+    other = counts[threadIdx.x % kWarps];
+  }
   int parity = 0;
-  for (; w.more(); w.next()) {
+
+  // first half of the current row: v, and the mean and squares of the warp's part
+  auto first_half = [&](uint64_t (&v)[VECS][P], float& mu, float& q) {
     w.arrive();
-    const bool active = w.active();
-    uint64_t v[VECS][P], s2 = 0, q2 = 0;
+    const bool active = S::ROWS == 1 || w.active();
+    uint64_t s2 = 0, q2 = 0;
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
-      const int c = w.column(j);
-      if (active && c < a.C) {
-        float f[E];
-        w.get(0, j, f);
-        if (DROP) drop_vec<E>(f, w.element(j), a.drop);
-        if (add) {
-          float r[E];
-          w.get(1, j, r);
+      float f[E];
+      w.get(w.take, 0, j, f);
+      if (DROP) drop_vec<E>(f, w.e + w.offset(j), a.drop);
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const uint64_t o = ptx::f2_add(ptx::f2_make(f[2 * i], f[2 * i + 1]),
-                                           ptx::f2_make(r[2 * i], r[2 * i + 1]));
-            f[2 * i] = ptx::f2_lo(o);
-            f[2 * i + 1] = ptx::f2_hi(o);
-          }
-        }
-        if (a.z != nullptr)
-          store_row_vec<T, RAGGED>(static_cast<T*>(a.z) + w.element(j), f, c, a.C);
-        if (RAGGED) keep_inside<E>(f, c, a.C, 0.f);
+      for (int i = 0; i < P; ++i) v[j][i] = ptx::f2_make(f[2 * i], f[2 * i + 1]);
+      if (ADD) {
+        float r[E];
+        w.get(w.take, NT - 1, j, r);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          v[j][i] = ptx::f2_make(f[2 * i], f[2 * i + 1]);
-          s2 = ptx::f2_add(s2, v[j][i]);
+          v[j][i] = ptx::f2_add(v[j][i], ptx::f2_make(r[2 * i], r[2 * i + 1]));
+          f[2 * i] = ptx::f2_lo(v[j][i]);
+          f[2 * i + 1] = ptx::f2_hi(v[j][i]);
         }
+        if (active && w.inside(j))
+          store_row_vec<T, RAGGED>(static_cast<T*>(a.z) + w.e + w.offset(j), f, w.column(j), a.C);
       }
+      if (RAGGED) {
+        keep_inside<E>(f, w.column(j), a.C, 0.f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[j][i] = ptx::f2_make(f[2 * i], f[2 * i + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) s2 = ptx::f2_add(s2, v[j][i]);
     }
-    float mu = lane_sum<kLanes>(ptx::f2_lo(s2) + ptx::f2_hi(s2)) *
-               (kWarps > 1 ? inv_count : inv_C);
-    const uint64_t minus = ptx::f2_make(-mu, -mu);
+    mu = lane_sum<kLanes>(ptx::f2_lo(s2) + ptx::f2_hi(s2)) * inv_count;
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
       const int c = w.column(j);
-      if (active && c < a.C) {
-        if (RAGGED && (c < 0 || c + E > a.C)) {
+      if (RAGGED && (c < 0 || c + E > a.C)) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const float d = (i % 2 == 0 ? ptx::f2_lo(v[j][i / 2]) : ptx::f2_hi(v[j][i / 2])) - mu;
-            if (static_cast<unsigned>(c + i) < static_cast<unsigned>(a.C))
-              q2 = ptx::f2_fma(ptx::f2_make(d, 0.f), ptx::f2_make(d, 0.f), q2);
-          }
-        } else {
+        for (int i = 0; i < E; ++i) {
+          const float d = (i % 2 == 0 ? ptx::f2_lo(v[j][i / 2]) : ptx::f2_hi(v[j][i / 2])) - mu;
+          if (static_cast<unsigned>(c + i) < static_cast<unsigned>(a.C))
+            q2 = ptx::f2_fma(ptx::f2_make(d, 0.f), ptx::f2_make(d, 0.f), q2);
+        }
+      } else {
+        const float m = w.inside(j) ? -mu : 0.f;  // outside the row v is 0
+        const uint64_t minus = ptx::f2_make(m, m);
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const uint64_t d = ptx::f2_add(v[j][i], minus);
-            q2 = ptx::f2_fma(d, d, q2);
-          }
+        for (int i = 0; i < P; ++i) {
+          const uint64_t d = ptx::f2_add(v[j][i], minus);
+          q2 = ptx::f2_fma(d, d, q2);
         }
       }
     }
-    float q = lane_sum<kLanes>(ptx::f2_lo(q2) + ptx::f2_hi(q2));
+    q = lane_sum<kLanes>(ptx::f2_lo(q2) + ptx::f2_hi(q2));
+  };
+  auto mark = [&]() { return Mark{w.e, w.row, w.take, S::ROWS == 1 || w.active()}; };
+  // second half of row m, from the parts' means and squares
+  auto second_half = [&](const Mark& m, const uint64_t (&v)[VECS][P], float mu, float q) {
     if (kWarps > 1) {
-      if ((threadIdx.x & 31) == 0) part[parity][threadIdx.x >> 5] = make_float2(mu, q);
-      __syncthreads();
-      const int k = threadIdx.x % kWarps;
-      const float2 p = part[parity][k];
-      const float n = counts[k];
-      mu = lane_sum<kWarps>(n * p.x) * inv_C;
-      const float d = p.x - mu;
-      q = lane_sum<kWarps>(n > 0.f ? fmaf(n * d, d, p.y) : 0.f);
-      parity ^= 1;
+      const float mean = lane_sum<kWarps>(other * mu) * inv_C, d = mu - mean;
+      mu = mean;
+      q = lane_sum<kWarps>(other > 0.f ? fmaf(other * d, d, q) : 0.f);
     }
     const float r = rsqrtf(fmaf(q, inv_C, a.eps));
     const uint64_t minus_mu = ptx::f2_make(-mu, -mu), r2 = ptx::f2_make(r, r);
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
-      const int c = w.column(j);
-      if (active && c < a.C) {
-        const int k = kKeep ? j : 0;
-        if (!kKeep) {
-          weight_pairs<E, RAGGED>(a.gamma, c, a.C, a.wdtype, 1.f, gamma[0]);
-          weight_pairs<E, RAGGED>(a.beta, c, a.C, a.wdtype, 0.f, beta[0]);
-        }
-        float f[E];
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const uint64_t h = ptx::f2_mul(ptx::f2_add(v[j][i], minus_mu), r2);
-          const uint64_t o = ptx::f2_fma(h, gamma[k][i], beta[k][i]);
-          f[2 * i] = ptx::f2_lo(o);
-          f[2 * i + 1] = ptx::f2_hi(o);
-        }
-        store_row_vec<T, RAGGED>(static_cast<T*>(a.y) + w.element(j), f, c, a.C);
+      const int c = w.column(j), k = kKeep ? j : 0;
+      if (!kKeep) {
+        weight_pairs<E, RAGGED>(a.gamma, c, a.C, a.wdtype, 1.f, gamma[0]);
+        weight_pairs<E, RAGGED>(a.beta, c, a.C, a.wdtype, 0.f, beta[0]);
       }
+      float f[E];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const uint64_t h = ptx::f2_mul(ptx::f2_add(v[j][i], minus_mu), r2);
+        const uint64_t o = ptx::f2_fma(h, gamma[k][i], beta[k][i]);
+        f[2 * i] = ptx::f2_lo(o);
+        f[2 * i + 1] = ptx::f2_hi(o);
+      }
+      if (m.active && w.inside(j))
+        store_row_vec<T, RAGGED>(static_cast<T*>(a.y) + m.e + w.offset(j), f, c, a.C);
     }
-    if (active && w.t == 0) {
-      if (a.mean != nullptr) a.mean[w.row] = mu;
-      if (a.rstd != nullptr) a.rstd[w.row] = r;
+    if (m.active && w.t == 0) {
+      if (a.mean != nullptr) a.mean[m.row] = mu;
+      if (a.rstd != nullptr) a.rstd[m.row] = r;
     }
+  };
+  // hands the warp's part to the block, and takes the parts back
+  auto give = [&](float mu, float q) {
+    if (kWarps > 1) {
+      if ((threadIdx.x & 31) == 0) part[parity][threadIdx.x >> 5] = make_float2(mu, q);
+      __syncthreads();
+    }
+  };
+  auto take = [&](float& mu, float& q) {
+    if (kWarps > 1) {
+      const float2 p = part[parity][threadIdx.x % kWarps];
+      mu = p.x;
+      q = p.y;
+      parity ^= 1;
+    }
+  };
+
+  long long turns = block_turns<S>(a.rows);
+  if (turns == 0) return;
+  uint64_t v[VECS][P];
+  float mu, q;
+  if (LAG == 0) {
+    for (; turns > 0; --turns, w.next()) {
+      first_half(v, mu, q);
+      give(mu, q);
+      take(mu, q);
+      second_half(mark(), v, mu, q);
+    }
+  } else {
+    first_half(v, mu, q);
+    Mark m = mark();
+    give(mu, q);
+    for (w.next(); turns > 1; --turns, w.next()) {
+      uint64_t v_next[VECS][P];
+      float mu_next, q_next;
+      take(mu, q);
+      first_half(v_next, mu_next, q_next);
+      second_half(m, v, mu, q);
+      m = mark();
+#pragma unroll
+      for (int j = 0; j < VECS; ++j)
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[j][i] = v_next[j][i];
+      mu = mu_next;
+      q = q_next;
+      give(mu, q);
+    }
+    take(mu, q);
+    second_half(m, v, mu, q);
   }
   copy_wait<0>();
 }
 
-// Backward: a thread's column sums of the weights' gradients stay in
-// registers over all of its rows; the two sums of a row are joined over its
-// threads with one barrier.
-template <typename T, typename S, int STAGES, bool DROP, bool RAGGED>
+// Sums of two values over groups of W lanes, the same values in each.
+template <int W>
+__device__ __forceinline__ void lane_sums(float& s, float& u) {
+  s = lane_sum<W>(s);
+  u = lane_sum<W>(u);
+}
+// Over a whole warp: the first exchange leaves half of the lanes with one
+// value and half with the other, so that one value a lane is left to sum.
+// Lane 0 has the first value's sum, lane 16 the second's.
+__device__ __forceinline__ float warp_sums(float s, float u) {
+  const bool low = (threadIdx.x & 16) == 0;
+  float v = (low ? s : u) + __shfl_xor_sync(0xffffffffu, low ? u : s, 16);
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// Backward, a row in two halves like the forward: first the row's two sums
+// and its part of the weights' gradients, whose column sums stay in registers
+// over all of the thread's rows; then, with the sums joined over the row's
+// threads, its gradient, from the ring again. DZ: with a dz to add.
+template <typename T, typename S, int STAGES, int LAG, bool DZ, bool DROP, bool RAGGED>
 __global__ void __launch_bounds__(S::BLOCK, 512 / S::BLOCK) bwd_kernel(BwdArgs a) {
   constexpr int E = Vec<T>::kElems, TPR = S::TPR, VECS = S::VECS, BLOCK = S::BLOCK, P = E / 2;
-  // up to 16 elements a thread, weights and row stay in registers over the
-  // reduction; above, they are read again from L1 and the ring
-  constexpr bool kKeep = VECS * E <= 16;
+  constexpr int NT = DZ ? 3 : 2;
+  constexpr bool kKeep = VECS * E <= 16;  // weights stay in registers
   constexpr int kLanes = TPR < 32 ? TPR : 32, kWarps = TPR / kLanes;
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float2 part[2][kWarps];
-  const T* const src[3] = {static_cast<const T*>(a.dy), static_cast<const T*>(a.z),
-                           static_cast<const T*>(a.dz)};
-  Walk<T, S, STAGES, 3, RAGGED> w(ring, src, a.dz != nullptr ? 3 : 2, a.rows, a.C);
+  __shared__ __align__(16) float2 part[2][kWarps];
+  const void* src[NT];
+  src[0] = a.dy;
+  src[1] = a.z;
+  if (DZ) src[NT - 1] = a.dz;
+  Walk<T, S, STAGES, LAG, NT, RAGGED> w(ring, src, a.rows, a.C);
   const float inv_C = 1.0f / static_cast<float>(a.C);
   // the statistics of the row to come, one row ahead
-  float mu = 0.f, r = 0.f;
-  if (w.active()) {
-    mu = a.mean[w.row];
-    r = a.rstd[w.row];
+  float mu_next = 0.f, r_next = 0.f;
+  if (w.left > 0) {
+    mu_next = a.mean[w.row];
+    r_next = a.rstd[w.row];
   }
   uint64_t dgamma[VECS][P], dbeta[VECS][P], gamma[kKeep ? VECS : 1][P];
 #pragma unroll
   for (int j = 0; j < VECS; ++j) {
 #pragma unroll
     for (int i = 0; i < P; ++i) dgamma[j][i] = dbeta[j][i] = 0;
-    if (kKeep && w.column(j) < a.C)
-      weight_pairs<E, RAGGED>(a.gamma, w.column(j), a.C, a.wdtype, 1.f, gamma[j]);
+    if (kKeep) weight_pairs<E, RAGGED>(a.gamma, w.column(j), a.C, a.wdtype, 1.f, gamma[j]);
   }
-  // dy, (z - mean) rstd and dy gamma of vector j (columns outside the row: 0)
-  auto gather = [&](int j, uint64_t (&dy)[P], uint64_t (&h)[P], uint64_t (&g)[P]) {
+  // dy, (z - mean) rstd and dy gamma of vector j (columns outside the row: dy = 0)
+  auto gather = [&](int stage, int j, float mu, float r, uint64_t (&dy)[P], uint64_t (&h)[P],
+                    uint64_t (&g)[P]) {
     float fd[E], fz[E];
-    w.get(0, j, fd);
-    w.get(1, j, fz);
+    w.get(stage, 0, j, fd);
+    w.get(stage, 1, j, fz);
     if (RAGGED) {
       keep_inside<E>(fd, w.column(j), a.C, 0.f);
-      keep_inside<E>(fz, w.column(j), a.C, mu);
+      keep_inside<E>(fz, w.column(j), a.C, 0.f);
     }
     if (!kKeep) weight_pairs<E, RAGGED>(a.gamma, w.column(j), a.C, a.wdtype, 1.f, gamma[0]);
     const uint64_t minus_mu = ptx::f2_make(-mu, -mu), r2 = ptx::f2_make(r, r);
@@ -429,76 +522,113 @@ __global__ void __launch_bounds__(S::BLOCK, 512 / S::BLOCK) bwd_kernel(BwdArgs a
     }
   };
   int parity = 0;
-  for (; w.more(); w.next()) {
-    const bool active = w.active();
-    float mu_next = 0.f, r_next = 0.f;
-    if (w.row + w.step < a.rows) {
+  // first half of the current row: s = sum g and u = sum g h of this thread
+  auto first_half = [&](float& mu, float& r, float& s, float& u) {
+    mu = mu_next;
+    r = r_next;
+    mu_next = r_next = 0.f;
+    if (w.left > 1) {
       mu_next = a.mean[w.row + w.step];
       r_next = a.rstd[w.row + w.step];
     }
     w.arrive();
     uint64_t s2 = 0, u2 = 0;
-    uint64_t h[kKeep ? VECS : 1][P], g[kKeep ? VECS : 1][P];
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
-      if (active && w.column(j) < a.C) {
-        const int k = kKeep ? j : 0;
-        uint64_t dy[P];
-        gather(j, dy, h[k], g[k]);
+      uint64_t dy[P], h[P], g[P];
+      gather(w.take, j, mu, r, dy, h, g);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          dgamma[j][i] = ptx::f2_fma(dy[i], h[k][i], dgamma[j][i]);
-          dbeta[j][i] = ptx::f2_add(dbeta[j][i], dy[i]);
-          s2 = ptx::f2_add(s2, g[k][i]);
-          u2 = ptx::f2_fma(g[k][i], h[k][i], u2);
-        }
+      for (int i = 0; i < P; ++i) {
+        dgamma[j][i] = ptx::f2_fma(dy[i], h[i], dgamma[j][i]);
+        dbeta[j][i] = ptx::f2_add(dbeta[j][i], dy[i]);
+        s2 = ptx::f2_add(s2, g[i]);
+        u2 = ptx::f2_fma(g[i], h[i], u2);
       }
     }
-    float s = lane_sum<kLanes>(ptx::f2_lo(s2) + ptx::f2_hi(s2));
-    float u = lane_sum<kLanes>(ptx::f2_lo(u2) + ptx::f2_hi(u2));
-    if (kWarps > 1) {
-      if ((threadIdx.x & 31) == 0) part[parity][threadIdx.x >> 5] = make_float2(s, u);
-      __syncthreads();
-      const float2 p = part[parity][threadIdx.x % kWarps];
-      s = lane_sum<kWarps>(p.x);
-      u = lane_sum<kWarps>(p.y);
-      parity ^= 1;
-    }
+    s = ptx::f2_lo(s2) + ptx::f2_hi(s2);
+    u = ptx::f2_lo(u2) + ptx::f2_hi(u2);
+    if (kWarps > 1)
+      s = warp_sums(s, u);
+    else
+      lane_sums<kLanes>(s, u);
+  };
+  auto mark = [&]() { return Mark{w.e, w.row, w.take, S::ROWS == 1 || w.active()}; };
+  auto second_half = [&](const Mark& m, float mu, float r, float s, float u) {
     // dz = r g + (-r mean(g h)) h + (-r mean(g)) + dz_in
     const float rs = -r * (s * inv_C), ru = -r * (u * inv_C);
     const uint64_t r2 = ptx::f2_make(r, r), rs2 = ptx::f2_make(rs, rs), ru2 = ptx::f2_make(ru, ru);
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
       const int c = w.column(j);
-      if (active && c < a.C) {
-        const int k = kKeep ? j : 0;
-        if (!kKeep) {
-          uint64_t dy[P];
-          gather(j, dy, h[0], g[0]);
-        }
-        float f[E];
-        if (a.dz != nullptr) {
-          w.get(2, j, f);
-        } else {
+      uint64_t dy[P], h[P], g[P];
+      gather(m.stage, j, mu, r, dy, h, g);
+      float f[E];
+      if (DZ) w.get(m.stage, NT - 1, j, f);
 #pragma unroll
-          for (int i = 0; i < E; ++i) f[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const uint64_t v = ptx::f2_fma(g[k][i], r2, ptx::f2_fma(h[k][i], ru2, rs2));
-          const uint64_t o = ptx::f2_add(v, ptx::f2_make(f[2 * i], f[2 * i + 1]));
-          f[2 * i] = ptx::f2_lo(o);
-          f[2 * i + 1] = ptx::f2_hi(o);
-        }
-        store_row_vec<T, RAGGED>(static_cast<T*>(a.dres) + w.element(j), f, c, a.C);
-        if (a.dx != nullptr) {
-          if (DROP) drop_vec<E>(f, w.element(j), a.drop);
-          store_row_vec<T, RAGGED>(static_cast<T*>(a.dx) + w.element(j), f, c, a.C);
-        }
+      for (int i = 0; i < P; ++i) {
+        uint64_t o = ptx::f2_fma(g[i], r2, ptx::f2_fma(h[i], ru2, rs2));
+        if (DZ) o = ptx::f2_add(o, ptx::f2_make(f[2 * i], f[2 * i + 1]));
+        f[2 * i] = ptx::f2_lo(o);
+        f[2 * i + 1] = ptx::f2_hi(o);
       }
+      if (m.active && w.inside(j))
+        store_row_vec<T, RAGGED>(static_cast<T*>(a.dres) + m.e + w.offset(j), f, c, a.C);
+      if (DROP) drop_vec<E>(f, m.e + w.offset(j), a.drop);
+      if ((DROP || a.dx != nullptr) && m.active && w.inside(j))
+        store_row_vec<T, RAGGED>(static_cast<T*>(a.dx) + m.e + w.offset(j), f, c, a.C);
     }
-    mu = mu_next;
-    r = r_next;
+  };
+  // hands the warp's sums to the block, and takes all of them back
+  auto give = [&](float s) {
+    if (kWarps > 1) {
+      if ((threadIdx.x & 15) == 0) {
+        float2* p = &part[parity][threadIdx.x >> 5];
+        ((threadIdx.x & 16) == 0 ? p->x : p->y) = s;
+      }
+      __syncthreads();
+    }
+  };
+  auto take = [&](float& s, float& u) {
+    if (kWarps > 1) {
+      uint64_t v = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; i += 2) {
+        const float4 p = *reinterpret_cast<const float4*>(&part[parity][i]);
+        v = ptx::f2_add(v, ptx::f2_add(ptx::f2_make(p.x, p.y), ptx::f2_make(p.z, p.w)));
+      }
+      s = ptx::f2_lo(v);
+      u = ptx::f2_hi(v);
+      parity ^= 1;
+    }
+  };
+
+  long long turns = block_turns<S>(a.rows);
+  float mu = 0.f, r = 0.f, s = 0.f, u = 0.f;
+  if (LAG == 0) {
+    for (; turns > 0; --turns, w.next()) {
+      first_half(mu, r, s, u);
+      give(s);
+      take(s, u);
+      second_half(mark(), mu, r, s, u);
+    }
+  } else if (turns > 0) {
+    first_half(mu, r, s, u);
+    Mark m = mark();
+    give(s);
+    for (w.next(); turns > 1; --turns, w.next()) {
+      float mu1, r1, s1, u1;
+      take(s, u);
+      first_half(mu1, r1, s1, u1);
+      second_half(m, mu, r, s, u);
+      m = mark();
+      mu = mu1;
+      r = r1;
+      s = s1;
+      u = u1;
+      give(s);
+    }
+    take(s, u);
+    second_half(m, mu, r, s, u);
   }
   copy_wait<0>();
   if (a.workspace == nullptr) return;
@@ -700,16 +830,13 @@ int blocks_per_sm(Kernel kern, int block, int smem, std::atomic<int> (&cache)[kM
 
 // Launches a walking kernel: as many blocks as are resident at a time, in
 // eights, no more than there are rows for or `most`; returns their number or a
-// negative error. ring(tensors): its shared memory.
-template <typename S, int TENSORS, typename Kernel, typename Args>
-int launch_walk(Kernel kern, const Args& a, int tensors, int stages, int least_smem,
-                long long most, std::atomic<bool> (&limit_set)[kMaxTrackedDevices],
-                std::atomic<int> (&resident)[2][kMaxTrackedDevices], cudaStream_t stream) {
-  const int stage_bytes = S::VECS * S::BLOCK * 16;
-  const int smem = std::max(stages * tensors * stage_bytes, least_smem);
-  if (!set_smem_limit_once(kern, stages * TENSORS * stage_bytes, limit_set))
-    return ATTN_ERR_LAUNCH;
-  const int per_sm = blocks_per_sm(kern, S::BLOCK, smem, resident[TENSORS - tensors]);
+// negative error. The ring takes `smem` bytes.
+template <typename S, typename Kernel, typename Args>
+int launch_walk(Kernel kern, const Args& a, int smem, long long most,
+                std::atomic<bool> (&limit_set)[kMaxTrackedDevices],
+                std::atomic<int> (&resident)[kMaxTrackedDevices], cudaStream_t stream) {
+  if (!set_smem_limit_once(kern, smem, limit_set)) return ATTN_ERR_LAUNCH;
+  const int per_sm = blocks_per_sm(kern, S::BLOCK, smem, resident);
   if (per_sm <= 0) return ATTN_ERR_LAUNCH;
   long long grid = static_cast<long long>(sm_count() > 0 ? sm_count() : 1) * per_sm;
   grid = std::max(8LL, std::min(grid, most) / 8 * 8);
@@ -719,24 +846,30 @@ int launch_walk(Kernel kern, const Args& a, int tensors, int stages, int least_s
   return rc != ATTN_OK ? rc : static_cast<int>(grid);
 }
 
-// Stages of a ring of rows of `bytes`: four within 48 KB a tensor, so that
-// several blocks share an SM, and what fits beyond.
-constexpr int stages_for(int tensors, int bytes) {
-  return tensors * bytes <= 32768 ? 4 : (tensors * bytes * 2 <= 196608 ? 2 : 1);
+// Stages of a ring whose stage has `bytes`: four while several blocks share
+// an SM, and what fits beyond.
+constexpr int stages_for(int bytes) {
+  return bytes <= 24576 ? 4 : (bytes * 3 <= 196608 ? 3 : (bytes * 2 <= 196608 ? 2 : 1));
 }
 
-template <typename T, bool DROP, bool RAGGED>
+template <typename T, bool ADD, bool DROP, bool RAGGED>
 int fwd_rows(const FwdArgs& a, cudaStream_t stream) {
   return with_shape<T>(a.C, [&](auto shape) {
     using S = decltype(shape);
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
-    static std::atomic<int> resident[2][kMaxTrackedDevices];
-    constexpr int kStages = stages_for(2, S::VECS * S::BLOCK * 16);
-    const int n = launch_walk<S, 2>(fwd_kernel<T, S, kStages, DROP, RAGGED>, a,
-                                    a.residual != nullptr ? 2 : 1, kStages, 0, 1LL << 20,
-                                    limit_set, resident, stream);
+    static std::atomic<int> resident[kMaxTrackedDevices];
+    constexpr int kBytes = (ADD ? 2 : 1) * S::VECS * S::BLOCK * 16, kStages = stages_for(kBytes);
+    const int n = launch_walk<S>(fwd_kernel<T, S, kStages, 1, ADD, DROP, RAGGED>, a, kStages * kBytes,
+                                 1LL << 20, limit_set, resident, stream);
     return n < 0 ? n : static_cast<int>(ATTN_OK);
   });
+}
+
+template <typename T, bool RAGGED>
+int fwd_kinds(const FwdArgs& a, cudaStream_t stream) {
+  if (a.residual == nullptr) return fwd_rows<T, false, false, RAGGED>(a, stream);
+  return a.drop.on ? fwd_rows<T, true, true, RAGGED>(a, stream)
+                   : fwd_rows<T, true, false, RAGGED>(a, stream);
 }
 
 template <typename T>
@@ -745,24 +878,31 @@ int run_fwd(const FwdArgs& a, cudaStream_t stream) {
     fwd_wide_kernel<T><<<grid_for(a.rows), kThreads, 0, stream>>>(a);
     return launch_status();
   }
-  const bool ragged = a.C % Vec<T>::kElems != 0;
-  if (a.drop.on)
-    return ragged ? fwd_rows<T, true, true>(a, stream) : fwd_rows<T, true, false>(a, stream);
-  return ragged ? fwd_rows<T, false, true>(a, stream) : fwd_rows<T, false, false>(a, stream);
+  return a.C % Vec<T>::kElems != 0 ? fwd_kinds<T, true>(a, stream) : fwd_kinds<T, false>(a, stream);
 }
 
-template <typename T, bool DROP, bool RAGGED>
+template <typename T, bool DZ, bool DROP, bool RAGGED>
 int bwd_rows(const BwdArgs& a, cudaStream_t stream) {
   return with_shape<T>(a.C, [&](auto shape) {
     using S = decltype(shape);
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
-    static std::atomic<int> resident[2][kMaxTrackedDevices];
-    constexpr int kStages = stages_for(3, S::VECS * S::BLOCK * 16);
-    // the block's sums of short rows go through the ring's memory
-    return launch_walk<S, 3>(bwd_kernel<T, S, kStages, DROP, RAGGED>, a,
-                             a.dz != nullptr ? 3 : 2, kStages, S::ROWS > 1 ? 2 * a.C * 4 : 0,
-                             kMaxChunks, limit_set, resident, stream);
+    static std::atomic<int> resident[kMaxTrackedDevices];
+    constexpr int kBytes = (DZ ? 3 : 2) * S::VECS * S::BLOCK * 16, kStages = stages_for(kBytes);
+    // the block's sums of short rows (two floats for each of up to 512
+    // columns) go through the ring's memory
+    static_assert(S::ROWS == 1 || kStages * kBytes >= 2 * 512 * 4, "ring too small for the sums");
+    return launch_walk<S>(bwd_kernel<T, S, kStages, (kStages > 2 ? 1 : 0), DZ, DROP, RAGGED>, a, kStages * kBytes,
+                          kMaxChunks, limit_set, resident, stream);
   });
+}
+
+template <typename T, bool RAGGED>
+int bwd_kinds(const BwdArgs& a, cudaStream_t stream) {
+  if (a.dz != nullptr)
+    return a.drop.on ? bwd_rows<T, true, true, RAGGED>(a, stream)
+                     : bwd_rows<T, true, false, RAGGED>(a, stream);
+  return a.drop.on ? bwd_rows<T, false, true, RAGGED>(a, stream)
+                   : bwd_rows<T, false, false, RAGGED>(a, stream);
 }
 
 template <typename T>
@@ -778,10 +918,7 @@ int run_bwd(const BwdArgs& a, cudaStream_t stream) {
     const int rc = launch_status();
     return rc != ATTN_OK ? rc : chunks;
   }
-  const bool ragged = a.C % Vec<T>::kElems != 0;
-  if (a.drop.on)
-    return ragged ? bwd_rows<T, true, true>(a, stream) : bwd_rows<T, true, false>(a, stream);
-  return ragged ? bwd_rows<T, false, true>(a, stream) : bwd_rows<T, false, false>(a, stream);
+  return a.C % Vec<T>::kElems != 0 ? bwd_kinds<T, true>(a, stream) : bwd_kinds<T, false>(a, stream);
 }
 
 }  // namespace norm
