@@ -248,13 +248,24 @@ def attn_rotary_frequencies(rot, base=10000.0, scaling=ATTN_ROTARY_PLAIN, factor
     return rc, list(turns[:n]), magnitude.value
 
 
+_stride_arrays = {}
+
+
 def _strides(values, count):
-    """A C array of `count` element strides, or NULL."""
+    """A C array of `count` element strides, or NULL. The arrays of the few
+    layouts that a program uses are kept by their values (building one costs
+    more than a launch's other arguments)."""
     if values is None:
         return None
-    if len(values) != count:
-        raise ValueError("expected %d strides, got %d" % (count, len(values)))
-    return (_L * count)(*values)
+    key = tuple(values)
+    array = _stride_arrays.get(key)
+    if array is None:
+        if len(_stride_arrays) >= 256:
+            _stride_arrays.clear()
+        array = _stride_arrays[key] = (_L * len(key))(*key)
+    if len(key) != count:
+        raise ValueError("expected %d strides, got %d" % (count, len(key)))
+    return array
 
 
 def attn_rotary(q, k, q_out, k_out, turns, positions, pos_stride, B, H, H_kv, N, d, rot, magnitude,

@@ -25,8 +25,10 @@ namespace norm {
 
 inline Drop make_drop(float p, unsigned long long seed) {
   Drop d;
-  d.seed_lo = static_cast<uint32_t>(seed);
-  d.seed_hi = static_cast<uint32_t>(seed >> 32);
+  for (uint32_t r = 0; r < 10; ++r) {
+    d.key[r][0] = static_cast<uint32_t>(seed) + r * 0x9E3779B9u;
+    d.key[r][1] = static_cast<uint32_t>(seed >> 32) + r * 0xBB67AE85u;
+  }
   d.threshold = dropout_threshold(p);
   d.inv_keep = static_cast<float>(1.0 / (1.0 - static_cast<double>(p)));
   d.on = p > 0.0f;
@@ -53,15 +55,11 @@ __global__ void __launch_bounds__(kThreads)
   }
   uint32_t w[U * E / 4][4];
   if (DROP) {
+    long long first[U * E / 4];
 #pragma unroll
-    for (int u = 0; u < U * E / 4; ++u) {
-      const long long c = ((e0 + (u / (E / 4)) * (kThreads * E)) >> 2) + u % (E / 4);
-      w[u][0] = static_cast<uint32_t>(c);
-      w[u][1] = static_cast<uint32_t>(c >> 32);
-      w[u][2] = 0u;
-      w[u][3] = 1u;
-    }
-    philox4x32_10_batch<U * E / 4, 10>(w, drop.seed_lo, drop.seed_hi);
+    for (int u = 0; u < U * E / 4; ++u)
+      first[u] = (e0 + (u / (E / 4)) * (kThreads * E)) | (4 * (u % (E / 4)));
+    keep_words<U * E / 4>(first, drop, w);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -81,9 +79,11 @@ __global__ void __launch_bounds__(kThreads)
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      if (DROP)
-        v[i] = w[u * E / 4 + i / 4][i % 4] >= drop.threshold ? v[i] * drop.inv_keep : 0.f;
-      if (residual != nullptr) v[i] += r[i];
+      if (DROP) v[i] = w[u * E / 4 + i / 4][i % 4] >= drop.threshold ? v[i] : 0.f;
+      if (residual != nullptr)
+        v[i] = DROP ? fmaf(v[i], drop.inv_keep, r[i]) : v[i] + r[i];
+      else if (DROP)
+        v[i] *= drop.inv_keep;
     }
     if (whole) {
       Vec<T> o;
@@ -98,14 +98,24 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Second stage of the weight gradients: a block takes 32 columns, its 32
-// warps every 32nd partial sum of each, and adds the warps' sums in order.
+// warps every 32nd partial sum of each (kept in flight eight at a time), and
+// adds the warps' sums in order.
 __global__ void __launch_bounds__(1024) weights_sum_kernel(BwdArgs a, int chunks) {
   __shared__ float part[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + tx;
   float v = 0.f;
-  if (i < 2 * a.C)
-    for (int k = ty; k < chunks; k += 32) v += a.workspace[2LL * k * a.C + i];
+  if (i < 2 * a.C) {
+    const float* p = a.workspace + i;
+    for (int k = ty; k < chunks; k += 256) {
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        x[u] = k + 32 * u < chunks ? p[2LL * (k + 32 * u) * a.C] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v += x[u];
+    }
+  }
   part[ty][tx] = v;
   __syncthreads();
   if (ty == 0 && i < 2 * a.C) {

@@ -5,7 +5,6 @@
 #include <cstdint>
 
 #include "element.cuh"
-#include "philox.cuh"
 
 namespace attn {
 namespace norm {
@@ -18,7 +17,10 @@ constexpr int kMaxChunks = 1024;
 constexpr int kMaxRow = 16384;
 
 struct Drop {
-  uint32_t seed_lo, seed_hi, threshold;
+  // the generator's ten round keys: as kernel parameters they are operands of
+  // the rounds' exclusive-ors and cost no instruction
+  uint32_t key[10][2];
+  uint32_t threshold;  // keep iff word >= threshold
   float inv_keep;
   int on;
 };
@@ -52,24 +54,51 @@ int run_fwd(const FwdArgs& a, cudaStream_t stream);
 template <typename T>
 int run_bwd(const BwdArgs& a, cudaStream_t stream);
 
-__device__ __forceinline__ bool kept(long long e, const Drop& d) {
-  const PhiloxOut w = philox4x32_10(static_cast<uint32_t>(e >> 2), static_cast<uint32_t>(e >> 34),
-                                    0u, 1u, d.seed_lo, d.seed_hi);
-  return w.w[e & 3] >= d.threshold;
-}
-
-// Keep words of the 4 NB elements from e (a multiple of 4) on.
+// Keep words of the 4 NB elements from e on, e a multiple of 4: calls of
+// consecutive counters, round by round, so that their multiplies interleave
+// (philox.cuh has the generator's definition).
 template <int NB>
-__device__ __forceinline__ void keep_words(long long e, const Drop& d, uint32_t (&w)[NB][4]) {
+__device__ __forceinline__ void keep_words(const long long (&e)[NB], const Drop& d,
+                                           uint32_t (&w)[NB][4]) {
 #pragma unroll
   for (int u = 0; u < NB; ++u) {
-    const long long c = (e >> 2) + u;
-    w[u][0] = static_cast<uint32_t>(c);
-    w[u][1] = static_cast<uint32_t>(c >> 32);
+    w[u][0] = static_cast<uint32_t>(e[u] >> 2);
+    w[u][1] = static_cast<uint32_t>(e[u] >> 34);
     w[u][2] = 0u;
     w[u][3] = 1u;
   }
-  philox4x32_10_batch<NB, 10>(w, d.seed_lo, d.seed_hi);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * w[u][0];
+      const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * w[u][2];
+      w[u][0] = static_cast<uint32_t>(p1 >> 32) ^ w[u][1] ^ d.key[r][0];
+      w[u][1] = static_cast<uint32_t>(p1);
+      w[u][2] = static_cast<uint32_t>(p0 >> 32) ^ w[u][3] ^ d.key[r][1];
+      w[u][3] = static_cast<uint32_t>(p0);
+    }
+  }
+}
+
+__device__ __forceinline__ bool kept(long long e, const Drop& d) {
+  const long long first[1] = {e & ~3LL};
+  uint32_t w[1][4];
+  keep_words<1>(first, d, w);
+  const int i = static_cast<int>(e & 3);
+  return (i == 0 ? w[0][0] : i == 1 ? w[0][1] : i == 2 ? w[0][2] : w[0][3]) >= d.threshold;
+}
+
+// Sets the dropped ones of the E elements from e (a multiple of 4) on to 0.
+template <int E>
+__device__ __forceinline__ void drop_vec(float (&f)[E], long long e, const Drop& d) {
+  long long first[E / 4];
+  uint32_t w[E / 4][4];
+#pragma unroll
+  for (int u = 0; u < E / 4; ++u) first[u] = e | (4 * u);  // e is a multiple of E
+  keep_words<E / 4>(first, d, w);
+#pragma unroll
+  for (int i = 0; i < E; ++i) f[i] = w[i / 4][i % 4] >= d.threshold ? f[i] : 0.f;
 }
 
 }  // namespace norm

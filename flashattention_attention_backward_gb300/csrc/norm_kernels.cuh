@@ -19,13 +19,25 @@
 namespace attn {
 namespace norm {
 
-template <int TPR_, int VECS_>
+template <int TPR_, int VECS_, int LEAST>
 struct Shape {
   static constexpr int TPR = TPR_;    // threads per row
   static constexpr int VECS = VECS_;  // 16-byte vectors per thread
-  static constexpr int BLOCK = TPR_ <= 32 ? 256 : TPR_;
+  static constexpr int BLOCK = TPR_ < LEAST ? LEAST : TPR_;
   static constexpr int ROWS = BLOCK / TPR_;  // rows of a block at a time
+  static constexpr int WARPS = TPR_ > 32 ? TPR_ / 32 : 1;  // warps per row
+  static constexpr int LANES = TPR_ > 32 ? 32 : TPR_;      // lanes of a warp per row
 };
+
+// Barrier over a row's threads (rows of several warps; the block's other rows
+// go on by themselves).
+template <typename S>
+__device__ __forceinline__ void row_barrier() {
+  if (S::ROWS == 1)
+    __syncthreads();
+  else
+    ptx::named_bar_sync(1 + threadIdx.x / S::TPR, S::TPR);
+}
 
 // The E weights (or biases) of columns c .. c + E - 1 (a multiple of four) as
 // they lie in memory, widened by get(); `fill` where there is no array.
@@ -93,15 +105,6 @@ __device__ __forceinline__ void keep_inside(float (&f)[E], int c, int C, float f
     if (static_cast<unsigned>(c + i) >= static_cast<unsigned>(C)) f[i] = fill;
 }
 
-// Drops and scales the E elements from e (a multiple of four) on.
-template <int E>
-__device__ __forceinline__ void drop_vec(float (&f)[E], long long e, const Drop& d) {
-  uint32_t w[E / 4][4];
-  keep_words<E / 4>(e, d, w);
-#pragma unroll
-  for (int i = 0; i < E; ++i) f[i] = w[i / 4][i % 4] >= d.threshold ? f[i] * d.inv_keep : 0.f;
-}
-
 // Writes the vector's elements that lie in the row.
 template <typename T, bool RAGGED, int E>
 __device__ __forceinline__ void store_row_vec(T* p, const float (&f)[E], int c, int C) {
@@ -136,17 +139,18 @@ __device__ __forceinline__ void copy_wait() {
 // LAG turns more. Vectors outside the row read as zeros.
 template <typename T, typename S, int STAGES, int LAG, int NT, bool RAGGED>
 struct Walk {
-  static constexpr int kAhead = STAGES - 1 - LAG;  // rows being copied
   static constexpr int E = Vec<T>::kElems;
-  static constexpr int kStageBytes = NT * S::VECS * S::BLOCK * 16;
-  uint4* ring;          // this thread's slots: [STAGES][NT][VECS], BLOCK apart
-  const T* from[NT];    // vector 0 of the next row to copy
-  const T* end[NT];     // behind the tensors (RAGGED)
-  long long stride;     // elements between this thread's rows
-  long long e;          // element of the current row's vector 0
-  long long row, step, left, to_copy;  // left: this thread's rows still to come
+  static constexpr int kAhead = STAGES - 1 - LAG;  // rows being copied
+  static constexpr int kStage = NT * S::VECS * S::BLOCK;  // slots of a stage
+  uint4* ring;        // this thread's slots: [STAGES][NT][VECS], BLOCK apart
+  const T* from[NT];  // vector 0 of the next row to copy
+  const T* end[NT];   // behind the tensors (RAGGED)
+  long long stride;   // elements between this thread's rows
+  long long e;        // element of the current row's vector 0
+  long long row, step;
+  int left, to_copy;  // this thread's rows still to come, and to be copied
   int t, shift, C;
-  int fill, take;       // stages
+  int fill, take;     // where the stages begin
 
   __device__ __forceinline__ Walk(uint4* smem, const void* const (&src)[NT], long long rows, int C_)
       : ring(smem + threadIdx.x), C(C_), fill(0), take(0) {
@@ -156,7 +160,7 @@ struct Walk {
     shift = RAGGED ? static_cast<int>((row * C) % E) : 0;
     e = row * C - shift + t * E;
     stride = step * C;
-    left = row < rows ? (rows - row + step - 1) / step : 0;
+    left = row < rows ? static_cast<int>((rows - row + step - 1) / step) : 0;
     to_copy = left;
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
@@ -177,10 +181,17 @@ struct Walk {
   __device__ __forceinline__ bool inside(int j) const { return column(j) < C; }
   // element of vector j, less that of vector 0
   __device__ __forceinline__ static constexpr int offset(int j) { return j * S::TPR * E; }
-  __device__ __forceinline__ bool active() const { return left > 0; }
+  // turns to take: this thread's rows; where several rows share a warp, the
+  // most that one of the block's has (active() tells whether a row is there)
+  __device__ __forceinline__ int turns(long long rows) const {
+    if (S::TPR >= 32) return left;
+    const long long first = static_cast<long long>(blockIdx.x) * S::ROWS;
+    return first < rows ? static_cast<int>((rows - first + step - 1) / step) : 0;
+  }
+  __device__ __forceinline__ bool active() const { return S::TPR >= 32 || left > 0; }
 
   __device__ __forceinline__ void copy_next() {
-    uint4* to = ring + fill * (kStageBytes / 16);
+    uint4* to = ring + fill;
     if (to_copy > 0) {
 #pragma unroll
       for (int j = 0; j < S::VECS; ++j) {
@@ -198,7 +209,7 @@ struct Walk {
           }
         }
       }
-    } else if (S::ROWS > 1) {  // other rows of the block go on: no stale values
+    } else if (S::TPR < 32) {  // the warp's other rows go on: no stale values
 #pragma unroll
       for (int k = 0; k < NT * S::VECS; ++k) to[k * S::BLOCK] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -206,34 +217,26 @@ struct Walk {
     --to_copy;
 #pragma unroll
     for (int q = 0; q < NT; ++q) from[q] += stride;
-    fill = fill == STAGES - 1 ? 0 : fill + 1;
+    fill = fill == (STAGES - 1) * kStage ? 0 : fill + kStage;
   }
   // starts the next copies and waits for the current row's
   __device__ __forceinline__ void arrive() {
     copy_next();
     copy_wait<kAhead>();
   }
-  __device__ __forceinline__ void get(int stage, int q, int j, float (&f)[E]) const {
+  // vector j of tensor q in the stage that begins at `at`
+  __device__ __forceinline__ void get(int at, int q, int j, float (&f)[E]) const {
     Vec<T> v;
-    v.w = ring[stage * (kStageBytes / 16) + (q * S::VECS + j) * S::BLOCK];
+    v.w = ring[at + (q * S::VECS + j) * S::BLOCK];
     unpack(v, f);
   }
   __device__ __forceinline__ void next() {
     row += step;
     e += stride;
     --left;
-    take = take == STAGES - 1 ? 0 : take + 1;
+    take = take == (STAGES - 1) * kStage ? 0 : take + kStage;
   }
 };
-
-// Rows of the block's first group of threads: as many turns as the block
-// takes, the same for all of its threads.
-template <typename S>
-__device__ __forceinline__ long long block_turns(long long rows) {
-  const long long first = static_cast<long long>(blockIdx.x) * S::ROWS;
-  const long long step = static_cast<long long>(gridDim.x) * S::ROWS;
-  return first < rows ? (rows - first + step - 1) / step : 0;
-}
 
 // Sum over groups of W lanes, the same value in each.
 template <int W>
@@ -280,14 +283,15 @@ struct Mark {
 // next row's first, so that the reductions of one are covered by the
 // arithmetic of the other. ADD: with a residual, and z written.
 template <typename T, typename S, int STAGES, int LAG, bool ADD, bool DROP, bool RAGGED>
-__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 512 / S::BLOCK : 1)
-    fwd_kernel(FwdArgs a) {
-  constexpr int E = Vec<T>::kElems, TPR = S::TPR, VECS = S::VECS, P = E / 2, NT = ADD ? 2 : 1;
-  constexpr bool kKeep = VECS * E <= 16;  // weights stay in registers
-  constexpr int kLanes = TPR < 32 ? TPR : 32, kWarps = TPR / kLanes;
+__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(FwdArgs a) {
+  constexpr int E = Vec<T>::kElems, VECS = S::VECS, P = E / 2, NT = ADD ? 2 : 1;
+  constexpr bool kKeep = VECS * E <= 16 && S::TPR <= 512;  // weights stay in registers
+  constexpr int kLanes = S::LANES, kWarps = S::WARPS;
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float2 part[2][kWarps];
-  __shared__ float counts[kWarps];
+  __shared__ float2 parts[S::ROWS][2][kWarps];
+  __shared__ float counts[S::BLOCK / 32];
+  auto& part = parts[kWarps > 1 ? threadIdx.x / S::TPR : 0];
+  const int warp = threadIdx.x / 32 % kWarps;  // of the row
   const void* src[NT];
   src[0] = a.x;
   if (ADD) src[NT - 1] = a.residual;
@@ -310,14 +314,15 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 512 / S::BLOCK : 1
   if (kWarps > 1) {
     if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = count;
     __syncthreads();
-    other = counts[threadIdx.x % kWarps];
+    other = counts[threadIdx.x / 32 - warp + threadIdx.x % kWarps];
   }
   int parity = 0;
 
   // first half of the current row: v, and the mean and squares of the warp's part
   auto first_half = [&](uint64_t (&v)[VECS][P], float& mu, float& q) {
     w.arrive();
-    const bool active = S::ROWS == 1 || w.active();
+    const bool active = w.active();
+    const uint64_t inv_keep = ptx::f2_make(a.drop.inv_keep, a.drop.inv_keep);
     uint64_t s2 = 0, q2 = 0;
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
@@ -331,7 +336,8 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 512 / S::BLOCK : 1
         w.get(w.take, NT - 1, j, r);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          v[j][i] = ptx::f2_add(v[j][i], ptx::f2_make(r[2 * i], r[2 * i + 1]));
+          const uint64_t r2 = ptx::f2_make(r[2 * i], r[2 * i + 1]);
+          v[j][i] = DROP ? ptx::f2_fma(v[j][i], inv_keep, r2) : ptx::f2_add(v[j][i], r2);
           f[2 * i] = ptx::f2_lo(v[j][i]);
           f[2 * i + 1] = ptx::f2_hi(v[j][i]);
         }
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 512 / S::BLOCK : 1
     }
     q = lane_sum<kLanes>(ptx::f2_lo(q2) + ptx::f2_hi(q2));
   };
-  auto mark = [&]() { return Mark{w.e, w.row, w.take, S::ROWS == 1 || w.active()}; };
+  auto mark = [&]() { return Mark{w.e, w.row, w.take, w.active()}; };
   // second half of row m, from the parts' means and squares
   auto second_half = [&](const Mark& m, const uint64_t (&v)[VECS][P], float mu, float q) {
     if (kWarps > 1) {
@@ -405,8 +411,8 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 512 / S::BLOCK : 1
   // hands the warp's part to the block, and takes the parts back
   auto give = [&](float mu, float q) {
     if (kWarps > 1) {
-      if ((threadIdx.x & 31) == 0) part[parity][threadIdx.x >> 5] = make_float2(mu, q);
-      __syncthreads();
+      if ((threadIdx.x & 31) == 0) part[parity][warp] = make_float2(mu, q);
+      row_barrier<S>();
     }
   };
   auto take = [&](float& mu, float& q) {
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 512 / S::BLOCK : 1
     }
   };
 
-  long long turns = block_turns<S>(a.rows);
+  int turns = w.turns(a.rows);
   if (turns == 0) return;
   uint64_t v[VECS][P];
   float mu, q;
@@ -476,13 +482,14 @@ __device__ __forceinline__ float warp_sums(float s, float u) {
 // over all of the thread's rows; then, with the sums joined over the row's
 // threads, its gradient, from the ring again. DZ: with a dz to add.
 template <typename T, typename S, int STAGES, int LAG, bool DZ, bool DROP, bool RAGGED>
-__global__ void __launch_bounds__(S::BLOCK, 512 / S::BLOCK) bwd_kernel(BwdArgs a) {
-  constexpr int E = Vec<T>::kElems, TPR = S::TPR, VECS = S::VECS, BLOCK = S::BLOCK, P = E / 2;
+__global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
+  constexpr int E = Vec<T>::kElems, VECS = S::VECS, BLOCK = S::BLOCK, P = E / 2;
   constexpr int NT = DZ ? 3 : 2;
   constexpr bool kKeep = VECS * E <= 16;  // weights stay in registers
-  constexpr int kLanes = TPR < 32 ? TPR : 32, kWarps = TPR / kLanes;
+  constexpr int kLanes = S::LANES, kWarps = S::WARPS;
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ __align__(16) float2 part[2][kWarps];
+  __shared__ __align__(16) float2 parts[S::ROWS][2][kWarps];
+  auto& part = parts[kWarps > 1 ? threadIdx.x / S::TPR : 0];
   const void* src[NT];
   src[0] = a.dy;
   src[1] = a.z;
@@ -502,27 +509,26 @@ __global__ void __launch_bounds__(S::BLOCK, 512 / S::BLOCK) bwd_kernel(BwdArgs a
     for (int i = 0; i < P; ++i) dgamma[j][i] = dbeta[j][i] = 0;
     if (kKeep) weight_pairs<E, RAGGED>(a.gamma, w.column(j), a.C, a.wdtype, 1.f, gamma[j]);
   }
-  // dy, (z - mean) rstd and dy gamma of vector j (columns outside the row: dy = 0)
-  auto gather = [&](int stage, int j, float mu, float r, uint64_t (&dy)[P], uint64_t (&h)[P],
-                    uint64_t (&g)[P]) {
+  // dy and z - mean of vector j (columns outside the row: dy = 0)
+  auto gather = [&](int at, int j, float mu, uint64_t (&dy)[P], uint64_t (&d)[P]) {
     float fd[E], fz[E];
-    w.get(stage, 0, j, fd);
-    w.get(stage, 1, j, fz);
+    w.get(at, 0, j, fd);
+    w.get(at, 1, j, fz);
     if (RAGGED) {
       keep_inside<E>(fd, w.column(j), a.C, 0.f);
       keep_inside<E>(fz, w.column(j), a.C, 0.f);
     }
     if (!kKeep) weight_pairs<E, RAGGED>(a.gamma, w.column(j), a.C, a.wdtype, 1.f, gamma[0]);
-    const uint64_t minus_mu = ptx::f2_make(-mu, -mu), r2 = ptx::f2_make(r, r);
+    const uint64_t minus_mu = ptx::f2_make(-mu, -mu);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       dy[i] = ptx::f2_make(fd[2 * i], fd[2 * i + 1]);
-      h[i] = ptx::f2_mul(ptx::f2_add(ptx::f2_make(fz[2 * i], fz[2 * i + 1]), minus_mu), r2);
-      g[i] = ptx::f2_mul(dy[i], gamma[kKeep ? j : 0][i]);
+      d[i] = ptx::f2_add(ptx::f2_make(fz[2 * i], fz[2 * i + 1]), minus_mu);
     }
   };
   int parity = 0;
-  // first half of the current row: s = sum g and u = sum g h of this thread
+  // first half of the current row: this thread's s = sum dy gamma and
+  // u = sum dy (z - mean) gamma; rstd comes in behind the sums
   auto first_half = [&](float& mu, float& r, float& s, float& u) {
     mu = mu_next;
     r = r_next;
@@ -532,17 +538,19 @@ __global__ void __launch_bounds__(S::BLOCK, 512 / S::BLOCK) bwd_kernel(BwdArgs a
       r_next = a.rstd[w.row + w.step];
     }
     w.arrive();
+    const uint64_t r2 = ptx::f2_make(r, r);
     uint64_t s2 = 0, u2 = 0;
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
-      uint64_t dy[P], h[P], g[P];
-      gather(w.take, j, mu, r, dy, h, g);
+      uint64_t dy[P], d[P];
+      gather(w.take, j, mu, dy, d);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        dgamma[j][i] = ptx::f2_fma(dy[i], h[i], dgamma[j][i]);
+        const uint64_t t = ptx::f2_mul(dy[i], d[i]);
+        dgamma[j][i] = ptx::f2_fma(t, r2, dgamma[j][i]);
         dbeta[j][i] = ptx::f2_add(dbeta[j][i], dy[i]);
-        s2 = ptx::f2_add(s2, g[i]);
-        u2 = ptx::f2_fma(g[i], h[i], u2);
+        s2 = ptx::f2_fma(dy[i], gamma[kKeep ? j : 0][i], s2);
+        u2 = ptx::f2_fma(t, gamma[kKeep ? j : 0][i], u2);
       }
     }
     s = ptx::f2_lo(s2) + ptx::f2_hi(s2);
@@ -552,29 +560,39 @@ __global__ void __launch_bounds__(S::BLOCK, 512 / S::BLOCK) bwd_kernel(BwdArgs a
     else
       lane_sums<kLanes>(s, u);
   };
-  auto mark = [&]() { return Mark{w.e, w.row, w.take, S::ROWS == 1 || w.active()}; };
+  auto mark = [&]() { return Mark{w.e, w.row, w.take, w.active()}; };
   auto second_half = [&](const Mark& m, float mu, float r, float s, float u) {
-    // dz = r g + (-r mean(g h)) h + (-r mean(g)) + dz_in
-    const float rs = -r * (s * inv_C), ru = -r * (u * inv_C);
+    // dz = r g - r (r u / C) h - r s / C + dz_in, h = (z - mean) r
+    const float rs = -r * (s * inv_C), ru = -r * (r * u * inv_C);
     const uint64_t r2 = ptx::f2_make(r, r), rs2 = ptx::f2_make(rs, rs), ru2 = ptx::f2_make(ru, ru);
+    const uint64_t inv_keep = ptx::f2_make(a.drop.inv_keep, a.drop.inv_keep);
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
       const int c = w.column(j);
-      uint64_t dy[P], h[P], g[P];
-      gather(m.stage, j, mu, r, dy, h, g);
+      uint64_t dy[P], d[P];
+      gather(m.stage, j, mu, dy, d);
       float f[E];
       if (DZ) w.get(m.stage, NT - 1, j, f);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        uint64_t o = ptx::f2_fma(g[i], r2, ptx::f2_fma(h[i], ru2, rs2));
-        if (DZ) o = ptx::f2_add(o, ptx::f2_make(f[2 * i], f[2 * i + 1]));
-        f[2 * i] = ptx::f2_lo(o);
-        f[2 * i + 1] = ptx::f2_hi(o);
+        const uint64_t g = ptx::f2_mul(dy[i], gamma[kKeep ? j : 0][i]);
+        dy[i] = ptx::f2_fma(g, r2, ptx::f2_fma(ptx::f2_mul(d[i], r2), ru2, rs2));
+        if (DZ) dy[i] = ptx::f2_add(dy[i], ptx::f2_make(f[2 * i], f[2 * i + 1]));
+        f[2 * i] = ptx::f2_lo(dy[i]);
+        f[2 * i + 1] = ptx::f2_hi(dy[i]);
       }
-      if (m.active && w.inside(j))
-        store_row_vec<T, RAGGED>(static_cast<T*>(a.dres) + m.e + w.offset(j), f, c, a.C);
-      if (DROP) drop_vec<E>(f, m.e + w.offset(j), a.drop);
-      if ((DROP || a.dx != nullptr) && m.active && w.inside(j))
+      const bool write = m.active && w.inside(j);
+      if (write) store_row_vec<T, RAGGED>(static_cast<T*>(a.dres) + m.e + w.offset(j), f, c, a.C);
+      if (DROP) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          dy[i] = ptx::f2_mul(dy[i], inv_keep);
+          f[2 * i] = ptx::f2_lo(dy[i]);
+          f[2 * i + 1] = ptx::f2_hi(dy[i]);
+        }
+        drop_vec<E>(f, m.e + w.offset(j), a.drop);
+      }
+      if ((DROP || a.dx != nullptr) && write)
         store_row_vec<T, RAGGED>(static_cast<T*>(a.dx) + m.e + w.offset(j), f, c, a.C);
     }
   };
@@ -582,10 +600,10 @@ __global__ void __launch_bounds__(S::BLOCK, 512 / S::BLOCK) bwd_kernel(BwdArgs a
   auto give = [&](float s) {
     if (kWarps > 1) {
       if ((threadIdx.x & 15) == 0) {
-        float2* p = &part[parity][threadIdx.x >> 5];
+        float2* p = &part[parity][threadIdx.x / 32 % kWarps];
         ((threadIdx.x & 16) == 0 ? p->x : p->y) = s;
       }
-      __syncthreads();
+      row_barrier<S>();
     }
   };
   auto take = [&](float& s, float& u) {
@@ -602,7 +620,7 @@ __global__ void __launch_bounds__(S::BLOCK, 512 / S::BLOCK) bwd_kernel(BwdArgs a
     }
   };
 
-  long long turns = block_turns<S>(a.rows);
+  int turns = w.turns(a.rows);
   float mu = 0.f, r = 0.f, s = 0.f, u = 0.f;
   if (LAG == 0) {
     for (; turns > 0; --turns, w.next()) {
@@ -653,20 +671,22 @@ __global__ void __launch_bounds__(S::BLOCK, 512 / S::BLOCK) bwd_kernel(BwdArgs a
       out[a.C + c] = y;
     });
   } else {
-    // the row groups of the block add up in shared memory, one after another
-    float* sum = reinterpret_cast<float*>(ring);
+    // the block's rows of threads leave theirs side by side in the ring's
+    // memory, and each column is added up over them in order
+    float* sums = reinterpret_cast<float*>(ring);
+    float* own = sums + threadIdx.x / S::TPR * 2 * a.C;
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.C; i += BLOCK) sum[i] = 0.f;
-    for (int k = 0; k < S::ROWS; ++k) {
-      __syncthreads();
-      if (k == threadIdx.x / TPR)
-        columns([&](int c, float x, float y) {
-          sum[c] += x;
-          sum[a.C + c] += y;
-        });
+    columns([&](int c, float x, float y) {
+      own[c] = x;
+      own[a.C + c] = y;
+    });
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.C; i += BLOCK) {
+      float v = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < S::ROWS; ++k) v += sums[k * 2 * a.C + i];
+      out[i] = v;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.C; i += BLOCK) out[i] = sum[i];
   }
 }
 
@@ -788,21 +808,22 @@ inline unsigned grid_for(long long want) {
 }
 
 // f(Shape) for the row length: up to 16 elements a thread (32 for the widest),
-// so that the backward's sums stay in registers.
-template <typename T, typename F>
+// so that the backward's sums stay in registers; blocks of at least LEAST
+// threads.
+template <typename T, int LEAST, typename F>
 int with_shape(int C, F f) {
   constexpr int E = Vec<T>::kElems;
   // a ragged row takes up to one vector more than its length needs
   const int n = C % E == 0 ? C : C + 2 * E - 2;
-  if (n <= 64) return f(Shape<8, 8 / E>{});
-  if (n <= 128) return f(Shape<8, 16 / E>{});
-  if (n <= 256) return f(Shape<16, 16 / E>{});
-  if (n <= 512) return f(Shape<32, 16 / E>{});
-  if (n <= 1024) return f(Shape<128, 8 / E>{});
-  if (n <= 2048) return f(Shape<128, 16 / E>{});
-  if (n <= 4096) return f(Shape<256, 16 / E>{});
-  if (n <= 8192) return f(Shape<512, 16 / E>{});
-  return f(Shape<512, 32 / E>{});
+  if (n <= 64) return f(Shape<8, 8 / E, LEAST>{});
+  if (n <= 128) return f(Shape<8, 16 / E, LEAST>{});
+  if (n <= 256) return f(Shape<16, 16 / E, LEAST>{});
+  if (n <= 512) return f(Shape<32, 16 / E, LEAST>{});
+  if (n <= 1024) return f(Shape<64, 16 / E, LEAST>{});
+  if (n <= 2048) return f(Shape<128, 16 / E, LEAST>{});
+  if (n <= 4096) return f(Shape<256, 16 / E, LEAST>{});
+  if (n <= 8192) return f(Shape<512, 16 / E, LEAST>{});
+  return f(Shape<512, 32 / E, LEAST>{});
 }
 
 template <typename T>
@@ -846,19 +867,19 @@ int launch_walk(Kernel kern, const Args& a, int smem, long long most,
   return rc != ATTN_OK ? rc : static_cast<int>(grid);
 }
 
-// Stages of a ring whose stage has `bytes`: four while several blocks share
-// an SM, and what fits beyond.
-constexpr int stages_for(int bytes) {
-  return bytes <= 24576 ? 4 : (bytes * 3 <= 196608 ? 3 : (bytes * 2 <= 196608 ? 2 : 1));
+// Stages of a ring whose stage has `bytes`: four, or what `room` has place for.
+constexpr int stages_for(int bytes, int room) {
+  return bytes * 4 <= room ? 4 : (bytes * 3 <= room ? 3 : (bytes * 2 <= room ? 2 : 1));
 }
 
 template <typename T, bool ADD, bool DROP, bool RAGGED>
 int fwd_rows(const FwdArgs& a, cudaStream_t stream) {
-  return with_shape<T>(a.C, [&](auto shape) {
+  return with_shape<T, 256>(a.C, [&](auto shape) {
     using S = decltype(shape);
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
     static std::atomic<int> resident[kMaxTrackedDevices];
-    constexpr int kBytes = (ADD ? 2 : 1) * S::VECS * S::BLOCK * 16, kStages = stages_for(kBytes);
+    constexpr int kBytes = (ADD ? 2 : 1) * S::VECS * S::BLOCK * 16, 
+                  kStages = stages_for(kBytes, S::BLOCK <= 256 ? 98304 : 196608);
     const int n = launch_walk<S>(fwd_kernel<T, S, kStages, 1, ADD, DROP, RAGGED>, a, kStages * kBytes,
                                  1LL << 20, limit_set, resident, stream);
     return n < 0 ? n : static_cast<int>(ATTN_OK);
@@ -883,14 +904,16 @@ int run_fwd(const FwdArgs& a, cudaStream_t stream) {
 
 template <typename T, bool DZ, bool DROP, bool RAGGED>
 int bwd_rows(const BwdArgs& a, cudaStream_t stream) {
-  return with_shape<T>(a.C, [&](auto shape) {
+  // one block of 512 threads an SM: one partial sum a column each
+  return with_shape<T, 512>(a.C, [&](auto shape) {
     using S = decltype(shape);
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
     static std::atomic<int> resident[kMaxTrackedDevices];
-    constexpr int kBytes = (DZ ? 3 : 2) * S::VECS * S::BLOCK * 16, kStages = stages_for(kBytes);
-    // the block's sums of short rows (two floats for each of up to 512
-    // columns) go through the ring's memory
-    static_assert(S::ROWS == 1 || kStages * kBytes >= 2 * 512 * 4, "ring too small for the sums");
+    constexpr int kBytes = (DZ ? 3 : 2) * S::VECS * S::BLOCK * 16;
+    constexpr int kStages = stages_for(kBytes, 196608);
+    // the ring's memory also takes the sums of the block's rows of threads
+    static_assert(S::ROWS == 1 || kStages * kBytes >= S::BLOCK * S::VECS * Vec<T>::kElems * 8,
+                  "ring too small for the sums");
     return launch_walk<S>(bwd_kernel<T, S, kStages, (kStages > 2 ? 1 : 0), DZ, DROP, RAGGED>, a, kStages * kBytes,
                           kMaxChunks, limit_set, resident, stream);
   });
