@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "norm_common.cuh"
+#include "sm103_ptx.cuh"
 
 namespace attn {
 namespace norm {
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(1024) weights_sum_kernel(BwdArgs a, int chunks
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + tx;
   float v = 0.f;
+  ptx::grid_dependency_wait();  // launched before the first stage has ended
   if (i < 2 * a.C) {
     const float* p = a.workspace + i;
     for (int k = ty; k < chunks; k += 256) {
@@ -155,7 +157,19 @@ int backward(const BwdArgs& a, int dtype, cudaStream_t stream) {
     if (chunks < 0) return chunks;
   }
   if (!weights) return ATTN_OK;
-  weights_sum_kernel<<<(2 * a.C + 31) / 32, 1024, 0, stream>>>(a, chunks);
+  // launched while the first stage still runs (its launch is then behind it);
+  // it waits for that stage's results on the device
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(static_cast<unsigned>((2 * a.C + 31) / 32));
+  config.blockDim = dim3(1024);
+  config.stream = stream;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  if (cudaLaunchKernelEx(&config, weights_sum_kernel, a, chunks) != cudaSuccess)
+    return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
   return launch_status();
 }
 

@@ -39,84 +39,113 @@ __device__ __forceinline__ void row_barrier() {
     ptx::named_bar_sync(1 + threadIdx.x / S::TPR, S::TPR);
 }
 
-// The E weights (or biases) of columns c .. c + E - 1 (a multiple of four) as
-// they lie in memory, widened by get(); `fill` where there is no array.
-template <int E>
-struct Weights {
-  uint32_t w[E];  // 16-bit types fill the first half
-  __device__ __forceinline__ void load(const void* p, int c, int wdtype) {
-    if (p == nullptr) return;
+// The weights (or biases) of a thread's N vectors of E columns, from column
+// c(j) on, in fp32 pairs: `fill` where there is no array, 0 outside the row.
+// All loads go out before any is used.
+template <int N, int E, bool RAGGED, typename F>
+__device__ __forceinline__ void load_weights(const void* p, int C, int wdtype, float fill, F c,
+                                             uint64_t (&g)[N][E / 2]) {
+  float f[N][E];
 #pragma unroll
-    for (int i = 0; i < E; i += 4) {
-      if (wdtype == ATTN_FP32) {
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + c + i);
-        w[i] = v.x;
-        w[i + 1] = v.y;
-        w[i + 2] = v.z;
-        w[i + 3] = v.w;
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c + i);
-        w[i / 2] = v.x;
-        w[i / 2 + 1] = v.y;
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      f[j][i] = static_cast<unsigned>(c(j) + i) < static_cast<unsigned>(C) ? fill : 0.f;
+  if (p != nullptr && RAGGED) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (static_cast<unsigned>(c(j) + i) < static_cast<unsigned>(C))
+          f[j][i] = load_as(p, c(j) + i, wdtype);
+  } else if (p != nullptr && wdtype == ATTN_FP32) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (c(j) >= C) continue;
+#pragma unroll
+      for (int i = 0; i < E; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + c(j) + i);
+        f[j][i] = v.x;
+        f[j][i + 1] = v.y;
+        f[j][i + 2] = v.z;
+        f[j][i + 3] = v.w;
+      }
+    }
+  } else if (p != nullptr) {
+    uint2 v[N][E / 4];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (c(j) >= C) continue;
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i)
+        v[j][i] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c(j) + 4 * i);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (c(j) >= C) continue;
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const uint32_t w = i % 2 == 0 ? v[j][i / 2].x : v[j][i / 2].y;
+        const float2 h = wdtype == ATTN_BF16
+                             ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+                             : __half22float2(*reinterpret_cast<const __half2*>(&w));
+        f[j][2 * i] = h.x;
+        f[j][2 * i + 1] = h.y;
       }
     }
   }
-  __device__ __forceinline__ void get(const void* p, int wdtype, float fill, float (&f)[E]) const {
-    if (p == nullptr) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = fill;
-    } else if (wdtype == ATTN_FP32) {
+  for (int j = 0; j < N; ++j)
 #pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = __uint_as_float(w[i]);
-    } else if (wdtype == ATTN_BF16) {
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        f[2 * i] = h.x;
-        f[2 * i + 1] = h.y;
-      }
-    }
-  }
-};
-
-// The same for any c, one element at a time; `fill` outside the row too.
-template <int E>
-__device__ __forceinline__ void load_weights_ragged(const void* p, int c, int C, int wdtype,
-                                                    float fill, float (&f)[E]) {
-#pragma unroll
-  for (int i = 0; i < E; ++i)
-    f[i] = p != nullptr && static_cast<unsigned>(c + i) < static_cast<unsigned>(C)
-               ? load_as(p, c + i, wdtype)
-               : fill;
+    for (int i = 0; i < E / 2; ++i) g[j][i] = ptx::f2_make(f[j][2 * i], f[j][2 * i + 1]);
 }
 
-// Sets the elements of columns outside the row to `fill`.
-template <int E>
-__device__ __forceinline__ void keep_inside(float (&f)[E], int c, int C, float fill) {
-  if (c >= 0 && c + E <= C) return;
+// Writes the elements of a vector that reach over the row's ends: the last
+// ones (start of a row) or the first ones (end of a row) in pieces of four,
+// two and one element of 16 bits, or two and one of 32 bits.
+template <typename T>
+__device__ __forceinline__ void store_edge(T* p, const Vec<T>& v, int c, int C) {
+  constexpr int E = Vec<T>::kElems;
+  const uint32_t w[4] = {v.w.x, v.w.y, v.w.z, v.w.w};
+  if (c < 0 && c + E > C) {  // a row inside one vector
+    const T* e = reinterpret_cast<const T*>(w);
 #pragma unroll
-  for (int i = 0; i < E; ++i)
-    if (static_cast<unsigned>(c + i) >= static_cast<unsigned>(C)) f[i] = fill;
+    for (int i = 0; i < E; ++i)
+      if (static_cast<unsigned>(c + i) < static_cast<unsigned>(C)) p[i] = e[i];
+    return;
+  }
+  const bool start = c < 0;
+  const int n = start ? E + c : C - c;  // elements in the row
+  uint32_t* const q = reinterpret_cast<uint32_t*>(p);
+  if (E == 4) {
+    if (n & 2) *reinterpret_cast<uint2*>(q + (start ? 2 : 0)) = start ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
+    if (n & 1) {
+      const int i = start ? 4 - n : n - 1;
+      q[i] = i < 2 ? (i == 0 ? w[0] : w[1]) : (i == 2 ? w[2] : w[3]);
+    }
+  } else {
+    if (n & 4) *reinterpret_cast<uint2*>(q + (start ? 2 : 0)) = start ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
+    if (n & 2) {
+      const int i = start ? (n & 4 ? 1 : 3) : (n & 4 ? 2 : 0);
+      q[i] = i < 2 ? (i == 0 ? w[0] : w[1]) : (i == 2 ? w[2] : w[3]);
+    }
+    if (n & 1) {
+      const int i = start ? 8 - n : n - 1;  // odd at the start of a row, even at its end
+      const uint32_t x = i < 4 ? (i < 2 ? w[0] : w[1]) : (i < 6 ? w[2] : w[3]);
+      reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(start ? x >> 16 : x);
+    }
+  }
 }
 
 // Writes the vector's elements that lie in the row.
 template <typename T, bool RAGGED, int E>
 __device__ __forceinline__ void store_row_vec(T* p, const float (&f)[E], int c, int C) {
-  if (!RAGGED || (c >= 0 && c + E <= C)) {
-    Vec<T> v;
-    pack(f, v);
+  Vec<T> v;
+  pack(f, v);
+  if (!RAGGED || (c >= 0 && c + E <= C))
     store_vec(p, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (static_cast<unsigned>(c + i) < static_cast<unsigned>(C)) p[i] = from_f32<T>(f[i]);
-  }
+  else
+    store_edge(p, v, c, C);
 }
 
 __device__ __forceinline__ void copy_async16(uint32_t smem, const void* global) {
@@ -135,18 +164,20 @@ __device__ __forceinline__ void copy_wait() {
 // the weights' gradients, stay in registers. Rows of NT tensors come through
 // a ring of STAGES in shared memory, filled by asynchronous copies: a thread
 // reads back only what it copied itself, so the ring needs no barrier, and
-// the next rows' loads run while this one is reduced. A row's slots stay for
-// LAG turns more. Vectors outside the row read as zeros.
-template <typename T, typename S, int STAGES, int LAG, int NT, bool RAGGED>
+// the next rows' loads run while these are reduced. A turn takes R rows, whose
+// chains of dependent steps (sums over lanes, the barrier) then overlap.
+// Vectors outside the row read as zeros, rows behind the last too.
+template <typename T, typename S, int STAGES, int R, int NT, bool RAGGED>
 struct Walk {
   static constexpr int E = Vec<T>::kElems;
-  static constexpr int kAhead = STAGES - 1 - LAG;  // rows being copied
+  static constexpr int kAhead = STAGES - R;               // rows being copied
   static constexpr int kStage = NT * S::VECS * S::BLOCK;  // slots of a stage
+  static_assert(STAGES % R == 0 && kAhead >= 0, "a turn's rows lie side by side in the ring");
   uint4* ring;        // this thread's slots: [STAGES][NT][VECS], BLOCK apart
   const T* from[NT];  // vector 0 of the next row to copy
   const T* end[NT];   // behind the tensors (RAGGED)
   long long stride;   // elements between this thread's rows
-  long long e;        // element of the current row's vector 0
+  long long e;        // element of the turn's first row's vector 0
   long long row, step;
   int left, to_copy;  // this thread's rows still to come, and to be copied
   int t, shift, C;
@@ -179,16 +210,25 @@ struct Walk {
   // vector from the row's end, it reaches over the row's ends (RAGGED)
   __device__ __forceinline__ int column(int j) const { return (t + j * S::TPR) * E - shift; }
   __device__ __forceinline__ bool inside(int j) const { return column(j) < C; }
+  __device__ __forceinline__ bool edge(int j) const {
+    return RAGGED && (column(j) < 0 || column(j) + E > C);
+  }
   // element of vector j, less that of vector 0
   __device__ __forceinline__ static constexpr int offset(int j) { return j * S::TPR * E; }
-  // turns to take: this thread's rows; where several rows share a warp, the
-  // most that one of the block's has (active() tells whether a row is there)
+  // turns to take: for this thread's rows; where several rows share a warp,
+  // for the most that one of the block's has
   __device__ __forceinline__ int turns(long long rows) const {
-    if (S::TPR >= 32) return left;
-    const long long first = static_cast<long long>(blockIdx.x) * S::ROWS;
-    return first < rows ? static_cast<int>((rows - first + step - 1) / step) : 0;
+    int n = left;
+    if (S::TPR < 32) {
+      const long long first = static_cast<long long>(blockIdx.x) * S::ROWS;
+      n = first < rows ? static_cast<int>((rows - first + step - 1) / step) : 0;
+    }
+    return (n + R - 1) / R;
   }
-  __device__ __forceinline__ bool active() const { return S::TPR >= 32 || left > 0; }
+  // whether the turn's k-th row is one
+  __device__ __forceinline__ bool active(int k) const {
+    return (k == 0 && S::TPR >= 32) || left > k;
+  }
 
   __device__ __forceinline__ void copy_next() {
     uint4* to = ring + fill;
@@ -209,7 +249,7 @@ struct Walk {
           }
         }
       }
-    } else if (S::TPR < 32) {  // the warp's other rows go on: no stale values
+    } else {
 #pragma unroll
       for (int k = 0; k < NT * S::VECS; ++k) to[k * S::BLOCK] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -219,22 +259,39 @@ struct Walk {
     for (int q = 0; q < NT; ++q) from[q] += stride;
     fill = fill == (STAGES - 1) * kStage ? 0 : fill + kStage;
   }
-  // starts the next copies and waits for the current row's
-  __device__ __forceinline__ void arrive() {
-    copy_next();
+  // starts the next copies and waits for the turn's rows; of the first
+  // `trimmed` tensors, what lies outside a row becomes zero
+  __device__ __forceinline__ void arrive(int trimmed) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) copy_next();
     copy_wait<kAhead>();
+#pragma unroll
+    for (int j = 0; j < S::VECS; ++j) {
+      if (inside(j) && edge(j)) {
+        uint32_t m[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (static_cast<unsigned>(column(j) + i) < static_cast<unsigned>(C))
+            m[i * 4 / E] |= sizeof(T) == 4 ? 0xffffffffu : (i % 2 == 0 ? 0xffffu : 0xffff0000u);
+        for (int k = 0; k < R; ++k)
+          for (int q = 0; q < trimmed; ++q) {
+            uint4& v = ring[take + k * kStage + (q * S::VECS + j) * S::BLOCK];
+            v = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
+          }
+      }
+    }
   }
-  // vector j of tensor q in the stage that begins at `at`
-  __device__ __forceinline__ void get(int at, int q, int j, float (&f)[E]) const {
+  // vector j of tensor q of the turn's k-th row
+  __device__ __forceinline__ void get(int k, int q, int j, float (&f)[E]) const {
     Vec<T> v;
-    v.w = ring[at + (q * S::VECS + j) * S::BLOCK];
+    v.w = ring[take + k * kStage + (q * S::VECS + j) * S::BLOCK];
     unpack(v, f);
   }
   __device__ __forceinline__ void next() {
-    row += step;
-    e += stride;
-    --left;
-    take = take == (STAGES - 1) * kStage ? 0 : take + kStage;
+    row += R * step;
+    e += R * stride;
+    left -= R;
+    take = take == (STAGES - R) * kStage ? 0 : take + R * kStage;
   }
 };
 
@@ -246,279 +303,265 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// Weights of columns c .. c + E - 1 in fp32 pairs (a null array: `fill`).
-template <int E, bool RAGGED>
-__device__ __forceinline__ void weight_pairs(const void* p, int c, int C, int wdtype, float fill,
-                                             uint64_t (&g)[E / 2]) {
-  float f[E];
-  if (c >= C) {
+// R values to sum over a warp's lanes, R = 1, 2 or 4. While more than one is
+// left a lane hands half of them to its partner and keeps the others, so that
+// R values take few more exchanges than one: 5, 5 or 6 instead of 5, 10 or 20.
+// A lane ends with the sum of value lane / (32 / R).
+template <int R>
+__device__ __forceinline__ float warp_sums(float (&v)[R]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = 0.f;
-  } else if (RAGGED) {
-    load_weights_ragged<E>(p, c, C, wdtype, fill, f);
-  } else {
-    Weights<E> w;
-    w.load(p, c, wdtype);
-    w.get(p, wdtype, fill, f);
+  for (int n = R; n > 1; n /= 2) {
+    const int off = 16 * n / R;
+    const bool low = (lane & off) == 0;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float give = low ? v[n / 2 + i] : v[i];
+      v[i] = (low ? v[i] : v[n / 2 + i]) + __shfl_xor_sync(0xffffffffu, give, off);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) g[i] = ptx::f2_make(f[2 * i], f[2 * i + 1]);
+  for (int off = 16 / R; off >= 1; off /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+  return v[0];
 }
 
-// What a row leaves for the second half of its turn.
-struct Mark {
-  long long e, row;
-  int stage;
-  bool active;
-};
+// Sum of R values over a row's threads, the same in each; all R at a time.
+// `part` has R * WARPS floats of the row's own. One barrier.
+template <typename S, int R>
+__device__ __forceinline__ void row_sums(float (&v)[R], float* part) {
+  if (S::WARPS == 1) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] = lane_sum<S::LANES>(v[i]);
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 % S::WARPS;
+  const float mine = warp_sums<R>(v);
+  if (lane % (32 / R) == 0) part[lane / (32 / R) * S::WARPS + warp] = mine;
+  row_barrier<S>();
+  // a group of lanes adds up each value's parts
+  constexpr int kGroup = S::WARPS < 32 / R ? S::WARPS : 32 / R;
+  const float* p = part + lane / kGroup % R * S::WARPS + lane % kGroup;
+  float sum = p[0];
+#pragma unroll
+  for (int i = kGroup; i < S::WARPS; i += kGroup) sum += p[i];
+  sum = lane_sum<kGroup>(sum);
+#pragma unroll
+  for (int i = 0; i < R; ++i) v[i] = R == 1 ? sum : __shfl_sync(0xffffffffu, sum, i * kGroup);
+}
 
-// Forward, a row in two halves.
-// First half: its sum with the residual, behind the dropout, goes to fp32
-// registers, in pairs (one instruction for two columns); a warp takes the mean
-// of its part and the squares about that. Second half: parts of n_w elements
-// are joined by
+// Forward: a row (its sum with the residual, behind the dropout) is held in
+// fp32 registers, in pairs (one instruction for two columns). A warp takes the
+// mean of its part and the squares about that; parts of n_w elements are
+// joined by
 //   mu = sum n_w mu_w / C,  sum of squares = sum (q_w + n_w (mu_w - mu)^2),
-// which loses nothing to cancellation and costs one barrier a row, and the
-// output is written. LAG = 1: a row's second half runs in one turn with the
-// next row's first, so that the reductions of one are covered by the
-// arithmetic of the other. ADD: with a residual, and z written.
-template <typename T, typename S, int STAGES, int LAG, bool ADD, bool DROP, bool RAGGED>
+// which loses nothing to cancellation and costs one barrier a turn of R rows.
+// ADD: with a residual, and z written.
+template <typename T, typename S, int STAGES, int R, bool ADD, bool DROP, bool RAGGED>
 __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(FwdArgs a) {
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, P = E / 2, NT = ADD ? 2 : 1;
-  constexpr bool kKeep = VECS * E <= 16 && S::TPR <= 512;  // weights stay in registers
   constexpr int kLanes = S::LANES, kWarps = S::WARPS;
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float2 parts[S::ROWS][2][kWarps];
+  __shared__ float2 parts[S::ROWS][2][R * kWarps];
   __shared__ float counts[S::BLOCK / 32];
   auto& part = parts[kWarps > 1 ? threadIdx.x / S::TPR : 0];
-  const int warp = threadIdx.x / 32 % kWarps;  // of the row
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 % kWarps;  // of the row
   const void* src[NT];
   src[0] = a.x;
   if (ADD) src[NT - 1] = a.residual;
-  Walk<T, S, STAGES, 0, NT, RAGGED> w(ring, src, a.rows, a.C);
+  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.rows, a.C);
   const float inv_C = 1.0f / static_cast<float>(a.C);
-  uint64_t gamma[kKeep ? VECS : 1][P], beta[kKeep ? VECS : 1][P];
+  uint64_t gamma[VECS][P], beta[VECS][P];
+  auto column = [&](int j) { return w.column(j); };
+  load_weights<VECS, E, RAGGED>(a.gamma, a.C, a.wdtype, 1.f, column, gamma);
+  load_weights<VECS, E, RAGGED>(a.beta, a.C, a.wdtype, 0.f, column, beta);
   int mine = 0;  // this thread's columns inside the row
 #pragma unroll
-  for (int j = 0; j < VECS; ++j) {
-    const int c = w.column(j);
-    if (kKeep) {
-      weight_pairs<E, RAGGED>(a.gamma, c, a.C, a.wdtype, 1.f, gamma[j]);
-      weight_pairs<E, RAGGED>(a.beta, c, a.C, a.wdtype, 0.f, beta[j]);
-    }
-    if (w.inside(j)) mine += RAGGED ? min(c + E, a.C) - max(c, 0) : E;
-  }
+  for (int j = 0; j < VECS; ++j)
+    if (w.inside(j)) mine += RAGGED ? min(w.column(j) + E, a.C) - max(w.column(j), 0) : E;
   const float count = lane_sum<kLanes>(static_cast<float>(mine));  // n_w
   const float inv_count = count > 0.f ? 1.0f / count : 0.f;
-  float other = count;  // n_w of the warp whose part this lane joins
+  // the parts that a lane joins: of the turn's row lane / kGroup
+  constexpr int kGroup = kWarps < 32 / R ? kWarps : 32 / R;
   if (kWarps > 1) {
-    if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = count;
+    if (lane == 0) counts[threadIdx.x / 32] = count;
     __syncthreads();
-    other = counts[threadIdx.x / 32 - warp + threadIdx.x % kWarps];
   }
+  const uint64_t inv_keep = ptx::f2_make(a.drop.inv_keep, a.drop.inv_keep);
   int parity = 0;
-
-  // first half of the current row: v, and the mean and squares of the warp's part
-  auto first_half = [&](uint64_t (&v)[VECS][P], float& mu, float& q) {
-    w.arrive();
-    const bool active = w.active();
-    const uint64_t inv_keep = ptx::f2_make(a.drop.inv_keep, a.drop.inv_keep);
-    uint64_t s2 = 0, q2 = 0;
+  for (int turns = w.turns(a.rows); turns > 0; --turns, w.next()) {
+    w.arrive(NT);
+    uint64_t v[R][VECS][P];
+    float mu[R], q[R];
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      float f[E];
-      w.get(w.take, 0, j, f);
-      if (DROP) drop_vec<E>(f, w.e + w.offset(j), a.drop);
+    for (int k = 0; k < R; ++k) {
+      uint64_t s2 = 0;
 #pragma unroll
-      for (int i = 0; i < P; ++i) v[j][i] = ptx::f2_make(f[2 * i], f[2 * i + 1]);
-      if (ADD) {
-        float r[E];
-        w.get(w.take, NT - 1, j, r);
+      for (int j = 0; j < VECS; ++j) {
+        const long long e = w.e + k * w.stride + w.offset(j);
+        float f[E];
+        w.get(k, 0, j, f);
+        if (DROP) drop_vec<E>(f, e, a.drop);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const uint64_t r2 = ptx::f2_make(r[2 * i], r[2 * i + 1]);
-          v[j][i] = DROP ? ptx::f2_fma(v[j][i], inv_keep, r2) : ptx::f2_add(v[j][i], r2);
-          f[2 * i] = ptx::f2_lo(v[j][i]);
-          f[2 * i + 1] = ptx::f2_hi(v[j][i]);
+        for (int i = 0; i < P; ++i) v[k][j][i] = ptx::f2_make(f[2 * i], f[2 * i + 1]);
+        if (ADD) {
+          float r[E];
+          w.get(k, NT - 1, j, r);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const uint64_t r2 = ptx::f2_make(r[2 * i], r[2 * i + 1]);
+            v[k][j][i] = DROP ? ptx::f2_fma(v[k][j][i], inv_keep, r2) : ptx::f2_add(v[k][j][i], r2);
+            f[2 * i] = ptx::f2_lo(v[k][j][i]);
+            f[2 * i + 1] = ptx::f2_hi(v[k][j][i]);
+          }
+          if (w.active(k) && w.inside(j))
+            store_row_vec<T, RAGGED>(static_cast<T*>(a.z) + e, f, w.column(j), a.C);
         }
-        if (active && w.inside(j))
-          store_row_vec<T, RAGGED>(static_cast<T*>(a.z) + w.e + w.offset(j), f, w.column(j), a.C);
-      }
-      if (RAGGED) {
-        keep_inside<E>(f, w.column(j), a.C, 0.f);
 #pragma unroll
-        for (int i = 0; i < P; ++i) v[j][i] = ptx::f2_make(f[2 * i], f[2 * i + 1]);
+        for (int i = 0; i < P; ++i) s2 = ptx::f2_add(s2, v[k][j][i]);
       }
-#pragma unroll
-      for (int i = 0; i < P; ++i) s2 = ptx::f2_add(s2, v[j][i]);
+      mu[k] = ptx::f2_lo(s2) + ptx::f2_hi(s2);
     }
-    mu = lane_sum<kLanes>(ptx::f2_lo(s2) + ptx::f2_hi(s2)) * inv_count;
+    if (kWarps > 1 && R > 1) {
+      const float sum = warp_sums<R>(mu);
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      const int c = w.column(j);
-      if (RAGGED && (c < 0 || c + E > a.C)) {
+      for (int k = 0; k < R; ++k)
+        mu[k] = __shfl_sync(0xffffffffu, sum, k * (32 / R)) * inv_count;
+    } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float d = (i % 2 == 0 ? ptx::f2_lo(v[j][i / 2]) : ptx::f2_hi(v[j][i / 2])) - mu;
-          if (static_cast<unsigned>(c + i) < static_cast<unsigned>(a.C))
-            q2 = ptx::f2_fma(ptx::f2_make(d, 0.f), ptx::f2_make(d, 0.f), q2);
+      for (int k = 0; k < R; ++k) mu[k] = lane_sum<kLanes>(mu[k]) * inv_count;
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      uint64_t q2 = 0;
+#pragma unroll
+      for (int j = 0; j < VECS; ++j) {
+        if (w.edge(j)) {  // partly, or all, outside: mu in place of its zeros there
+          const int c = w.column(j);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const bool lo = static_cast<unsigned>(c + 2 * i) < static_cast<unsigned>(a.C);
+            const bool hi = static_cast<unsigned>(c + 2 * i + 1) < static_cast<unsigned>(a.C);
+            v[k][j][i] = ptx::f2_make(lo ? ptx::f2_lo(v[k][j][i]) : mu[k],
+                                      hi ? ptx::f2_hi(v[k][j][i]) : mu[k]);
+          }
         }
-      } else {
-        const float m = w.inside(j) ? -mu : 0.f;  // outside the row v is 0
+        const float m = RAGGED || w.inside(j) ? -mu[k] : 0.f;  // outside the row v is 0
         const uint64_t minus = ptx::f2_make(m, m);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          const uint64_t d = ptx::f2_add(v[j][i], minus);
+          const uint64_t d = ptx::f2_add(v[k][j][i], minus);
           q2 = ptx::f2_fma(d, d, q2);
         }
       }
+      q[k] = ptx::f2_lo(q2) + ptx::f2_hi(q2);
     }
-    q = lane_sum<kLanes>(ptx::f2_lo(q2) + ptx::f2_hi(q2));
-  };
-  auto mark = [&]() { return Mark{w.e, w.row, w.take, w.active()}; };
-  // second half of row m, from the parts' means and squares
-  auto second_half = [&](const Mark& m, const uint64_t (&v)[VECS][P], float mu, float q) {
+    float rstd[R];
     if (kWarps > 1) {
-      const float mean = lane_sum<kWarps>(other * mu) * inv_C, d = mu - mean;
-      mu = mean;
-      q = lane_sum<kWarps>(other > 0.f ? fmaf(other * d, d, q) : 0.f);
-    }
-    const float r = rsqrtf(fmaf(q, inv_C, a.eps));
-    const uint64_t minus_mu = ptx::f2_make(-mu, -mu), r2 = ptx::f2_make(r, r);
+      const float sum = warp_sums<R>(q);
+      float mean = mu[0];  // of the row that this lane's sum belongs to
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      const int c = w.column(j), k = kKeep ? j : 0;
-      if (!kKeep) {
-        weight_pairs<E, RAGGED>(a.gamma, c, a.C, a.wdtype, 1.f, gamma[0]);
-        weight_pairs<E, RAGGED>(a.beta, c, a.C, a.wdtype, 0.f, beta[0]);
-      }
-      float f[E];
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const uint64_t h = ptx::f2_mul(ptx::f2_add(v[j][i], minus_mu), r2);
-        const uint64_t o = ptx::f2_fma(h, gamma[k][i], beta[k][i]);
-        f[2 * i] = ptx::f2_lo(o);
-        f[2 * i + 1] = ptx::f2_hi(o);
-      }
-      if (m.active && w.inside(j))
-        store_row_vec<T, RAGGED>(static_cast<T*>(a.y) + m.e + w.offset(j), f, c, a.C);
-    }
-    if (m.active && w.t == 0) {
-      if (a.mean != nullptr) a.mean[m.row] = mu;
-      if (a.rstd != nullptr) a.rstd[m.row] = r;
-    }
-  };
-  // hands the warp's part to the block, and takes the parts back
-  auto give = [&](float mu, float q) {
-    if (kWarps > 1) {
-      if ((threadIdx.x & 31) == 0) part[parity][warp] = make_float2(mu, q);
+      for (int k = 1; k < R; ++k) mean = lane / (32 / R) == k ? mu[k] : mean;
+      if (lane % (32 / R) == 0)
+        part[parity][lane / (32 / R) * kWarps + warp] = make_float2(mean, sum);
       row_barrier<S>();
-    }
-  };
-  auto take = [&](float& mu, float& q) {
-    if (kWarps > 1) {
-      const float2 p = part[parity][threadIdx.x % kWarps];
-      mu = p.x;
-      q = p.y;
+      // a group of lanes joins each row's parts
+      const int first = lane / kGroup % R * kWarps + lane % kGroup;
+      const float* n = &counts[threadIdx.x / 32 - warp + lane % kGroup];
+      float2 p[kWarps / kGroup];
+      float total = 0.f, squares = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps / kGroup; ++i) {
+        p[i] = part[parity][first + i * kGroup];
+        total = fmaf(n[i * kGroup], p[i].x, total);
+      }
+      total = lane_sum<kGroup>(total) * inv_C;
+#pragma unroll
+      for (int i = 0; i < kWarps / kGroup; ++i) {
+        const float d = p[i].x - total, c = n[i * kGroup];
+        squares += c > 0.f ? fmaf(c * d, d, p[i].y) : 0.f;
+      }
+      squares = lane_sum<kGroup>(squares);
+      const float r = rsqrtf(fmaf(squares, inv_C, a.eps));
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        mu[k] = R == 1 ? total : __shfl_sync(0xffffffffu, total, k * kGroup);
+        rstd[k] = R == 1 ? r : __shfl_sync(0xffffffffu, r, k * kGroup);
+      }
       parity ^= 1;
-    }
-  };
-
-  int turns = w.turns(a.rows);
-  if (turns == 0) return;
-  uint64_t v[VECS][P];
-  float mu, q;
-  if (LAG == 0) {
-    for (; turns > 0; --turns, w.next()) {
-      first_half(v, mu, q);
-      give(mu, q);
-      take(mu, q);
-      second_half(mark(), v, mu, q);
-    }
-  } else {
-    first_half(v, mu, q);
-    Mark m = mark();
-    give(mu, q);
-    for (w.next(); turns > 1; --turns, w.next()) {
-      uint64_t v_next[VECS][P];
-      float mu_next, q_next;
-      take(mu, q);
-      first_half(v_next, mu_next, q_next);
-      second_half(m, v, mu, q);
-      m = mark();
+    } else {
 #pragma unroll
-      for (int j = 0; j < VECS; ++j)
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[j][i] = v_next[j][i];
-      mu = mu_next;
-      q = q_next;
-      give(mu, q);
+      for (int k = 0; k < R; ++k) rstd[k] = rsqrtf(fmaf(lane_sum<kLanes>(q[k]), inv_C, a.eps));
     }
-    take(mu, q);
-    second_half(m, v, mu, q);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const uint64_t minus_mu = ptx::f2_make(-mu[k], -mu[k]), r2 = ptx::f2_make(rstd[k], rstd[k]);
+#pragma unroll
+      for (int j = 0; j < VECS; ++j) {
+        float f[E];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const uint64_t h = ptx::f2_mul(ptx::f2_add(v[k][j][i], minus_mu), r2);
+          const uint64_t o = ptx::f2_fma(h, gamma[j][i], beta[j][i]);
+          f[2 * i] = ptx::f2_lo(o);
+          f[2 * i + 1] = ptx::f2_hi(o);
+        }
+        if (w.active(k) && w.inside(j))
+          store_row_vec<T, RAGGED>(static_cast<T*>(a.y) + w.e + k * w.stride + w.offset(j), f,
+                                   w.column(j), a.C);
+      }
+      if (w.active(k) && w.t == 0) {
+        if (a.mean != nullptr) a.mean[w.row + k * w.step] = mu[k];
+        if (a.rstd != nullptr) a.rstd[w.row + k * w.step] = rstd[k];
+      }
+    }
   }
   copy_wait<0>();
 }
 
-// Sums of two values over groups of W lanes, the same values in each.
-template <int W>
-__device__ __forceinline__ void lane_sums(float& s, float& u) {
-  s = lane_sum<W>(s);
-  u = lane_sum<W>(u);
-}
-// Over a whole warp: the first exchange leaves half of the lanes with one
-// value and half with the other, so that one value a lane is left to sum.
-// Lane 0 has the first value's sum, lane 16 the second's.
-__device__ __forceinline__ float warp_sums(float s, float u) {
-  const bool low = (threadIdx.x & 16) == 0;
-  float v = (low ? s : u) + __shfl_xor_sync(0xffffffffu, low ? u : s, 16);
-#pragma unroll
-  for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
-
-// Backward, a row in two halves like the forward: first the row's two sums
-// and its part of the weights' gradients, whose column sums stay in registers
-// over all of the thread's rows; then, with the sums joined over the row's
-// threads, its gradient, from the ring again. DZ: with a dz to add.
-template <typename T, typename S, int STAGES, int LAG, bool DZ, bool DROP, bool RAGGED>
+// Backward: first the turn's rows' two sums each and their part of the
+// weights' gradients, whose column sums stay in registers over all of the
+// thread's rows; then, with the sums joined over the rows' threads, the rows'
+// gradients, from the ring again. DZ: with a dz to add.
+template <typename T, typename S, int STAGES, int R, bool DZ, bool DROP, bool RAGGED>
 __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, BLOCK = S::BLOCK, P = E / 2;
   constexpr int NT = DZ ? 3 : 2;
-  constexpr bool kKeep = VECS * E <= 16;  // weights stay in registers
-  constexpr int kLanes = S::LANES, kWarps = S::WARPS;
+  ptx::grid_dependency_launch();  // the second stage's launch, which waits for this grid's end
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ __align__(16) float2 parts[S::ROWS][2][kWarps];
-  auto& part = parts[kWarps > 1 ? threadIdx.x / S::TPR : 0];
+  __shared__ float parts[S::ROWS][2][2 * R * S::WARPS];
+  auto& part = parts[S::WARPS > 1 ? threadIdx.x / S::TPR : 0];
   const void* src[NT];
   src[0] = a.dy;
   src[1] = a.z;
   if (DZ) src[NT - 1] = a.dz;
-  Walk<T, S, STAGES, LAG, NT, RAGGED> w(ring, src, a.rows, a.C);
+  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.rows, a.C);
   const float inv_C = 1.0f / static_cast<float>(a.C);
-  // the statistics of the row to come, one row ahead
-  float mu_next = 0.f, r_next = 0.f;
-  if (w.left > 0) {
-    mu_next = a.mean[w.row];
-    r_next = a.rstd[w.row];
-  }
-  uint64_t dgamma[VECS][P], dbeta[VECS][P], gamma[kKeep ? VECS : 1][P];
+  // the statistics of the rows to come, one turn ahead
+  float mu_next[R], r_next[R];
+  auto statistics = [&](int ahead) {
 #pragma unroll
-  for (int j = 0; j < VECS; ++j) {
+    for (int k = 0; k < R; ++k) {
+      mu_next[k] = r_next[k] = 0.f;
+      if (w.left > ahead + k) {
+        mu_next[k] = a.mean[w.row + (ahead + k) * w.step];
+        r_next[k] = a.rstd[w.row + (ahead + k) * w.step];
+      }
+    }
+  };
+  statistics(0);
+  uint64_t dgamma[VECS][P], dbeta[VECS][P], gamma[VECS][P];
+#pragma unroll
+  for (int j = 0; j < VECS; ++j)
 #pragma unroll
     for (int i = 0; i < P; ++i) dgamma[j][i] = dbeta[j][i] = 0;
-    if (kKeep) weight_pairs<E, RAGGED>(a.gamma, w.column(j), a.C, a.wdtype, 1.f, gamma[j]);
-  }
-  // dy and z - mean of vector j (columns outside the row: dy = 0)
-  auto gather = [&](int at, int j, float mu, uint64_t (&dy)[P], uint64_t (&d)[P]) {
+  load_weights<VECS, E, RAGGED>(a.gamma, a.C, a.wdtype, 1.f, [&](int j) { return w.column(j); },
+                                gamma);
+  const uint64_t inv_keep = ptx::f2_make(a.drop.inv_keep, a.drop.inv_keep);
+  // dy and z - mean of vector j of the turn's k-th row (dy = 0 outside the row)
+  auto gather = [&](int k, int j, float mu, uint64_t (&dy)[P], uint64_t (&d)[P]) {
     float fd[E], fz[E];
-    w.get(at, 0, j, fd);
-    w.get(at, 1, j, fz);
-    if (RAGGED) {
-      keep_inside<E>(fd, w.column(j), a.C, 0.f);
-      keep_inside<E>(fz, w.column(j), a.C, 0.f);
-    }
-    if (!kKeep) weight_pairs<E, RAGGED>(a.gamma, w.column(j), a.C, a.wdtype, 1.f, gamma[0]);
+    w.get(k, 0, j, fd);
+    w.get(k, 1, j, fz);
     const uint64_t minus_mu = ptx::f2_make(-mu, -mu);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -527,126 +570,75 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
     }
   };
   int parity = 0;
-  // first half of the current row: this thread's s = sum dy gamma and
-  // u = sum dy (z - mean) gamma; rstd comes in behind the sums
-  auto first_half = [&](float& mu, float& r, float& s, float& u) {
-    mu = mu_next;
-    r = r_next;
-    mu_next = r_next = 0.f;
-    if (w.left > 1) {
-      mu_next = a.mean[w.row + w.step];
-      r_next = a.rstd[w.row + w.step];
+  for (int turns = w.turns(a.rows); turns > 0; --turns, w.next()) {
+    float mu[R], r[R], sums[2 * R];  // of row k: sum dy gamma, sum dy (z - mean) gamma
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      mu[k] = mu_next[k];
+      r[k] = r_next[k];
     }
-    w.arrive();
-    const uint64_t r2 = ptx::f2_make(r, r);
-    uint64_t s2 = 0, u2 = 0;
+    statistics(R);
+    w.arrive(2);
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      uint64_t dy[P], d[P];
-      gather(w.take, j, mu, dy, d);
+    for (int k = 0; k < R; ++k) {
+      const uint64_t r2 = ptx::f2_make(r[k], r[k]);
+      uint64_t s2 = 0, u2 = 0;
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const uint64_t t = ptx::f2_mul(dy[i], d[i]);
-        dgamma[j][i] = ptx::f2_fma(t, r2, dgamma[j][i]);
-        dbeta[j][i] = ptx::f2_add(dbeta[j][i], dy[i]);
-        s2 = ptx::f2_fma(dy[i], gamma[kKeep ? j : 0][i], s2);
-        u2 = ptx::f2_fma(t, gamma[kKeep ? j : 0][i], u2);
-      }
-    }
-    s = ptx::f2_lo(s2) + ptx::f2_hi(s2);
-    u = ptx::f2_lo(u2) + ptx::f2_hi(u2);
-    if (kWarps > 1)
-      s = warp_sums(s, u);
-    else
-      lane_sums<kLanes>(s, u);
-  };
-  auto mark = [&]() { return Mark{w.e, w.row, w.take, w.active()}; };
-  auto second_half = [&](const Mark& m, float mu, float r, float s, float u) {
-    // dz = r g - r (r u / C) h - r s / C + dz_in, h = (z - mean) r
-    const float rs = -r * (s * inv_C), ru = -r * (r * u * inv_C);
-    const uint64_t r2 = ptx::f2_make(r, r), rs2 = ptx::f2_make(rs, rs), ru2 = ptx::f2_make(ru, ru);
-    const uint64_t inv_keep = ptx::f2_make(a.drop.inv_keep, a.drop.inv_keep);
-#pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      const int c = w.column(j);
-      uint64_t dy[P], d[P];
-      gather(m.stage, j, mu, dy, d);
-      float f[E];
-      if (DZ) w.get(m.stage, NT - 1, j, f);
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const uint64_t g = ptx::f2_mul(dy[i], gamma[kKeep ? j : 0][i]);
-        dy[i] = ptx::f2_fma(g, r2, ptx::f2_fma(ptx::f2_mul(d[i], r2), ru2, rs2));
-        if (DZ) dy[i] = ptx::f2_add(dy[i], ptx::f2_make(f[2 * i], f[2 * i + 1]));
-        f[2 * i] = ptx::f2_lo(dy[i]);
-        f[2 * i + 1] = ptx::f2_hi(dy[i]);
-      }
-      const bool write = m.active && w.inside(j);
-      if (write) store_row_vec<T, RAGGED>(static_cast<T*>(a.dres) + m.e + w.offset(j), f, c, a.C);
-      if (DROP) {
+      for (int j = 0; j < VECS; ++j) {
+        uint64_t dy[P], d[P];
+        gather(k, j, mu[k], dy, d);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          dy[i] = ptx::f2_mul(dy[i], inv_keep);
+          const uint64_t t = ptx::f2_mul(dy[i], d[i]);
+          dgamma[j][i] = ptx::f2_fma(t, r2, dgamma[j][i]);
+          dbeta[j][i] = ptx::f2_add(dbeta[j][i], dy[i]);
+          s2 = ptx::f2_fma(dy[i], gamma[j][i], s2);
+          u2 = ptx::f2_fma(t, gamma[j][i], u2);
+        }
+      }
+      sums[2 * k] = ptx::f2_lo(s2) + ptx::f2_hi(s2);
+      sums[2 * k + 1] = ptx::f2_lo(u2) + ptx::f2_hi(u2);
+    }
+    row_sums<S, 2 * R>(sums, part[parity]);
+    parity ^= 1;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      // dz = r g - r (r u / C) h - r s / C + dz_in, h = (z - mean) r
+      const float rs = -r[k] * (sums[2 * k] * inv_C);
+      const float ru = -r[k] * (r[k] * sums[2 * k + 1] * inv_C);
+      const uint64_t r2 = ptx::f2_make(r[k], r[k]);
+      const uint64_t rs2 = ptx::f2_make(rs, rs), ru2 = ptx::f2_make(ru, ru);
+#pragma unroll
+      for (int j = 0; j < VECS; ++j) {
+        const int c = w.column(j);
+        const long long e = w.e + k * w.stride + w.offset(j);
+        uint64_t dy[P], d[P];
+        gather(k, j, mu[k], dy, d);
+        float f[E];
+        if (DZ) w.get(k, NT - 1, j, f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const uint64_t g = ptx::f2_mul(dy[i], gamma[j][i]);
+          dy[i] = ptx::f2_fma(g, r2, ptx::f2_fma(ptx::f2_mul(d[i], r2), ru2, rs2));
+          if (DZ) dy[i] = ptx::f2_add(dy[i], ptx::f2_make(f[2 * i], f[2 * i + 1]));
           f[2 * i] = ptx::f2_lo(dy[i]);
           f[2 * i + 1] = ptx::f2_hi(dy[i]);
         }
-        drop_vec<E>(f, m.e + w.offset(j), a.drop);
-      }
-      if ((DROP || a.dx != nullptr) && write)
-        store_row_vec<T, RAGGED>(static_cast<T*>(a.dx) + m.e + w.offset(j), f, c, a.C);
-    }
-  };
-  // hands the warp's sums to the block, and takes all of them back
-  auto give = [&](float s) {
-    if (kWarps > 1) {
-      if ((threadIdx.x & 15) == 0) {
-        float2* p = &part[parity][threadIdx.x / 32 % kWarps];
-        ((threadIdx.x & 16) == 0 ? p->x : p->y) = s;
-      }
-      row_barrier<S>();
-    }
-  };
-  auto take = [&](float& s, float& u) {
-    if (kWarps > 1) {
-      uint64_t v = 0;
+        const bool write = w.active(k) && w.inside(j);
+        if (write) store_row_vec<T, RAGGED>(static_cast<T*>(a.dres) + e, f, c, a.C);
+        if (DROP) {
 #pragma unroll
-      for (int i = 0; i < kWarps; i += 2) {
-        const float4 p = *reinterpret_cast<const float4*>(&part[parity][i]);
-        v = ptx::f2_add(v, ptx::f2_add(ptx::f2_make(p.x, p.y), ptx::f2_make(p.z, p.w)));
+          for (int i = 0; i < P; ++i) {
+            dy[i] = ptx::f2_mul(dy[i], inv_keep);
+            f[2 * i] = ptx::f2_lo(dy[i]);
+            f[2 * i + 1] = ptx::f2_hi(dy[i]);
+          }
+          drop_vec<E>(f, e, a.drop);
+        }
+        if ((DROP || a.dx != nullptr) && write)
+          store_row_vec<T, RAGGED>(static_cast<T*>(a.dx) + e, f, c, a.C);
       }
-      s = ptx::f2_lo(v);
-      u = ptx::f2_hi(v);
-      parity ^= 1;
     }
-  };
-
-  int turns = w.turns(a.rows);
-  float mu = 0.f, r = 0.f, s = 0.f, u = 0.f;
-  if (LAG == 0) {
-    for (; turns > 0; --turns, w.next()) {
-      first_half(mu, r, s, u);
-      give(s);
-      take(s, u);
-      second_half(mark(), mu, r, s, u);
-    }
-  } else if (turns > 0) {
-    first_half(mu, r, s, u);
-    Mark m = mark();
-    give(s);
-    for (w.next(); turns > 1; --turns, w.next()) {
-      float mu1, r1, s1, u1;
-      take(s, u);
-      first_half(mu1, r1, s1, u1);
-      second_half(m, mu, r, s, u);
-      m = mark();
-      mu = mu1;
-      r = r1;
-      s = s1;
-      u = u1;
-      give(s);
-    }
-    take(s, u);
-    second_half(m, mu, r, s, u);
   }
   copy_wait<0>();
   if (a.workspace == nullptr) return;
@@ -867,9 +859,10 @@ int launch_walk(Kernel kern, const Args& a, int smem, long long most,
   return rc != ATTN_OK ? rc : static_cast<int>(grid);
 }
 
-// Stages of a ring whose stage has `bytes`: four, or what `room` has place for.
+// Stages of a ring whose stage has `bytes`: what `room` has place for, in
+// pairs, up to eight.
 constexpr int stages_for(int bytes, int room) {
-  return bytes * 4 <= room ? 4 : (bytes * 3 <= room ? 3 : (bytes * 2 <= room ? 2 : 1));
+  return bytes * 8 <= room ? 8 : bytes * 6 <= room ? 6 : bytes * 4 <= room ? 4 : bytes * 2 <= room ? 2 : 1;
 }
 
 template <typename T, bool ADD, bool DROP, bool RAGGED>
@@ -879,8 +872,8 @@ int fwd_rows(const FwdArgs& a, cudaStream_t stream) {
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
     static std::atomic<int> resident[kMaxTrackedDevices];
     constexpr int kBytes = (ADD ? 2 : 1) * S::VECS * S::BLOCK * 16, 
-                  kStages = stages_for(kBytes, S::BLOCK <= 256 ? 98304 : 196608);
-    const int n = launch_walk<S>(fwd_kernel<T, S, kStages, 1, ADD, DROP, RAGGED>, a, kStages * kBytes,
+                  kStages = stages_for(kBytes, S::BLOCK <= 256 ? 108 * 1024 : 216 * 1024);
+    const int n = launch_walk<S>(fwd_kernel<T, S, kStages, (kStages > 2 ? 2 : 1), ADD, DROP, RAGGED>, a, kStages * kBytes,
                                  1LL << 20, limit_set, resident, stream);
     return n < 0 ? n : static_cast<int>(ATTN_OK);
   });
@@ -910,11 +903,11 @@ int bwd_rows(const BwdArgs& a, cudaStream_t stream) {
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
     static std::atomic<int> resident[kMaxTrackedDevices];
     constexpr int kBytes = (DZ ? 3 : 2) * S::VECS * S::BLOCK * 16;
-    constexpr int kStages = stages_for(kBytes, 196608);
+    constexpr int kStages = stages_for(kBytes, 216 * 1024);
     // the ring's memory also takes the sums of the block's rows of threads
     static_assert(S::ROWS == 1 || kStages * kBytes >= S::BLOCK * S::VECS * Vec<T>::kElems * 8,
                   "ring too small for the sums");
-    return launch_walk<S>(bwd_kernel<T, S, kStages, (kStages > 2 ? 1 : 0), DZ, DROP, RAGGED>, a, kStages * kBytes,
+    return launch_walk<S>(bwd_kernel<T, S, kStages, (kStages > 2 && S::WARPS > 1 ? 2 : 1), DZ, DROP, RAGGED>, a, kStages * kBytes,
                           kMaxChunks, limit_set, resident, stream);
   });
 }
