@@ -19,24 +19,49 @@
 namespace attn {
 namespace norm {
 
-template <int TPR_, int VECS_, int LEAST>
+template <int TPR_, int VECS_, int LEAST, int CTAS_ = 1>
 struct Shape {
-  static constexpr int TPR = TPR_;    // threads per row
+  static constexpr int TPR = TPR_;    // threads of a block per row
   static constexpr int VECS = VECS_;  // 16-byte vectors per thread
+  static constexpr int CTAS = CTAS_;  // blocks (of a cluster) per row
   static constexpr int BLOCK = TPR_ < LEAST ? LEAST : TPR_;
   static constexpr int ROWS = BLOCK / TPR_;  // rows of a block at a time
-  static constexpr int WARPS = TPR_ > 32 ? TPR_ / 32 : 1;  // warps per row
-  static constexpr int LANES = TPR_ > 32 ? 32 : TPR_;      // lanes of a warp per row
+  static constexpr int WARPS = (TPR_ > 32 ? TPR_ / 32 : 1) * CTAS_;  // warps per row
+  static constexpr int LANES = TPR_ > 32 ? 32 : TPR_;  // lanes of a warp per row
+  static_assert(CTAS_ == 1 || BLOCK / TPR_ == 1, "a cluster has one row");
 };
 
 // Barrier over a row's threads (rows of several warps; the block's other rows
 // go on by themselves).
 template <typename S>
 __device__ __forceinline__ void row_barrier() {
-  if (S::ROWS == 1)
+  if (S::CTAS > 1)
+    ptx::cluster_barrier();
+  else if (S::ROWS == 1)
     __syncthreads();
   else
     ptx::named_bar_sync(1 + threadIdx.x / S::TPR, S::TPR);
+}
+// This block's place among those of a row.
+template <typename S>
+__device__ __forceinline__ int row_rank() {
+  return S::CTAS > 1 ? static_cast<int>(ptx::cluster_rank()) : 0;
+}
+// This thread's warp among those of its row.
+template <typename S>
+__device__ __forceinline__ int row_warp() {
+  constexpr int kHere = S::WARPS / S::CTAS;
+  return row_rank<S>() * kHere + threadIdx.x / 32 % kHere;
+}
+// Writes a float of the row's, in the shared memory of each of its blocks.
+template <typename S>
+__device__ __forceinline__ void row_share(float* p, float v) {
+  if (S::CTAS == 1) {
+    *p = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < S::CTAS; ++i) ptx::st_cluster_f32(ptx::smem_u32(p), i, v);
+  }
 }
 
 // The weights (or biases) of a thread's N vectors of E columns, from column
@@ -137,12 +162,13 @@ __device__ __forceinline__ void store_edge(T* p, const Vec<T>& v, int c, int C) 
   }
 }
 
-// Writes the vector's elements that lie in the row.
-template <typename T, bool RAGGED, int E>
-__device__ __forceinline__ void store_row_vec(T* p, const float (&f)[E], int c, int C) {
+// Writes the vector's elements that lie in the row; edge: it reaches over the
+// row's ends.
+template <typename T, int E>
+__device__ __forceinline__ void store_row_vec(T* p, const float (&f)[E], bool edge, int c, int C) {
   Vec<T> v;
   pack(f, v);
-  if (!RAGGED || (c >= 0 && c + E <= C))
+  if (!edge)
     store_vec(p, v);
   else
     store_edge(p, v, c, C);
@@ -176,6 +202,8 @@ struct Walk {
   uint4* ring;        // this thread's slots: [STAGES][NT][VECS], BLOCK apart
   const T* from[NT];  // vector 0 of the next row to copy
   const T* end[NT];   // behind the tensors (RAGGED)
+  bool tail;          // the thread's last row ends the tensors (RAGGED)
+  int edges;          // bits: vectors that reach over the row's ends (RAGGED)
   long long stride;   // elements between this thread's rows
   long long e;        // element of the turn's first row's vector 0
   long long row, step;
@@ -185,14 +213,19 @@ struct Walk {
 
   __device__ __forceinline__ Walk(uint4* smem, const void* const (&src)[NT], long long rows, int C_)
       : ring(smem + threadIdx.x), C(C_), fill(0), take(0) {
-    t = threadIdx.x % S::TPR;
-    row = static_cast<long long>(blockIdx.x) * S::ROWS + threadIdx.x / S::TPR;
-    step = static_cast<long long>(gridDim.x) * S::ROWS;
+    row = static_cast<long long>(blockIdx.x) / S::CTAS * S::ROWS + threadIdx.x / S::TPR;
+    step = static_cast<long long>(gridDim.x) / S::CTAS * S::ROWS;
     shift = RAGGED ? static_cast<int>((row * C) % E) : 0;
+    t = threadIdx.x % S::TPR + row_rank<S>() * (S::TPR * S::VECS);
     e = row * C - shift + t * E;
     stride = step * C;
     left = row < rows ? static_cast<int>((rows - row + step - 1) / step) : 0;
     to_copy = left;
+    tail = RAGGED && left > 0 && row + (left - 1) * step == rows - 1;
+    edges = 0;
+#pragma unroll
+    for (int j = 0; j < S::VECS; ++j)
+      if (RAGGED && inside(j) && (column(j) < 0 || column(j) + E > C)) edges |= 1 << j;
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
       from[q] = static_cast<const T*>(src[q]) + e;
@@ -210,9 +243,7 @@ struct Walk {
   // vector from the row's end, it reaches over the row's ends (RAGGED)
   __device__ __forceinline__ int column(int j) const { return (t + j * S::TPR) * E - shift; }
   __device__ __forceinline__ bool inside(int j) const { return column(j) < C; }
-  __device__ __forceinline__ bool edge(int j) const {
-    return RAGGED && (column(j) < 0 || column(j) + E > C);
-  }
+  __device__ __forceinline__ bool edge(int j) const { return RAGGED && (edges >> j & 1) != 0; }
   // element of vector j, less that of vector 0
   __device__ __forceinline__ static constexpr int offset(int j) { return j * S::TPR * E; }
   // turns to take: for this thread's rows; where several rows share a warp,
@@ -220,7 +251,7 @@ struct Walk {
   __device__ __forceinline__ int turns(long long rows) const {
     int n = left;
     if (S::TPR < 32) {
-      const long long first = static_cast<long long>(blockIdx.x) * S::ROWS;
+      const long long first = static_cast<long long>(blockIdx.x) * S::ROWS;  // (CTAS is 1)
       n = first < rows ? static_cast<int>((rows - first + step - 1) / step) : 0;
     }
     return (n + R - 1) / R;
@@ -240,7 +271,7 @@ struct Walk {
           for (int q = 0; q < NT; ++q) {
             uint4* slot = to + (q * S::VECS + j) * S::BLOCK;
             const T* p = from[q] + offset(j);
-            if (!RAGGED || p + E <= end[q]) {
+            if (!RAGGED || !(tail && to_copy == 1 && edge(j)) || p + E <= end[q]) {
               copy_async16(ptx::smem_u32(slot), p);
             } else {  // the tensor's last vector is no whole one
               T* v = reinterpret_cast<T*>(slot);
@@ -267,7 +298,7 @@ struct Walk {
     copy_wait<kAhead>();
 #pragma unroll
     for (int j = 0; j < S::VECS; ++j) {
-      if (inside(j) && edge(j)) {
+      if (edge(j)) {
         uint32_t m[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int i = 0; i < E; ++i)
@@ -334,9 +365,10 @@ __device__ __forceinline__ void row_sums(float (&v)[R], float* part) {
     for (int i = 0; i < R; ++i) v[i] = lane_sum<S::LANES>(v[i]);
     return;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 % S::WARPS;
+  const int lane = threadIdx.x & 31;
   const float mine = warp_sums<R>(v);
-  if (lane % (32 / R) == 0) part[lane / (32 / R) * S::WARPS + warp] = mine;
+  if (lane % (32 / R) == 0)
+    row_share<S>(part + lane / (32 / R) * S::WARPS + row_warp<S>(), mine);
   row_barrier<S>();
   // a group of lanes adds up each value's parts
   constexpr int kGroup = S::WARPS < 32 / R ? S::WARPS : 32 / R;
@@ -362,9 +394,10 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
   constexpr int kLanes = S::LANES, kWarps = S::WARPS;
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float2 parts[S::ROWS][2][R * kWarps];
-  __shared__ float counts[S::BLOCK / 32];
+  __shared__ float all_counts[S::ROWS][kWarps];
   auto& part = parts[kWarps > 1 ? threadIdx.x / S::TPR : 0];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 % kWarps;  // of the row
+  auto& counts = all_counts[kWarps > 1 ? threadIdx.x / S::TPR : 0];
+  const int lane = threadIdx.x & 31, warp = row_warp<S>();
   const void* src[NT];
   src[0] = a.x;
   if (ADD) src[NT - 1] = a.residual;
@@ -383,8 +416,9 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
   // the parts that a lane joins: of the turn's row lane / kGroup
   constexpr int kGroup = kWarps < 32 / R ? kWarps : 32 / R;
   if (kWarps > 1) {
-    if (lane == 0) counts[threadIdx.x / 32] = count;
-    __syncthreads();
+    if (S::CTAS > 1) ptx::cluster_barrier();  // all of the cluster's blocks have begun
+    if (lane == 0) row_share<S>(&counts[warp], count);
+    row_barrier<S>();
   }
   const uint64_t inv_keep = ptx::f2_make(a.drop.inv_keep, a.drop.inv_keep);
   int parity = 0;
@@ -414,7 +448,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
             f[2 * i + 1] = ptx::f2_hi(v[k][j][i]);
           }
           if (w.active(k) && w.inside(j))
-            store_row_vec<T, RAGGED>(static_cast<T*>(a.z) + e, f, w.column(j), a.C);
+            store_row_vec(static_cast<T*>(a.z) + e, f, w.edge(j), w.column(j), a.C);
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) s2 = ptx::f2_add(s2, v[k][j][i]);
@@ -435,7 +469,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
       uint64_t q2 = 0;
 #pragma unroll
       for (int j = 0; j < VECS; ++j) {
-        if (w.edge(j)) {  // partly, or all, outside: mu in place of its zeros there
+        if (w.edge(j)) {  // partly outside: mu in place of its zeros there
           const int c = w.column(j);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
@@ -445,7 +479,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
                                       hi ? ptx::f2_hi(v[k][j][i]) : mu[k]);
           }
         }
-        const float m = RAGGED || w.inside(j) ? -mu[k] : 0.f;  // outside the row v is 0
+        const float m = w.inside(j) ? -mu[k] : 0.f;  // outside the row v is 0
         const uint64_t minus = ptx::f2_make(m, m);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -461,12 +495,15 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
       float mean = mu[0];  // of the row that this lane's sum belongs to
 #pragma unroll
       for (int k = 1; k < R; ++k) mean = lane / (32 / R) == k ? mu[k] : mean;
-      if (lane % (32 / R) == 0)
-        part[parity][lane / (32 / R) * kWarps + warp] = make_float2(mean, sum);
+      if (lane % (32 / R) == 0) {
+        float2* to = &part[parity][lane / (32 / R) * kWarps + warp];
+        row_share<S>(&to->x, mean);
+        row_share<S>(&to->y, sum);
+      }
       row_barrier<S>();
       // a group of lanes joins each row's parts
       const int first = lane / kGroup % R * kWarps + lane % kGroup;
-      const float* n = &counts[threadIdx.x / 32 - warp + lane % kGroup];
+      const float* n = &counts[lane % kGroup];
       float2 p[kWarps / kGroup];
       float total = 0.f, squares = 0.f;
 #pragma unroll
@@ -506,8 +543,8 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
           f[2 * i + 1] = ptx::f2_hi(o);
         }
         if (w.active(k) && w.inside(j))
-          store_row_vec<T, RAGGED>(static_cast<T*>(a.y) + w.e + k * w.stride + w.offset(j), f,
-                                   w.column(j), a.C);
+          store_row_vec(static_cast<T*>(a.y) + w.e + k * w.stride + w.offset(j), f, w.edge(j),
+                        w.column(j), a.C);
       }
       if (w.active(k) && w.t == 0) {
         if (a.mean != nullptr) a.mean[w.row + k * w.step] = mu[k];
@@ -569,6 +606,7 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
       d[i] = ptx::f2_add(ptx::f2_make(fz[2 * i], fz[2 * i + 1]), minus_mu);
     }
   };
+  if (S::CTAS > 1) ptx::cluster_barrier();  // all of the cluster's blocks have begun
   int parity = 0;
   for (int turns = w.turns(a.rows); turns > 0; --turns, w.next()) {
     float mu[R], r[R], sums[2 * R];  // of row k: sum dy gamma, sum dy (z - mean) gamma
@@ -625,7 +663,7 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
           f[2 * i + 1] = ptx::f2_hi(dy[i]);
         }
         const bool write = w.active(k) && w.inside(j);
-        if (write) store_row_vec<T, RAGGED>(static_cast<T*>(a.dres) + e, f, c, a.C);
+        if (write) store_row_vec(static_cast<T*>(a.dres) + e, f, w.edge(j), c, a.C);
         if (DROP) {
 #pragma unroll
           for (int i = 0; i < P; ++i) {
@@ -636,13 +674,13 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
           drop_vec<E>(f, e, a.drop);
         }
         if ((DROP || a.dx != nullptr) && write)
-          store_row_vec<T, RAGGED>(static_cast<T*>(a.dx) + e, f, c, a.C);
+          store_row_vec(static_cast<T*>(a.dx) + e, f, w.edge(j), c, a.C);
       }
     }
   }
   copy_wait<0>();
   if (a.workspace == nullptr) return;
-  float* out = a.workspace + 2LL * blockIdx.x * a.C;
+  float* out = a.workspace + 2LL * (blockIdx.x / S::CTAS) * a.C;
   // f(column, dgamma, dbeta) for each of this thread's columns
   auto columns = [&](auto f) {
 #pragma unroll
@@ -799,9 +837,11 @@ inline unsigned grid_for(long long want) {
   return static_cast<unsigned>(want < cap ? want : cap);
 }
 
-// f(Shape) for the row length: up to 16 elements a thread (32 for the widest),
-// so that the backward's sums stay in registers; blocks of at least LEAST
-// threads.
+// f(Shape) for the row length: up to 16 elements a thread, so that weights and
+// the backward's sums stay in registers. The widest rows take a cluster of two
+// blocks for it (2048 x 16384 bf16: forward 40 us, backward 67 us; with one
+// block and 32 elements a thread 45 and 72 us, with the weights read again for
+// each row 44 and 97 us). Blocks have at least LEAST threads.
 template <typename T, int LEAST, typename F>
 int with_shape(int C, F f) {
   constexpr int E = Vec<T>::kElems;
@@ -815,7 +855,7 @@ int with_shape(int C, F f) {
   if (n <= 2048) return f(Shape<128, 16 / E, LEAST>{});
   if (n <= 4096) return f(Shape<256, 16 / E, LEAST>{});
   if (n <= 8192) return f(Shape<512, 16 / E, LEAST>{});
-  return f(Shape<512, 32 / E, LEAST>{});
+  return f(Shape<512, 16 / E, LEAST, 2>{});
 }
 
 template <typename T>
@@ -824,39 +864,49 @@ bool fits(int C) {
   return (C % E == 0 ? C : C + 2 * E - 2) <= kMaxRow;
 }
 
-// Blocks of a kernel that fit an SM at a time (cached per device by the
-// caller's record); 0 on error.
-template <typename Kernel>
-int blocks_per_sm(Kernel kern, int block, int smem, std::atomic<int> (&cache)[kMaxTrackedDevices]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  const bool tracked = dev >= 0 && dev < kMaxTrackedDevices;
-  if (tracked) {
-    const int n = cache[dev].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-  }
-  int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, block, smem) != cudaSuccess) return 0;
-  if (tracked) cache[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-// Launches a walking kernel: as many blocks as are resident at a time, in
-// eights, no more than there are rows for or `most`; returns their number or a
-// negative error. The ring takes `smem` bytes.
+// Launches a walking kernel: as many rows' blocks as are resident at a time, in
+// eights, no more than there are rows for or `most`; returns how many rows (of
+// threads) that are, per block of several rows one, or a negative error. The
+// ring takes `smem` bytes. `resident` is the caller's record per device.
 template <typename S, typename Kernel, typename Args>
 int launch_walk(Kernel kern, const Args& a, int smem, long long most,
                 std::atomic<bool> (&limit_set)[kMaxTrackedDevices],
                 std::atomic<int> (&resident)[kMaxTrackedDevices], cudaStream_t stream) {
   if (!set_smem_limit_once(kern, smem, limit_set)) return ATTN_ERR_LAUNCH;
-  const int per_sm = blocks_per_sm(kern, S::BLOCK, smem, resident);
-  if (per_sm <= 0) return ATTN_ERR_LAUNCH;
-  long long grid = static_cast<long long>(sm_count() > 0 ? sm_count() : 1) * per_sm;
-  grid = std::max(8LL, std::min(grid, most) / 8 * 8);
-  grid = std::min(grid, ((a.rows + S::ROWS - 1) / S::ROWS + 7) / 8 * 8);
-  kern<<<static_cast<unsigned>(grid), S::BLOCK, smem, stream>>>(a);
-  const int rc = launch_status();
-  return rc != ATTN_OK ? rc : static_cast<int>(grid);
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = S::CTAS;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(S::CTAS);
+  config.blockDim = dim3(S::BLOCK);
+  config.dynamicSmemBytes = static_cast<size_t>(smem);
+  config.stream = stream;
+  config.attrs = &cluster;
+  config.numAttrs = S::CTAS > 1 ? 1 : 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  const bool tracked = dev >= 0 && dev < kMaxTrackedDevices;
+  int at_once = tracked ? resident[dev].load(std::memory_order_relaxed) : 0;
+  if (at_once <= 0) {
+    if (S::CTAS > 1) {
+      if (cudaOccupancyMaxActiveClusters(&at_once, kern, &config) != cudaSuccess)
+        return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
+    } else {
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&at_once, kern, S::BLOCK, smem) !=
+          cudaSuccess)
+        return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
+      at_once *= sm_count();
+    }
+    if (at_once <= 0) return ATTN_ERR_LAUNCH;
+    if (tracked) resident[dev].store(at_once, std::memory_order_relaxed);
+  }
+  long long n = std::max(8LL, std::min<long long>(at_once, most) / 8 * 8);
+  n = std::min(n, ((a.rows + S::ROWS - 1) / S::ROWS + 7) / 8 * 8);
+  config.gridDim = dim3(static_cast<unsigned>(n * S::CTAS));
+  if (cudaLaunchKernelEx(&config, kern, a) != cudaSuccess)
+    return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
+  return static_cast<int>(n);
 }
 
 // Stages of a ring whose stage has `bytes`: what `room` has place for, in
