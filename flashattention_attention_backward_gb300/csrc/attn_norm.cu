@@ -42,7 +42,7 @@ inline Drop make_drop(float p, unsigned long long seed) {
 template <typename T, bool DROP>
 __global__ void __launch_bounds__(kThreads)
     dropout_add_kernel(const T* x, const T* residual, T* y, long long n, Drop drop) {
-  constexpr int E = Vec<T>::kElems, U = 2;
+  constexpr int E = Vec<T>::kElems, U = 1;
   const long long e0 =
       (static_cast<long long>(blockIdx.x) * (U * kThreads) + threadIdx.x) * E;
   Vec<T> vx[U], vr[U];
@@ -214,7 +214,7 @@ extern "C" int attn_dropout_add(const void* x, const void* residual, void* y, lo
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const T *xt = static_cast<const T*>(x), *rt = static_cast<const T*>(residual);
-    const long long per_block = 2LL * norm::kThreads * Vec<T>::kElems;
+    const long long per_block = 1LL * norm::kThreads * Vec<T>::kElems;
     const unsigned grid = static_cast<unsigned>((n + per_block - 1) / per_block);
     if (drop.on)
       norm::dropout_add_kernel<T, true>

@@ -172,12 +172,17 @@ __device__ __forceinline__ void rotate_heads(const Args& p, const Side& s, int h
         const long long pos = p.positions != nullptr ? p.positions[b * p.pos_stride + n] : n;
         const int first = INTERLEAVED ? ca / 2 : ca;
         const int count = p.half - first < E ? p.half - first : E;
+        const float m = p.magnitude * s.scale, ms = m * p.sign;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          cs[i] = sn[i] = 0.f;
-          if (i < count) angle(pos, p.turns[first + i], cs[i], sn[i]);
-          cs[i] *= p.magnitude * s.scale;
-          sn[i] *= p.magnitude * s.scale * p.sign;
+        for (int i = 0; i < E; i += 2) {  // rot / 2 is even here, first too
+          ulonglong2 f = make_ulonglong2(0, 0);
+          if (i < count) f = *reinterpret_cast<const ulonglong2*>(p.turns + first + i);
+          angle(pos, f.x, cs[i], sn[i]);
+          angle(pos, f.y, cs[i + 1], sn[i + 1]);
+          cs[i] *= m;
+          cs[i + 1] *= m;
+          sn[i] *= ms;
+          sn[i + 1] *= ms;
         }
       }
     }
@@ -232,10 +237,22 @@ template <typename TQ, typename TK, typename TO, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
     rotary_kernel(Args p, int items, int per, int q_groups, long long tokens) {
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const long long token = i / items;
+  long long token, b, n;
+  int item;
+  if (tokens * items <= 0x7fffffffLL) {  // 32-bit divisions take a fifth of the time
+    const uint32_t j = static_cast<uint32_t>(i), t = j / static_cast<uint32_t>(items);
+    const uint32_t q = t / static_cast<uint32_t>(p.N);
+    token = t;
+    item = static_cast<int>(j - t * static_cast<uint32_t>(items));
+    b = q;
+    n = t - q * static_cast<uint32_t>(p.N);
+  } else {
+    token = i / items;
+    item = static_cast<int>(i - token * items);
+    b = token / p.N;
+    n = token - b * p.N;
+  }
   if (token >= tokens) return;
-  const int item = static_cast<int>(i - token * items);
-  const long long b = token / p.N, n = token - b * p.N;
   const int g = blockIdx.y;
   // loads in flight per thread: 128 bytes
   if (g < q_groups) {

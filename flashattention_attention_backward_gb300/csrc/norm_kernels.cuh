@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "norm_common.cuh"
 #include "sm103_ptx.cuh"
@@ -183,6 +184,13 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// How the rows fall to the grid's places for one (blocks times rows of threads
+// a block): `whole` to each, one more to the first `rest`.
+struct Split {
+  int whole;
+  long long rest;
+};
+
 // A block's walk over rows, shared by the two kernels: blocks stay and take
 // rows a grid apart, so that a thread's columns are the same in all of its
 // rows (RAGGED: the grid is a multiple of 8 blocks, so all of a thread's rows
@@ -211,15 +219,16 @@ struct Walk {
   int t, shift, C;
   int fill, take;     // where the stages begin
 
-  __device__ __forceinline__ Walk(uint4* smem, const void* const (&src)[NT], long long rows, int C_)
+  __device__ __forceinline__ Walk(uint4* smem, const void* const (&src)[NT], long long rows, int C_,
+                                  const Split& split)
       : ring(smem + threadIdx.x), C(C_), fill(0), take(0) {
     row = static_cast<long long>(blockIdx.x) / S::CTAS * S::ROWS + threadIdx.x / S::TPR;
     step = static_cast<long long>(gridDim.x) / S::CTAS * S::ROWS;
-    shift = RAGGED ? static_cast<int>((row * C) % E) : 0;
+    shift = RAGGED ? static_cast<int>((row * C) & (E - 1)) : 0;
     t = threadIdx.x % S::TPR + row_rank<S>() * (S::TPR * S::VECS);
     e = row * C - shift + t * E;
     stride = step * C;
-    left = row < rows ? static_cast<int>((rows - row + step - 1) / step) : 0;
+    left = split.whole + (row < split.rest);
     to_copy = left;
     tail = RAGGED && left > 0 && row + (left - 1) * step == rows - 1;
     edges = 0;
@@ -246,15 +255,11 @@ struct Walk {
   __device__ __forceinline__ bool edge(int j) const { return RAGGED && (edges >> j & 1) != 0; }
   // element of vector j, less that of vector 0
   __device__ __forceinline__ static constexpr int offset(int j) { return j * S::TPR * E; }
-  // turns to take: for this thread's rows; where several rows share a warp,
-  // for the most that one of the block's has
-  __device__ __forceinline__ int turns(long long rows) const {
-    int n = left;
-    if (S::TPR < 32) {
-      const long long first = static_cast<long long>(blockIdx.x) * S::ROWS;  // (CTAS is 1)
-      n = first < rows ? static_cast<int>((rows - first + step - 1) / step) : 0;
-    }
-    return (n + R - 1) / R;
+  // rows to take: this thread's; where several rows share a warp, the most
+  // that one of the block's threads has
+  __device__ __forceinline__ int count(const Split& split) const {
+    if (S::TPR >= 32) return left;
+    return split.whole + (static_cast<long long>(blockIdx.x) * S::ROWS < split.rest);
   }
   // whether the turn's k-th row is one
   __device__ __forceinline__ bool active(int k) const {
@@ -290,11 +295,13 @@ struct Walk {
     for (int q = 0; q < NT; ++q) from[q] += stride;
     fill = fill == (STAGES - 1) * kStage ? 0 : fill + kStage;
   }
-  // starts the next copies and waits for the turn's rows; of the first
-  // `trimmed` tensors, what lies outside a row becomes zero
+  // starts the next copies and waits for the turn's N rows (R of them, fewer
+  // in the last turn); of the first `trimmed` tensors, what lies outside a row
+  // becomes zero
+  template <int N>
   __device__ __forceinline__ void arrive(int trimmed) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) copy_next();
+    for (int k = 0; k < N; ++k) copy_next();
     copy_wait<kAhead>();
 #pragma unroll
     for (int j = 0; j < S::VECS; ++j) {
@@ -304,7 +311,7 @@ struct Walk {
         for (int i = 0; i < E; ++i)
           if (static_cast<unsigned>(column(j) + i) < static_cast<unsigned>(C))
             m[i * 4 / E] |= sizeof(T) == 4 ? 0xffffffffu : (i % 2 == 0 ? 0xffffu : 0xffff0000u);
-        for (int k = 0; k < R; ++k)
+        for (int k = 0; k < N; ++k)
           for (int q = 0; q < trimmed; ++q) {
             uint4& v = ring[take + k * kStage + (q * S::VECS + j) * S::BLOCK];
             v = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
@@ -389,7 +396,7 @@ __device__ __forceinline__ void row_sums(float (&v)[R], float* part) {
 // which loses nothing to cancellation and costs one barrier a turn of R rows.
 // ADD: with a residual, and z written.
 template <typename T, typename S, int STAGES, int R, bool ADD, bool DROP, bool RAGGED>
-__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(FwdArgs a) {
+__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(FwdArgs a, Split split) {
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, P = E / 2, NT = ADD ? 2 : 1;
   constexpr int kLanes = S::LANES, kWarps = S::WARPS;
   extern __shared__ __align__(16) uint4 ring[];
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
   const void* src[NT];
   src[0] = a.x;
   if (ADD) src[NT - 1] = a.residual;
-  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.rows, a.C);
+  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.rows, a.C, split);
   const float inv_C = 1.0f / static_cast<float>(a.C);
   uint64_t gamma[VECS][P], beta[VECS][P];
   auto column = [&](int j) { return w.column(j); };
@@ -413,8 +420,6 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
     if (w.inside(j)) mine += RAGGED ? min(w.column(j) + E, a.C) - max(w.column(j), 0) : E;
   const float count = lane_sum<kLanes>(static_cast<float>(mine));  // n_w
   const float inv_count = count > 0.f ? 1.0f / count : 0.f;
-  // the parts that a lane joins: of the turn's row lane / kGroup
-  constexpr int kGroup = kWarps < 32 / R ? kWarps : 32 / R;
   if (kWarps > 1) {
     if (S::CTAS > 1) ptx::cluster_barrier();  // all of the cluster's blocks have begun
     if (lane == 0) row_share<S>(&counts[warp], count);
@@ -422,12 +427,15 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
   }
   const uint64_t inv_keep = ptx::f2_make(a.drop.inv_keep, a.drop.inv_keep);
   int parity = 0;
-  for (int turns = w.turns(a.rows); turns > 0; --turns, w.next()) {
-    w.arrive(NT);
-    uint64_t v[R][VECS][P];
-    float mu[R], q[R];
+  auto turn = [&](auto rows_of_turn) {
+    constexpr int N = decltype(rows_of_turn)::value;
+    // the parts that a lane joins: of the turn's row lane / kGroup
+    constexpr int kGroup = kWarps < 32 / N ? kWarps : 32 / N;
+    w.template arrive<N>(NT);
+    uint64_t v[N][VECS][P];
+    float mu[N], q[N];
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
+    for (int k = 0; k < N; ++k) {
       uint64_t s2 = 0;
 #pragma unroll
       for (int j = 0; j < VECS; ++j) {
@@ -455,17 +463,17 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
       }
       mu[k] = ptx::f2_lo(s2) + ptx::f2_hi(s2);
     }
-    if (kWarps > 1 && R > 1) {
-      const float sum = warp_sums<R>(mu);
+    if (kWarps > 1 && N > 1) {
+      const float sum = warp_sums<N>(mu);
 #pragma unroll
-      for (int k = 0; k < R; ++k)
-        mu[k] = __shfl_sync(0xffffffffu, sum, k * (32 / R)) * inv_count;
+      for (int k = 0; k < N; ++k)
+        mu[k] = __shfl_sync(0xffffffffu, sum, k * (32 / N)) * inv_count;
     } else {
 #pragma unroll
-      for (int k = 0; k < R; ++k) mu[k] = lane_sum<kLanes>(mu[k]) * inv_count;
+      for (int k = 0; k < N; ++k) mu[k] = lane_sum<kLanes>(mu[k]) * inv_count;
     }
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
+    for (int k = 0; k < N; ++k) {
       uint64_t q2 = 0;
 #pragma unroll
       for (int j = 0; j < VECS; ++j) {
@@ -489,20 +497,20 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
       }
       q[k] = ptx::f2_lo(q2) + ptx::f2_hi(q2);
     }
-    float rstd[R];
+    float rstd[N];
     if (kWarps > 1) {
-      const float sum = warp_sums<R>(q);
+      const float sum = warp_sums<N>(q);
       float mean = mu[0];  // of the row that this lane's sum belongs to
 #pragma unroll
-      for (int k = 1; k < R; ++k) mean = lane / (32 / R) == k ? mu[k] : mean;
-      if (lane % (32 / R) == 0) {
-        float2* to = &part[parity][lane / (32 / R) * kWarps + warp];
+      for (int k = 1; k < N; ++k) mean = lane / (32 / N) == k ? mu[k] : mean;
+      if (lane % (32 / N) == 0) {
+        float2* to = &part[parity][lane / (32 / N) * kWarps + warp];
         row_share<S>(&to->x, mean);
         row_share<S>(&to->y, sum);
       }
       row_barrier<S>();
       // a group of lanes joins each row's parts
-      const int first = lane / kGroup % R * kWarps + lane % kGroup;
+      const int first = lane / kGroup % N * kWarps + lane % kGroup;
       const float* n = &counts[lane % kGroup];
       float2 p[kWarps / kGroup];
       float total = 0.f, squares = 0.f;
@@ -520,17 +528,17 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
       squares = lane_sum<kGroup>(squares);
       const float r = rsqrtf(fmaf(squares, inv_C, a.eps));
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        mu[k] = R == 1 ? total : __shfl_sync(0xffffffffu, total, k * kGroup);
-        rstd[k] = R == 1 ? r : __shfl_sync(0xffffffffu, r, k * kGroup);
+      for (int k = 0; k < N; ++k) {
+        mu[k] = N == 1 ? total : __shfl_sync(0xffffffffu, total, k * kGroup);
+        rstd[k] = N == 1 ? r : __shfl_sync(0xffffffffu, r, k * kGroup);
       }
       parity ^= 1;
     } else {
 #pragma unroll
-      for (int k = 0; k < R; ++k) rstd[k] = rsqrtf(fmaf(lane_sum<kLanes>(q[k]), inv_C, a.eps));
+      for (int k = 0; k < N; ++k) rstd[k] = rsqrtf(fmaf(lane_sum<kLanes>(q[k]), inv_C, a.eps));
     }
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
+    for (int k = 0; k < N; ++k) {
       const uint64_t minus_mu = ptx::f2_make(-mu[k], -mu[k]), r2 = ptx::f2_make(rstd[k], rstd[k]);
 #pragma unroll
       for (int j = 0; j < VECS; ++j) {
@@ -551,7 +559,10 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
         if (a.rstd != nullptr) a.rstd[w.row + k * w.step] = rstd[k];
       }
     }
-  }
+  };
+  int count_down = w.count(split);
+  for (; count_down >= R; count_down -= R, w.next()) turn(std::integral_constant<int, R>{});
+  if (R > 1 && count_down > 0) turn(std::integral_constant<int, 1>{});
   copy_wait<0>();
 }
 
@@ -560,7 +571,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
 // thread's rows; then, with the sums joined over the rows' threads, the rows'
 // gradients, from the ring again. DZ: with a dz to add.
 template <typename T, typename S, int STAGES, int R, bool DZ, bool DROP, bool RAGGED>
-__global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a, Split split) {
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, BLOCK = S::BLOCK, P = E / 2;
   constexpr int NT = DZ ? 3 : 2;
   ptx::grid_dependency_launch();  // the second stage's launch, which waits for this grid's end
@@ -571,7 +582,7 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
   src[0] = a.dy;
   src[1] = a.z;
   if (DZ) src[NT - 1] = a.dz;
-  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.rows, a.C);
+  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.rows, a.C, split);
   const float inv_C = 1.0f / static_cast<float>(a.C);
   // the statistics of the rows to come, one turn ahead
   float mu_next[R], r_next[R];
@@ -608,17 +619,18 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
   };
   if (S::CTAS > 1) ptx::cluster_barrier();  // all of the cluster's blocks have begun
   int parity = 0;
-  for (int turns = w.turns(a.rows); turns > 0; --turns, w.next()) {
-    float mu[R], r[R], sums[2 * R];  // of row k: sum dy gamma, sum dy (z - mean) gamma
+  auto turn = [&](auto rows_of_turn) {
+    constexpr int N = decltype(rows_of_turn)::value;
+    float mu[N], r[N], sums[2 * N];  // of row k: sum dy gamma, sum dy (z - mean) gamma
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
+    for (int k = 0; k < N; ++k) {
       mu[k] = mu_next[k];
       r[k] = r_next[k];
     }
     statistics(R);
-    w.arrive(2);
+    w.template arrive<N>(2);
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
+    for (int k = 0; k < N; ++k) {
       const uint64_t r2 = ptx::f2_make(r[k], r[k]);
       uint64_t s2 = 0, u2 = 0;
 #pragma unroll
@@ -637,10 +649,10 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
       sums[2 * k] = ptx::f2_lo(s2) + ptx::f2_hi(s2);
       sums[2 * k + 1] = ptx::f2_lo(u2) + ptx::f2_hi(u2);
     }
-    row_sums<S, 2 * R>(sums, part[parity]);
+    row_sums<S, 2 * N>(sums, part[parity]);
     parity ^= 1;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
+    for (int k = 0; k < N; ++k) {
       // dz = r g - r (r u / C) h - r s / C + dz_in, h = (z - mean) r
       const float rs = -r[k] * (sums[2 * k] * inv_C);
       const float ru = -r[k] * (r[k] * sums[2 * k + 1] * inv_C);
@@ -677,7 +689,10 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a) {
           store_row_vec(static_cast<T*>(a.dx) + e, f, w.edge(j), c, a.C);
       }
     }
-  }
+  };
+  int count_down = w.count(split);
+  for (; count_down >= R; count_down -= R, w.next()) turn(std::integral_constant<int, R>{});
+  if (R > 1 && count_down > 0) turn(std::integral_constant<int, 1>{});
   copy_wait<0>();
   if (a.workspace == nullptr) return;
   float* out = a.workspace + 2LL * (blockIdx.x / S::CTAS) * a.C;
@@ -904,7 +919,8 @@ int launch_walk(Kernel kern, const Args& a, int smem, long long most,
   long long n = std::max(8LL, std::min<long long>(at_once, most) / 8 * 8);
   n = std::min(n, ((a.rows + S::ROWS - 1) / S::ROWS + 7) / 8 * 8);
   config.gridDim = dim3(static_cast<unsigned>(n * S::CTAS));
-  if (cudaLaunchKernelEx(&config, kern, a) != cudaSuccess)
+  const Split split{static_cast<int>(a.rows / (n * S::ROWS)), a.rows % (n * S::ROWS)};
+  if (cudaLaunchKernelEx(&config, kern, a, split) != cudaSuccess)
     return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
   return static_cast<int>(n);
 }
