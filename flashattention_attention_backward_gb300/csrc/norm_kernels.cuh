@@ -78,12 +78,21 @@ __device__ __forceinline__ void load_weights(const void* p, int C, int wdtype, f
     for (int i = 0; i < E; ++i)
       f[j][i] = static_cast<unsigned>(c(j) + i) < static_cast<unsigned>(C) ? fill : 0.f;
   if (p != nullptr && RAGGED) {
+    auto take = [&](auto t) {
+      using W = decltype(t);
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+      for (int j = 0; j < N; ++j)
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (static_cast<unsigned>(c(j) + i) < static_cast<unsigned>(C))
-          f[j][i] = load_as(p, c(j) + i, wdtype);
+        for (int i = 0; i < E; ++i)
+          if (static_cast<unsigned>(c(j) + i) < static_cast<unsigned>(C))
+            f[j][i] = to_f32(static_cast<const W*>(p)[c(j) + i]);
+    };
+    if (wdtype == ATTN_FP32)
+      take(float{});
+    else if (wdtype == ATTN_BF16)
+      take(__nv_bfloat16{});
+    else
+      take(__half{});
   } else if (p != nullptr && wdtype == ATTN_FP32) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -399,6 +408,8 @@ template <typename T, typename S, int STAGES, int R, bool ADD, bool DROP, bool R
 __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(FwdArgs a, Split split) {
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, P = E / 2, NT = ADD ? 2 : 1;
   constexpr int kLanes = S::LANES, kWarps = S::WARPS;
+  // a block behind the last row (the grid comes in eights)
+  if (split.whole == 0 && blockIdx.x / S::CTAS * S::ROWS >= split.rest) return;
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float2 parts[S::ROWS][2][R * kWarps];
   __shared__ float all_counts[S::ROWS][kWarps];
@@ -575,6 +586,8 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a, Split split) {
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, BLOCK = S::BLOCK, P = E / 2;
   constexpr int NT = DZ ? 3 : 2;
   ptx::grid_dependency_launch();  // the second stage's launch, which waits for this grid's end
+  // a block behind the last row (the grid comes in eights)
+  if (split.whole == 0 && blockIdx.x / S::CTAS * S::ROWS >= split.rest) return;
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float parts[S::ROWS][2][2 * R * S::WARPS];
   auto& part = parts[S::WARPS > 1 ? threadIdx.x / S::TPR : 0];
@@ -695,41 +708,46 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a, Split split) {
   if (R > 1 && count_down > 0) turn(std::integral_constant<int, 1>{});
   copy_wait<0>();
   if (a.workspace == nullptr) return;
-  float* out = a.workspace + 2LL * (blockIdx.x / S::CTAS) * a.C;
-  // f(column, dgamma, dbeta) for each of this thread's columns
-  auto columns = [&](auto f) {
+  // This thread's sums go side by side with those of the block's other rows of
+  // threads to the ring's memory, where each column is added up over them in
+  // order; straight to the workspace where there is one row of threads.
+  float* const out = a.workspace + 2LL * (blockIdx.x / S::CTAS) * a.C;
+  float* const sums = reinterpret_cast<float*>(ring);
+  float* const own = S::ROWS == 1 ? out : sums + threadIdx.x / S::TPR * 2 * a.C;
+  if (S::ROWS > 1) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      const int c = w.column(j);
-      if (c >= a.C) continue;
+  for (int j = 0; j < VECS; ++j) {
+    const int c = w.column(j);
+    if (c >= a.C) continue;
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (RAGGED && static_cast<unsigned>(c + i) >= static_cast<unsigned>(a.C)) continue;
-        f(c + i, i % 2 == 0 ? ptx::f2_lo(dgamma[j][i / 2]) : ptx::f2_hi(dgamma[j][i / 2]),
-          i % 2 == 0 ? ptx::f2_lo(dbeta[j][i / 2]) : ptx::f2_hi(dbeta[j][i / 2]));
+    for (int half = 0; half < 2; ++half) {
+      const uint64_t(&v)[P] = half == 0 ? dgamma[j] : dbeta[j];
+      float* const to = own + half * a.C + c;
+      if (!RAGGED) {  // columns and C are multiples of four
+#pragma unroll
+        for (int i = 0; i < P; i += 2)
+          *reinterpret_cast<float4*>(to + 2 * i) =
+              make_float4(ptx::f2_lo(v[i]), ptx::f2_hi(v[i]), ptx::f2_lo(v[i + 1]),
+                          ptx::f2_hi(v[i + 1]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (static_cast<unsigned>(c + i) < static_cast<unsigned>(a.C))
+            to[i] = i % 2 == 0 ? ptx::f2_lo(v[i / 2]) : ptx::f2_hi(v[i / 2]);
       }
     }
-  };
-  if (S::ROWS == 1) {
-    columns([&](int c, float x, float y) {
-      out[c] = x;
-      out[a.C + c] = y;
-    });
-  } else {
-    // the block's rows of threads leave theirs side by side in the ring's
-    // memory, and each column is added up over them in order
-    float* sums = reinterpret_cast<float*>(ring);
-    float* own = sums + threadIdx.x / S::TPR * 2 * a.C;
-    __syncthreads();
-    columns([&](int c, float x, float y) {
-      own[c] = x;
-      own[a.C + c] = y;
-    });
+  }
+  if (S::ROWS > 1) {
+    // rows of threads that had rows
+    const int n = split.whole > 0
+                      ? S::ROWS
+                      : static_cast<int>(min(static_cast<long long>(S::ROWS),
+                                             split.rest - static_cast<long long>(blockIdx.x) * S::ROWS));
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * a.C; i += BLOCK) {
       float v = 0.f;
 #pragma unroll 8
-      for (int k = 0; k < S::ROWS; ++k) v += sums[k * 2 * a.C + i];
+      for (int k = 0; k < n; ++k) v += sums[k * 2 * a.C + i];
       out[i] = v;
     }
   }
@@ -880,9 +898,9 @@ bool fits(int C) {
 }
 
 // Launches a walking kernel: as many rows' blocks as are resident at a time, in
-// eights, no more than there are rows for or `most`; returns how many rows (of
-// threads) that are, per block of several rows one, or a negative error. The
-// ring takes `smem` bytes. `resident` is the caller's record per device.
+// eights, no more than there are rows for or `most`; returns the number of
+// blocks (clusters, for rows of several blocks) that get rows, or a negative
+// error. The ring takes `smem` bytes. `resident` is the caller's record per device.
 template <typename S, typename Kernel, typename Args>
 int launch_walk(Kernel kern, const Args& a, int smem, long long most,
                 std::atomic<bool> (&limit_set)[kMaxTrackedDevices],
@@ -922,7 +940,7 @@ int launch_walk(Kernel kern, const Args& a, int smem, long long most,
   const Split split{static_cast<int>(a.rows / (n * S::ROWS)), a.rows % (n * S::ROWS)};
   if (cudaLaunchKernelEx(&config, kern, a, split) != cudaSuccess)
     return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
-  return static_cast<int>(n);
+  return static_cast<int>(std::min(n, (a.rows + S::ROWS - 1) / S::ROWS));
 }
 
 // Stages of a ring whose stage has `bytes`: what `room` has place for, in
