@@ -67,10 +67,13 @@ __device__ __forceinline__ void row_share(float* p, float v) {
 
 // The weights (or biases) of a thread's N vectors of E columns, from column
 // c(j) on, in fp32 pairs: `fill` where there is no array, 0 outside the row.
-// All loads go out before any is used.
-template <int N, int E, bool RAGGED, typename F>
+// All loads go out before any is used. RAGGED: the columns lie at no vector's
+// place, and a thread's own one by one would take as many requests as elements
+// with a few bytes of each line; the lanes of a row (LANES of them) read them
+// side by side and pass them on through `stage` (32 E floats of the warp's).
+template <int N, int E, bool RAGGED, int LANES, typename F>
 __device__ __forceinline__ void load_weights(const void* p, int C, int wdtype, float fill, F c,
-                                             uint64_t (&g)[N][E / 2]) {
+                                             float* stage, uint64_t (&g)[N][E / 2]) {
   float f[N][E];
 #pragma unroll
   for (int j = 0; j < N; ++j)
@@ -78,21 +81,41 @@ __device__ __forceinline__ void load_weights(const void* p, int C, int wdtype, f
     for (int i = 0; i < E; ++i)
       f[j][i] = static_cast<unsigned>(c(j) + i) < static_cast<unsigned>(C) ? fill : 0.f;
   if (p != nullptr && RAGGED) {
-    auto take = [&](auto t) {
-      using W = decltype(t);
+    const int lane = threadIdx.x & 31, t = lane % LANES;
+    auto load = [&](auto w) {
+      using W = decltype(w);
 #pragma unroll
       for (int j = 0; j < N; ++j)
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (static_cast<unsigned>(c(j) + i) < static_cast<unsigned>(C))
-            f[j][i] = to_f32(static_cast<const W*>(p)[c(j) + i]);
+        for (int i = 0; i < E; ++i) {
+          const int col = c(j) - t * E + i * LANES + t;
+          f[j][i] = static_cast<unsigned>(col) < static_cast<unsigned>(C)
+                        ? to_f32(static_cast<const W*>(p)[col])
+                        : 0.f;
+        }
     };
     if (wdtype == ATTN_FP32)
-      take(float{});
+      load(float{});
     else if (wdtype == ATTN_BF16)
-      take(__nv_bfloat16{});
+      load(__nv_bfloat16{});
     else
-      take(__half{});
+      load(__half{});
+    float* const at = stage + lane / LANES * LANES * E;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) at[i * LANES + t] = f[j][i];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < E; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(at + t * E + i);
+        f[j][i] = v.x;
+        f[j][i + 1] = v.y;
+        f[j][i + 2] = v.z;
+        f[j][i + 3] = v.w;
+      }
+      __syncwarp();
+    }
   } else if (p != nullptr && wdtype == ATTN_FP32) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -422,9 +445,11 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(
   Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.rows, a.C, split);
   const float inv_C = 1.0f / static_cast<float>(a.C);
   uint64_t gamma[VECS][P], beta[VECS][P];
+  __shared__ __align__(16) float stages[RAGGED ? S::BLOCK / 32 : 1][32 * E];
+  float* const stage = stages[RAGGED ? threadIdx.x / 32 : 0];
   auto column = [&](int j) { return w.column(j); };
-  load_weights<VECS, E, RAGGED>(a.gamma, a.C, a.wdtype, 1.f, column, gamma);
-  load_weights<VECS, E, RAGGED>(a.beta, a.C, a.wdtype, 0.f, column, beta);
+  load_weights<VECS, E, RAGGED, kLanes>(a.gamma, a.C, a.wdtype, 1.f, column, stage, gamma);
+  load_weights<VECS, E, RAGGED, kLanes>(a.beta, a.C, a.wdtype, 0.f, column, stage, beta);
   int mine = 0;  // this thread's columns inside the row
 #pragma unroll
   for (int j = 0; j < VECS; ++j)
@@ -615,8 +640,10 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a, Split split) {
   for (int j = 0; j < VECS; ++j)
 #pragma unroll
     for (int i = 0; i < P; ++i) dgamma[j][i] = dbeta[j][i] = 0;
-  load_weights<VECS, E, RAGGED>(a.gamma, a.C, a.wdtype, 1.f, [&](int j) { return w.column(j); },
-                                gamma);
+  __shared__ __align__(16) float stages[RAGGED ? S::BLOCK / 32 : 1][32 * E];
+  load_weights<VECS, E, RAGGED, S::LANES>(
+      a.gamma, a.C, a.wdtype, 1.f, [&](int j) { return w.column(j); },
+      stages[RAGGED ? threadIdx.x / 32 : 0], gamma);
   const uint64_t inv_keep = ptx::f2_make(a.drop.inv_keep, a.drop.inv_keep);
   // dy and z - mean of vector j of the turn's k-th row (dy = 0 outside the row)
   auto gather = [&](int k, int j, float mu, uint64_t (&dy)[P], uint64_t (&d)[P]) {
@@ -710,11 +737,16 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a, Split split) {
   if (a.workspace == nullptr) return;
   // This thread's sums go side by side with those of the block's other rows of
   // threads to the ring's memory, where each column is added up over them in
-  // order; straight to the workspace where there is one row of threads.
+  // order; straight to the workspace where there is one row of threads. RAGGED:
+  // a thread's columns are at no vector's place and go one by one, a word of
+  // distance behind every eight so that the lanes' banks differ.
   float* const out = a.workspace + 2LL * (blockIdx.x / S::CTAS) * a.C;
   float* const sums = reinterpret_cast<float*>(ring);
-  float* const own = S::ROWS == 1 ? out : sums + threadIdx.x / S::TPR * 2 * a.C;
-  if (S::ROWS > 1) __syncthreads();
+  constexpr bool kGather = S::ROWS > 1 || (RAGGED && S::CTAS == 1);
+  auto place = [](int i) { return RAGGED && kGather ? i + (i >> 3) : i; };
+  const int size = place(2 * a.C);
+  float* const own = kGather ? sums + threadIdx.x / S::TPR * size : out;
+  if (kGather) __syncthreads();
 #pragma unroll
   for (int j = 0; j < VECS; ++j) {
     const int c = w.column(j);
@@ -722,33 +754,45 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a, Split split) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const uint64_t(&v)[P] = half == 0 ? dgamma[j] : dbeta[j];
-      float* const to = own + half * a.C + c;
+      const int first = half * a.C + c;
       if (!RAGGED) {  // columns and C are multiples of four
 #pragma unroll
         for (int i = 0; i < P; i += 2)
-          *reinterpret_cast<float4*>(to + 2 * i) =
+          *reinterpret_cast<float4*>(own + first + 2 * i) =
               make_float4(ptx::f2_lo(v[i]), ptx::f2_hi(v[i]), ptx::f2_lo(v[i + 1]),
                           ptx::f2_hi(v[i + 1]));
       } else {
 #pragma unroll
         for (int i = 0; i < E; ++i)
           if (static_cast<unsigned>(c + i) < static_cast<unsigned>(a.C))
-            to[i] = i % 2 == 0 ? ptx::f2_lo(v[i / 2]) : ptx::f2_hi(v[i / 2]);
+            own[place(first + i)] = i % 2 == 0 ? ptx::f2_lo(v[i / 2]) : ptx::f2_hi(v[i / 2]);
       }
     }
   }
-  if (S::ROWS > 1) {
+  if (kGather) {
     // rows of threads that had rows
     const int n = split.whole > 0
                       ? S::ROWS
                       : static_cast<int>(min(static_cast<long long>(S::ROWS),
                                              split.rest - static_cast<long long>(blockIdx.x) * S::ROWS));
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.C; i += BLOCK) {
-      float v = 0.f;
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) v += sums[k * 2 * a.C + i];
-      out[i] = v;
+    if (!RAGGED) {
+      for (int i = threadIdx.x; i < a.C / 2; i += BLOCK) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+          const float4 x = *reinterpret_cast<const float4*>(sums + k * size + 4 * i);
+          v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+        }
+        *reinterpret_cast<float4*>(out + 4 * i) = v;
+      }
+    } else {
+      for (int i = threadIdx.x; i < 2 * a.C; i += BLOCK) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) v += sums[k * size + place(i)];
+        out[i] = v;
+      }
     }
   }
 }
@@ -956,7 +1000,7 @@ int fwd_rows(const FwdArgs& a, cudaStream_t stream) {
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
     static std::atomic<int> resident[kMaxTrackedDevices];
     constexpr int kBytes = (ADD ? 2 : 1) * S::VECS * S::BLOCK * 16, 
-                  kStages = stages_for(kBytes, S::BLOCK <= 256 ? 108 * 1024 : 216 * 1024);
+                  kStages = stages_for(kBytes, (S::BLOCK <= 256 ? 104 : 208) * 1024);
     const int n = launch_walk<S>(fwd_kernel<T, S, kStages, (kStages > 2 ? 2 : 1), ADD, DROP, RAGGED>, a, kStages * kBytes,
                                  1LL << 20, limit_set, resident, stream);
     return n < 0 ? n : static_cast<int>(ATTN_OK);
@@ -987,9 +1031,9 @@ int bwd_rows(const BwdArgs& a, cudaStream_t stream) {
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
     static std::atomic<int> resident[kMaxTrackedDevices];
     constexpr int kBytes = (DZ ? 3 : 2) * S::VECS * S::BLOCK * 16;
-    constexpr int kStages = stages_for(kBytes, 216 * 1024);
+    constexpr int kStages = stages_for(kBytes, 208 * 1024);
     // the ring's memory also takes the sums of the block's rows of threads
-    static_assert(S::ROWS == 1 || kStages * kBytes >= S::BLOCK * S::VECS * Vec<T>::kElems * 8,
+    static_assert(kStages * kBytes >= S::BLOCK * S::VECS * Vec<T>::kElems * 9,
                   "ring too small for the sums");
     return launch_walk<S>(bwd_kernel<T, S, kStages, (kStages > 2 && S::WARPS > 1 ? 2 : 1), DZ, DROP, RAGGED>, a, kStages * kBytes,
                           kMaxChunks, limit_set, resident, stream);
