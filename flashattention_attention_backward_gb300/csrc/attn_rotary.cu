@@ -128,25 +128,32 @@ struct Group {
   }
 };
 
-// One thread keeps the cosines and sines of E column pairs of one token (two
-// 16-byte groups: the pairs' two halves, or two neighbouring groups where
-// interleaved) and takes them through `per` heads, U heads' loads in flight
-// at a time. The angles cost about as much as four heads' arithmetic, the
-// loads and stores are what bounds it.
+// One thread keeps the cosines and sines of E column pairs of one token and
+// takes them through `per` heads, U heads' loads in flight at a time: of two
+// 16-byte groups a row, the pairs' two halves (half layout), or two groups
+// apart of the turning columns (interleaved) or of the copied ones. Neighbour
+// lanes have neighbour groups, so that requests are whole sectors (with two
+// neighbouring groups a lane the interleaved d = 64 case took 14.8 us, not
+// 14.0). The angles cost about as much as four heads' arithmetic; the loads
+// and stores are what bounds it: B=2 H=32 H_kv=8 N=4096 d=128 bf16 takes 27.8
+// us for 168 MB (6.0 TB/s), the finalize step of that shape 36.5 us for 235 MB
+// (6.4 TB/s).
 template <typename TI, typename TO, int U, bool INTERLEAVED>
 __device__ __forceinline__ void rotate_heads(const Args& p, const Side& s, int h0, int h1,
                                              long long b, long long n, int item) {
   constexpr int E = Vec<TO>::kElems;
-  const int turning = INTERLEAVED ? 0 : p.half / E;  // items that turn (half layout)
   int ca, cb;
   bool turn_a, turn_b;
+  const int turning = INTERLEAVED ? 0 : p.half / E;  // items that turn (half layout)
   if (!INTERLEAVED && item < turning) {
     ca = item * E;
     cb = ca + p.half;
     turn_a = turn_b = true;
   } else {
-    ca = (INTERLEAVED ? 0 : 2 * p.half) + (item - turning) * 2 * E;
-    cb = ca + E;
+    const int start = INTERLEAVED ? 0 : 2 * p.half;  // groups from here on, two an item
+    const int items = ((p.d - start) / E + 1) / 2;
+    ca = start + (item - turning) * E;
+    cb = ca + items * E;
     turn_a = ca < 2 * p.half;
     turn_b = cb < 2 * p.half;
   }
@@ -170,13 +177,13 @@ __device__ __forceinline__ void rotate_heads(const Args& p, const Side& s, int h
       ready = true;
       if (turn_a) {
         const long long pos = p.positions != nullptr ? p.positions[b * p.pos_stride + n] : n;
-        const int first = INTERLEAVED ? ca / 2 : ca;
-        const int count = p.half - first < E ? p.half - first : E;
         const float m = p.magnitude * s.scale, ms = m * p.sign;
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {  // rot / 2 is even here, first too
+        for (int i = 0; i < E; i += 2) {  // pairs come in twos: so does rot / 2 here
+          // interleaved: the first E / 2 pairs are those of group a
+          const int pair = !INTERLEAVED ? ca + i : i < E / 2 ? ca / 2 + i : cb / 2 + i - E / 2;
           ulonglong2 f = make_ulonglong2(0, 0);
-          if (i < count) f = *reinterpret_cast<const ulonglong2*>(p.turns + first + i);
+          if (pair < p.half) f = *reinterpret_cast<const ulonglong2*>(p.turns + pair);
           angle(pos, f.x, cs[i], sn[i]);
           angle(pos, f.y, cs[i + 1], sn[i + 1]);
           cs[i] *= m;
