@@ -36,65 +36,61 @@ inline Drop make_drop(float p, unsigned long long seed) {
   return d;
 }
 
-// A thread takes two 16-byte groups a block apart: their loads are in flight
-// together, and the mask words (a generator call per 4 elements) are drawn
-// behind them.
+// A thread takes 16 bytes: both loads go out first, the mask words (a
+// generator call per 4 elements) are drawn behind them, and only then are the
+// loads waited for (with their elements widened before, 8192 x 4096 bf16 with a
+// residual took 48 us, not 32: 6.3 TB/s). Two groups a thread measured the
+// same. Without a residual the generator's multiplies bound it: a call has 19
+// of 32 x 32 to 64 bits, which issue every fourth cycle, and the kernel draws
+// 1.1e12 words a second of the 1.6e12 of a loop that does nothing else.
+constexpr int kDropThreads = 128;
+
 template <typename T, bool DROP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kDropThreads)
     dropout_add_kernel(const T* x, const T* residual, T* y, long long n, Drop drop) {
-  constexpr int E = Vec<T>::kElems, U = 1;
-  const long long e0 =
-      (static_cast<long long>(blockIdx.x) * (U * kThreads) + threadIdx.x) * E;
-  Vec<T> vx[U], vr[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long e = e0 + u * kThreads * E;
-    if (e + E <= n) {
-      vx[u] = load_vec(x + e);
-      if (residual != nullptr) vr[u] = load_vec(residual + e);
-    }
+  constexpr int E = Vec<T>::kElems;
+  const long long e = (static_cast<long long>(blockIdx.x) * kDropThreads + threadIdx.x) * E;
+  if (e >= n) return;
+  const bool whole = e + E <= n, add = residual != nullptr;
+  Vec<T> vx, vr;
+  if (whole) {
+    vx = load_vec(x + e);
+    if (add) vr = load_vec(residual + e);
   }
-  uint32_t w[U * E / 4][4];
+  uint32_t w[E / 4][4];
   if (DROP) {
-    long long first[U * E / 4];
+    long long first[E / 4];
 #pragma unroll
-    for (int u = 0; u < U * E / 4; ++u)
-      first[u] = (e0 + (u / (E / 4)) * (kThreads * E)) | (4 * (u % (E / 4)));
-    keep_words<U * E / 4>(first, drop, w);
+    for (int u = 0; u < E / 4; ++u) first[u] = e | (4 * u);
+    keep_words<E / 4>(first, drop, w);
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long e = e0 + u * kThreads * E;
-    if (e >= n) continue;
-    const bool whole = e + E <= n;
-    float v[E], r[E];
-    if (whole) {
-      unpack(vx[u], v);
-      if (residual != nullptr) unpack(vr[u], r);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        v[i] = e + i < n ? to_f32(x[e + i]) : 0.f;
-        r[i] = residual != nullptr && e + i < n ? to_f32(residual[e + i]) : 0.f;
-      }
-    }
+  float v[E], r[E];
+  if (whole) {
+    unpack(vx, v);
+    if (add) unpack(vr, r);
+  } else {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      if (DROP) v[i] = w[u * E / 4 + i / 4][i % 4] >= drop.threshold ? v[i] : 0.f;
-      if (residual != nullptr)
-        v[i] = DROP ? fmaf(v[i], drop.inv_keep, r[i]) : v[i] + r[i];
-      else if (DROP)
-        v[i] *= drop.inv_keep;
+      v[i] = e + i < n ? to_f32(x[e + i]) : 0.f;
+      r[i] = add && e + i < n ? to_f32(residual[e + i]) : 0.f;
     }
-    if (whole) {
-      Vec<T> o;
-      pack(v, o);
-      store_vec(y + e, o);
-    } else {
+  }
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (e + i < n) y[e + i] = from_f32<T>(v[i]);
-    }
+  for (int i = 0; i < E; ++i) {
+    if (DROP) v[i] = w[i / 4][i % 4] >= drop.threshold ? v[i] : 0.f;
+    if (add)
+      v[i] = DROP ? fmaf(v[i], drop.inv_keep, r[i]) : v[i] + r[i];
+    else if (DROP)
+      v[i] *= drop.inv_keep;
+  }
+  if (whole) {
+    Vec<T> o;
+    pack(v, o);
+    store_vec(y + e, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (e + i < n) y[e + i] = from_f32<T>(v[i]);
   }
 }
 
@@ -132,7 +128,7 @@ __global__ void __launch_bounds__(1024) weights_sum_kernel(BwdArgs a, int chunks
 int check(long long rows, int C, int dtype, int wdtype) {
   if (rows < 0 || C <= 0) return ATTN_ERR_SHAPE;
   if (!known_dtype(dtype) || !known_dtype(wdtype)) return ATTN_ERR_UNSUPPORTED;
-  if (rows >= (1LL << 40) / C) return ATTN_ERR_TOO_LARGE;
+  if (C > (1 << 29) || rows >= (1LL << 40) / C) return ATTN_ERR_TOO_LARGE;
   return ATTN_OK;
 }
 
@@ -214,14 +210,14 @@ extern "C" int attn_dropout_add(const void* x, const void* residual, void* y, lo
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const T *xt = static_cast<const T*>(x), *rt = static_cast<const T*>(residual);
-    const long long per_block = 1LL * norm::kThreads * Vec<T>::kElems;
+    const long long per_block = static_cast<long long>(norm::kDropThreads) * Vec<T>::kElems;
     const unsigned grid = static_cast<unsigned>((n + per_block - 1) / per_block);
     if (drop.on)
       norm::dropout_add_kernel<T, true>
-          <<<grid, norm::kThreads, 0, as_stream(stream)>>>(xt, rt, static_cast<T*>(y), n, drop);
+          <<<grid, norm::kDropThreads, 0, as_stream(stream)>>>(xt, rt, static_cast<T*>(y), n, drop);
     else
       norm::dropout_add_kernel<T, false>
-          <<<grid, norm::kThreads, 0, as_stream(stream)>>>(xt, rt, static_cast<T*>(y), n, drop);
+          <<<grid, norm::kDropThreads, 0, as_stream(stream)>>>(xt, rt, static_cast<T*>(y), n, drop);
     return launch_status();
   });
 }

@@ -281,7 +281,8 @@ bool whole_groups(const Args& a) {
   if (a.d % E != 0 || (a.interleaved ? 2 * a.half : a.half) % E != 0) return false;
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 3; ++j)
-      if (a.side[i].heads > 0 && (a.side[i].in_stride[j] % E != 0 || a.side[i].out_stride[j] % E != 0))
+      if (a.side[i].heads > 0 &&
+          (a.side[i].in_stride[j] % E != 0 || a.side[i].out_stride[j] % E != 0))
         return false;
   return true;
 }
@@ -305,10 +306,9 @@ int launch(const Args& a, cudaStream_t stream) {
   if (blocks > 0x7fffffffLL) return ATTN_ERR_TOO_LARGE;
   // heads per thread: as many as leave every SM a few blocks
   int per = 8;
-  while (per > 1 && blocks * ((a.side[0].heads + per - 1) / per + (a.side[1].heads + per - 1) / per) <
-                        sms * 8LL)
-    per /= 2;
-  const int qg = (a.side[0].heads + per - 1) / per, kg = (a.side[1].heads + per - 1) / per;
+  auto groups = [&](int i) { return (a.side[i].heads + per - 1) / per; };
+  while (per > 1 && blocks * (groups(0) + groups(1)) < sms * 8LL) per /= 2;
+  const int qg = groups(0), kg = groups(1);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(qg + kg));
   if (a.interleaved)
     rotary_kernel<TQ, TK, TO, true><<<grid, kThreads, 0, stream>>>(a, items, per, qg, tokens);
@@ -317,8 +317,7 @@ int launch(const Args& a, cudaStream_t stream) {
   return launch_status();
 }
 
-// Checks shared by the two calls; fills the geometry. contiguous(i) strides
-// where `strides` is NULL.
+// Checks shared by the two calls.
 int check_geometry(const void* turns, const void* positions, long long pos_stride, int B, int H,
                    int H_kv, int N, int d, int rot, float magnitude) {
   if (B < 0 || H < 0 || H_kv < 0 || N < 0 || d <= 0 || rot < 0 || rot > d || rot % 2 != 0 ||
@@ -335,23 +334,24 @@ int check_geometry(const void* turns, const void* positions, long long pos_strid
 }
 
 // Strides of one tensor: given ones (non-negative, the last element's offset
-// below 2^40) or those of a contiguous [B, heads, N, d].
-int set_strides(long long (&to)[3], const long long* from, int B, int heads, int N, int d) {
-  if (from == nullptr) {
-    to[0] = static_cast<long long>(heads) * N * d;
-    to[1] = static_cast<long long>(N) * d;
-    to[2] = d;
-    return ATTN_OK;
-  }
+// below 2^40; an output's not 0, where elements would share a place) or those
+// of a contiguous [B, heads, N, d]. A dimension of one element has stride 0.
+int set_strides(long long (&to)[3], const long long* from, bool output, int B, int heads, int N,
+                int d) {
+  const long long dense[3] = {static_cast<long long>(heads) * N * d,
+                              static_cast<long long>(N) * d, d};
   const long long count[3] = {B, heads, N};
+  const bool empty = B == 0 || heads == 0 || N == 0;
   long long last = d;
   for (int i = 0; i < 3; ++i) {
-    if (from[i] < 0) return ATTN_ERR_SHAPE;
+    const long long s = from != nullptr ? from[i] : dense[i];
+    if (s < 0 || (output && s == 0 && count[i] > 1 && !empty)) return ATTN_ERR_SHAPE;
+    to[i] = 0;
     if (count[i] > 1) {
-      if (from[i] >= (1LL << 40) / (count[i] - 1)) return ATTN_ERR_TOO_LARGE;
-      last += from[i] * (count[i] - 1);
+      if (s >= (1LL << 40) / (count[i] - 1)) return ATTN_ERR_TOO_LARGE;
+      last += s * (count[i] - 1);
+      to[i] = s;
     }
-    to[i] = from[i];
   }
   return last >= (1LL << 40) ? ATTN_ERR_TOO_LARGE : ATTN_OK;
 }
@@ -387,7 +387,8 @@ extern "C" int attn_rotary_frequencies(unsigned long long* turns, float* magnitu
     // w <= 1 radian, so the fraction stays below 2^62
     turns[i] = static_cast<unsigned long long>(std::nearbyint(w / two_pi * 18446744073709551616.0));
   }
-  *magnitude = scaling == ATTN_ROTARY_RAMP ? static_cast<float>(1.0 + 0.1 * std::log(factor)) : 1.0f;
+  *magnitude =
+      scaling == ATTN_ROTARY_RAMP ? static_cast<float>(1.0 + 0.1 * std::log(factor)) : 1.0f;
   return ATTN_OK;
 }
 
@@ -412,11 +413,11 @@ extern "C" int attn_rotary(const void* q, const void* k, void* q_out, void* k_ou
     a.side[i].out = out[i];
     a.side[i].heads = heads[i];
     a.side[i].scale = 1.0f;
-    rc = rotary::set_strides(a.side[i].in_stride, strides ? strides + 3 * i : nullptr, B, heads[i],
-                             N, d);
-    if (rc != ATTN_OK) return rc;
-    rc = rotary::set_strides(a.side[i].out_stride, strides ? strides + 6 + 3 * i : nullptr, B,
+    rc = rotary::set_strides(a.side[i].in_stride, strides ? strides + 3 * i : nullptr, false, B,
                              heads[i], N, d);
+    if (rc != ATTN_OK) return rc;
+    rc = rotary::set_strides(a.side[i].out_stride, strides ? strides + 6 + 3 * i : nullptr, true,
+                             B, heads[i], N, d);
     if (rc != ATTN_OK) return rc;
   }
   a.turns = turns;
@@ -457,8 +458,9 @@ extern "C" int attn_bwd_finalize_rotary(const float* dq_accum, void* dq, const v
     a.side[i].out = out[i];
     a.side[i].heads = heads[i];
     a.side[i].scale = i == 0 ? scale : 1.0f;
-    rotary::set_strides(a.side[i].in_stride, nullptr, B, heads[i], N, d);
-    rc = rotary::set_strides(a.side[i].out_stride, strides ? strides + 3 * i : nullptr, B,
+    rc = rotary::set_strides(a.side[i].in_stride, nullptr, false, B, heads[i], N, d);
+    if (rc != ATTN_OK) return rc;
+    rc = rotary::set_strides(a.side[i].out_stride, strides ? strides + 3 * i : nullptr, true, B,
                              heads[i], N, d);
     if (rc != ATTN_OK) return rc;
   }

@@ -145,7 +145,8 @@ __device__ __forceinline__ void load_weights(const void* p, int C, int wdtype, f
       for (int i = 0; i < E / 2; ++i) {
         const uint32_t w = i % 2 == 0 ? v[j][i / 2].x : v[j][i / 2].y;
         const float2 h = wdtype == ATTN_BF16
-                             ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+                             ? make_float2(__uint_as_float(w << 16),
+                                           __uint_as_float(w & 0xffff0000u))
                              : __half22float2(*reinterpret_cast<const __half2*>(&w));
         f[j][2 * i] = h.x;
         f[j][2 * i + 1] = h.y;
@@ -176,13 +177,17 @@ __device__ __forceinline__ void store_edge(T* p, const Vec<T>& v, int c, int C) 
   const int n = start ? E + c : C - c;  // elements in the row
   uint32_t* const q = reinterpret_cast<uint32_t*>(p);
   if (E == 4) {
-    if (n & 2) *reinterpret_cast<uint2*>(q + (start ? 2 : 0)) = start ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
+    if (n & 2)
+      *reinterpret_cast<uint2*>(q + (start ? 2 : 0)) =
+          start ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
     if (n & 1) {
       const int i = start ? 4 - n : n - 1;
       q[i] = i < 2 ? (i == 0 ? w[0] : w[1]) : (i == 2 ? w[2] : w[3]);
     }
   } else {
-    if (n & 4) *reinterpret_cast<uint2*>(q + (start ? 2 : 0)) = start ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
+    if (n & 4)
+      *reinterpret_cast<uint2*>(q + (start ? 2 : 0)) =
+          start ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
     if (n & 2) {
       const int i = start ? (n & 4 ? 1 : 3) : (n & 4 ? 2 : 0);
       q[i] = i < 2 ? (i == 0 ? w[0] : w[1]) : (i == 2 ? w[2] : w[3]);
@@ -210,7 +215,9 @@ __device__ __forceinline__ void store_row_vec(T* p, const float (&f)[E], bool ed
 __device__ __forceinline__ void copy_async16(uint32_t smem, const void* global) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(global) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -242,7 +249,8 @@ struct Walk {
   uint4* ring;        // this thread's slots: [STAGES][NT][VECS], BLOCK apart
   const T* from[NT];  // vector 0 of the next row to copy
   const T* end[NT];   // behind the tensors (RAGGED)
-  bool tail;          // the thread's last row ends the tensors (RAGGED)
+  bool tail;          // the thread's last row is at the tensors' end (RAGGED; the one
+                      // before it, at least eight rows earlier, is not)
   int edges;          // bits: vectors that reach over the row's ends (RAGGED)
   long long stride;   // elements between this thread's rows
   long long e;        // element of the turn's first row's vector 0
@@ -262,7 +270,9 @@ struct Walk {
     stride = step * C;
     left = split.whole + (row < split.rest);
     to_copy = left;
-    tail = RAGGED && left > 0 && row + (left - 1) * step == rows - 1;
+    // a row's last vector ends less than E elements behind the row; that is
+    // within the tensor unless fewer than E elements follow the row
+    tail = RAGGED && left > 0 && (rows - 1 - (row + (left - 1) * step)) * C < E;
     edges = 0;
 #pragma unroll
     for (int j = 0; j < S::VECS; ++j)
@@ -310,7 +320,7 @@ struct Walk {
             const T* p = from[q] + offset(j);
             if (!RAGGED || !(tail && to_copy == 1 && edge(j)) || p + E <= end[q]) {
               copy_async16(ptx::smem_u32(slot), p);
-            } else {  // the tensor's last vector is no whole one
+            } else {  // the tensor ends inside the vector
               T* v = reinterpret_cast<T*>(slot);
               for (int i = 0; i < E; ++i) v[i] = p + i < end[q] ? p[i] : from_f32<T>(0.f);
             }
@@ -428,7 +438,8 @@ __device__ __forceinline__ void row_sums(float (&v)[R], float* part) {
 // which loses nothing to cancellation and costs one barrier a turn of R rows.
 // ADD: with a residual, and z written.
 template <typename T, typename S, int STAGES, int R, bool ADD, bool DROP, bool RAGGED>
-__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1) fwd_kernel(FwdArgs a, Split split) {
+__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
+    fwd_kernel(FwdArgs a, Split split) {
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, P = E / 2, NT = ADD ? 2 : 1;
   constexpr int kLanes = S::LANES, kWarps = S::WARPS;
   // a block behind the last row (the grid comes in eights)
@@ -771,10 +782,10 @@ __global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a, Split split) {
   }
   if (kGather) {
     // rows of threads that had rows
-    const int n = split.whole > 0
+    const long long first = static_cast<long long>(blockIdx.x) * S::ROWS;
+    const int n = split.whole > 0 || split.rest - first > S::ROWS
                       ? S::ROWS
-                      : static_cast<int>(min(static_cast<long long>(S::ROWS),
-                                             split.rest - static_cast<long long>(blockIdx.x) * S::ROWS));
+                      : static_cast<int>(split.rest - first);
     __syncthreads();
     if (!RAGGED) {
       for (int i = threadIdx.x; i < a.C / 2; i += BLOCK) {
@@ -883,7 +894,8 @@ __global__ void __launch_bounds__(kThreads) bwd_wide_kernel(BwdArgs a) {
 
 // Weight gradients of wide rows: 32 columns by a chunk of rows.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) weights_wide_kernel(BwdArgs a, long long rows_per_chunk) {
+__global__ void __launch_bounds__(kThreads)
+    weights_wide_kernel(BwdArgs a, long long rows_per_chunk) {
   __shared__ float part[2][8][32];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
@@ -893,7 +905,8 @@ __global__ void __launch_bounds__(kThreads) weights_wide_kernel(BwdArgs a, long 
   if (c < a.C) {
     for (long long row = first + ty; row < last; row += 8) {
       const float g = to_f32(static_cast<const T*>(a.dy)[row * a.C + c]);
-      const float h = (to_f32(static_cast<const T*>(a.z)[row * a.C + c]) - a.mean[row]) * a.rstd[row];
+      const float z = to_f32(static_cast<const T*>(a.z)[row * a.C + c]);
+      const float h = (z - a.mean[row]) * a.rstd[row];
       s += g;
       t = fmaf(g, h, t);
     }
@@ -990,7 +1003,8 @@ int launch_walk(Kernel kern, const Args& a, int smem, long long most,
 // Stages of a ring whose stage has `bytes`: what `room` has place for, in
 // pairs, up to eight.
 constexpr int stages_for(int bytes, int room) {
-  return bytes * 8 <= room ? 8 : bytes * 6 <= room ? 6 : bytes * 4 <= room ? 4 : bytes * 2 <= room ? 2 : 1;
+  const int n = room / bytes;
+  return n >= 8 ? 8 : n >= 6 ? 6 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
 }
 
 template <typename T, bool ADD, bool DROP, bool RAGGED>
@@ -999,10 +1013,11 @@ int fwd_rows(const FwdArgs& a, cudaStream_t stream) {
     using S = decltype(shape);
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
     static std::atomic<int> resident[kMaxTrackedDevices];
-    constexpr int kBytes = (ADD ? 2 : 1) * S::VECS * S::BLOCK * 16, 
-                  kStages = stages_for(kBytes, (S::BLOCK <= 256 ? 104 : 208) * 1024);
-    const int n = launch_walk<S>(fwd_kernel<T, S, kStages, (kStages > 2 ? 2 : 1), ADD, DROP, RAGGED>, a, kStages * kBytes,
-                                 1LL << 20, limit_set, resident, stream);
+    constexpr int kBytes = (ADD ? 2 : 1) * S::VECS * S::BLOCK * 16;
+    constexpr int kStages = stages_for(kBytes, (S::BLOCK <= 256 ? 104 : 208) * 1024);
+    constexpr int kRows = kStages > 2 ? 2 : 1;
+    const int n = launch_walk<S>(fwd_kernel<T, S, kStages, kRows, ADD, DROP, RAGGED>, a,
+                                 kStages * kBytes, 1LL << 20, limit_set, resident, stream);
     return n < 0 ? n : static_cast<int>(ATTN_OK);
   });
 }
@@ -1035,7 +1050,9 @@ int bwd_rows(const BwdArgs& a, cudaStream_t stream) {
     // the ring's memory also takes the sums of the block's rows of threads
     static_assert(kStages * kBytes >= S::BLOCK * S::VECS * Vec<T>::kElems * 9,
                   "ring too small for the sums");
-    return launch_walk<S>(bwd_kernel<T, S, kStages, (kStages > 2 && S::WARPS > 1 ? 2 : 1), DZ, DROP, RAGGED>, a, kStages * kBytes,
+    // rows within a warp have no barrier to share, and two a turn spill
+    constexpr int kRows = kStages > 2 && S::WARPS > 1 ? 2 : 1;
+    return launch_walk<S>(bwd_kernel<T, S, kStages, kRows, DZ, DROP, RAGGED>, a, kStages * kBytes,
                           kMaxChunks, limit_set, resident, stream);
   });
 }

@@ -165,6 +165,20 @@ def _stream_of(stream, device):
     return stream if stream is not None else torch.cuda.current_stream(device)
 
 
+def _made_for(stream, device, *tensors):
+    """Tells torch's allocator that tensors which it made on the current
+    stream are used on the caller's, so that it does not hand their memory
+    out again before that work is done."""
+    if stream is None:
+        return
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream != torch.cuda.current_stream(device):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _check_cuda(device, **tensors):
     for name, t in tensors.items():
         if t is not None and (t.device != device or t.device.type != "cuda"):
@@ -238,6 +252,7 @@ def rotary(q, k, plan, positions=None, adjoint=False, out=None, stream=None):
         if d > 1 and (x.stride(3) != 1 or y.stride(3) != 1):
             raise ValueError("rows must be contiguous")
     _check_cuda(q.device, q=q, k=k, q_out=out[0], k_out=out[1])
+    _made_for(stream, q.device, *out)
     positions, pos_stride = _check_rotary(plan, positions, B, N, d, q.device)
     parts = [q, q if k is None else k, out[0], out[0] if k is None else out[1]]
     strides = [v for t in parts for v in t.stride()[:3]]
@@ -282,6 +297,7 @@ def layer_norm(x, gamma=None, beta=None, eps=1e-5, stream=None):
     rows, C, code, wcode = _norm_dims(x, gamma, beta)
     y = torch.empty_like(x)
     mean, rstd = _row_stats(x)
+    _made_for(stream, x.device, y, mean, rstd)
     with torch.cuda.device(x.device):
         check(attn_layer_norm(x, gamma, beta, y, mean, rstd, rows, C, eps, code, wcode,
                               _stream_of(stream, x.device)))
@@ -318,6 +334,7 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, weight_grads=True, stream=None
     _check_stats(x, mean, rstd)
     dx = torch.empty_like(x)
     dgamma, dbeta, workspace = _weight_grads(x, gamma, weight_grads, rows, C, x.dtype)
+    _made_for(stream, x.device, dx, dgamma, dbeta, workspace)
     with torch.cuda.device(x.device):
         check(attn_layer_norm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, rows, C,
                                   code, wcode, _stream_of(stream, x.device)))
@@ -332,6 +349,7 @@ def dropout_add(x, residual=None, dropout=(0.0, 0), stream=None):
     _check_like(x, x=x, residual=residual)
     _check_cuda(x.device, x=x, residual=residual)
     y = torch.empty_like(x)
+    _made_for(stream, x.device, y)
     with torch.cuda.device(x.device):
         check(attn_dropout_add(x, residual, y, x.numel(), dropout[0], dropout[1],
                                _DTYPES[x.dtype], _stream_of(stream, x.device)))
@@ -346,6 +364,7 @@ def dropout_add_norm(x, residual, gamma=None, beta=None, eps=1e-5, dropout=(0.0,
     _check_cuda(x.device, residual=residual)
     z, y = torch.empty_like(x), torch.empty_like(x)
     mean, rstd = _row_stats(x)
+    _made_for(stream, x.device, z, y, mean, rstd)
     with torch.cuda.device(x.device):
         check(attn_dropout_add_norm(x, residual, gamma, beta, z, y, mean, rstd, rows, C, eps,
                                     dropout[0], dropout[1], code, wcode,
@@ -365,6 +384,7 @@ def dropout_add_norm_backward(dy, dz, z, gamma, mean, rstd, dropout=(0.0, 0), we
     dres = torch.empty_like(z)
     dx = torch.empty_like(z) if dropout[0] != 0 else None
     dgamma, dbeta, workspace = _weight_grads(z, gamma, weight_grads, rows, C, z.dtype)
+    _made_for(stream, z.device, dx, dres, dgamma, dbeta, workspace)
     with torch.cuda.device(z.device):
         check(attn_dropout_add_norm_bwd(dy, dz, z, gamma, mean, rstd, dx, dres, dgamma, dbeta,
                                         workspace, rows, C, dropout[0], dropout[1], code, wcode,

@@ -281,8 +281,9 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  *   ATTN_ROTARY_LINEAR  w_i / factor (positions interpolated; Chen et al.,
  *                       "Extending context window of large language models
  *                       via positional interpolation", 2023);
- *   ATTN_ROTARY_BASE    base := base * factor^(rot / (rot - 2)): the highest
- *                       frequency stays, the lowest is divided by factor;
+ *   ATTN_ROTARY_BASE    base := base * factor^(rot / (rot - 2)) (rot > 2): the
+ *                       highest frequency stays, the lowest is divided by
+ *                       factor;
  *   ATTN_ROTARY_RAMP    w_i keeps its value where it makes high_turns turns
  *                       or more over original_length positions, is divided
  *                       by factor below low_turns turns, and goes over
@@ -315,7 +316,8 @@ int attn_rotary_frequencies(unsigned long long* turns, float* magnitude, int rot
  * strides: HOST array of 12 element strides, (batch, head, row) of q, k,
  *      q_out and k_out; NULL: all contiguous. They let q and k be parts of a
  *      packed [B, N, H + 2 H_kv, d] projection. A row's d elements are
- *      contiguous. Outputs must not overlap each other; q_out may be q (k_out
+ *      contiguous. Strides are >= 0, and > 0 for the outputs (but for
+ *      dimensions of one element). Outputs must not overlap each other; q_out may be q (k_out
  *      k) with the same strides, otherwise outputs must not overlap inputs.
  * H_kv = 0 leaves k out (k, k_out may be NULL), H = 0 leaves q out. H need
  * not be a multiple of H_kv. 0 <= rot <= d, rot even; rot = 0 copies (turns
@@ -352,7 +354,7 @@ int attn_bwd_finalize_rotary(const float* dq_accum, void* dq, const void* dk, vo
  * In:  x [rows, C] dtype; gamma, beta [C] wdtype (either may be NULL: 1, 0).
  * Out: y [rows, C] dtype (may be x); mean, rstd [rows] fp32 (mu and r, which
  *      the backward reads; either may be NULL).
- * C >= 1, eps >= 0. Rows of heads ([B,H,N,d] with C = d) and of hidden
+ * 1 <= C <= 2^29, eps >= 0. Rows of heads ([B,H,N,d] with C = d) and of hidden
  * states are the same to it.
  */
 int attn_layer_norm(const void* x, const void* gamma, const void* beta, void* y, float* mean,

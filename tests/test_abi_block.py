@@ -68,7 +68,9 @@ def test_rotary_refusals(lib):
     assert call(positions=FAKE + 4) == lib.ATTN_ERR_ALIGN
     for kw in (dict(B=-1), dict(H=-1), dict(H_kv=-1), dict(N=-1), dict(d=0), dict(rot=-2),
                dict(rot=63), dict(rot=66), dict(pos_stride=-1), dict(magnitude=NAN),
-               dict(strides=[0] * 11 + [-1])):
+               dict(strides=[0] * 11 + [-1]),
+               # inputs may be broadcast, outputs not
+               dict(strides=[0] * 12), dict(strides=[0] * 6 + [1024, 512, 64, 512, 64, 0])):
         assert call(**kw) == lib.ATTN_ERR_SHAPE, kw
     assert call(dtype=3) == call(dtype=-1) == lib.ATTN_ERR_UNSUPPORTED
     assert call(N=1 << 30, B=1 << 11) == lib.ATTN_ERR_TOO_LARGE
@@ -92,7 +94,7 @@ def test_finalize_rotary_refusals(lib):
         assert call(**{name: 0}) == lib.ATTN_ERR_NULL, name
         assert call(**{name: FAKE + 8}) == lib.ATTN_ERR_ALIGN, name
     for kw in (dict(B=-1), dict(rot=63), dict(rot=66), dict(scale=NAN), dict(scale=INF),
-               dict(strides=[-1] * 6)):
+               dict(strides=[-1] * 6), dict(strides=[0] * 6)):
         assert call(**kw) == lib.ATTN_ERR_SHAPE, kw
     assert call(B=0) == call(N=0) == lib.ATTN_OK
 
@@ -118,7 +120,8 @@ def test_layer_norm_refusals(lib):
             assert call(**{name: FAKE + 4}) == lib.ATTN_ERR_ALIGN, name
         assert call(rows=-1) == call(C=0) == call(C=-5) == lib.ATTN_ERR_SHAPE
         assert call(dtype=3) == call(wdtype=-1) == lib.ATTN_ERR_UNSUPPORTED
-        assert call(rows=1 << 40) == call(rows=1 << 30, C=1 << 20) == lib.ATTN_ERR_TOO_LARGE
+        assert call(rows=1 << 40) == call(rows=1 << 30, C=1 << 20) == \
+            call(rows=1, C=(1 << 29) + 1) == lib.ATTN_ERR_TOO_LARGE
     assert fwd(eps=-1.0) == fwd(eps=NAN) == fwd(eps=INF) == lib.ATTN_ERR_SHAPE
     assert fwd(rows=0, x=0, y=0, mean=0, rstd=0) == lib.ATTN_OK
     assert bwd(rows=0, dgamma=0, dbeta=0, workspace=0, dy=0, x=0, dx=0) == lib.ATTN_OK
