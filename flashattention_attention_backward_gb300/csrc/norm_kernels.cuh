@@ -618,7 +618,8 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
 // thread's rows; then, with the sums joined over the rows' threads, the rows'
 // gradients, from the ring again. DZ: with a dz to add.
 template <typename T, typename S, int STAGES, int R, bool DZ, bool DROP, bool RAGGED>
-__global__ void __launch_bounds__(S::BLOCK) bwd_kernel(BwdArgs a, Split split) {
+__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 3 : 1)
+    bwd_kernel(BwdArgs a, Split split) {
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, BLOCK = S::BLOCK, P = E / 2;
   constexpr int NT = DZ ? 3 : 2;
   ptx::grid_dependency_launch();  // the second stage's launch, which waits for this grid's end
@@ -932,13 +933,16 @@ inline unsigned grid_for(long long want) {
 // blocks for it (2048 x 16384 bf16: forward 40 us, backward 67 us; with one
 // block and 32 elements a thread 45 and 72 us, with the weights read again for
 // each row 44 and 97 us). Blocks have at least LEAST threads.
-template <typename T, int LEAST, typename F>
+template <typename T, int LEAST, bool BACKWARD, typename F>
 int with_shape(int C, F f) {
   constexpr int E = Vec<T>::kElems;
   // a ragged row takes up to one vector more than its length needs
   const int n = C % E == 0 ? C : C + 2 * E - 2;
-  if (n <= 64) return f(Shape<8, 8 / E, LEAST>{});
-  if (n <= 128) return f(Shape<8, 16 / E, LEAST>{});
+  // short rows of the backward: small blocks, three an SM (524288 x 64 bf16 36
+  // us against 47 with 512 threads, 262144 x 128 36 against 38; from 256 columns
+  // on the same or slower)
+  if (n <= 64) return f(Shape<8, 8 / E, 256>{});
+  if (n <= 128) return f(Shape<BACKWARD ? 16 : 8, (BACKWARD ? 8 : 16) / E, 256>{});
   if (n <= 256) return f(Shape<16, 16 / E, LEAST>{});
   if (n <= 512) return f(Shape<32, 16 / E, LEAST>{});
   if (n <= 1024) return f(Shape<64, 16 / E, LEAST>{});
@@ -1009,7 +1013,7 @@ constexpr int stages_for(int bytes, int room) {
 
 template <typename T, bool ADD, bool DROP, bool RAGGED>
 int fwd_rows(const FwdArgs& a, cudaStream_t stream) {
-  return with_shape<T, 256>(a.C, [&](auto shape) {
+  return with_shape<T, 256, false>(a.C, [&](auto shape) {
     using S = decltype(shape);
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
     static std::atomic<int> resident[kMaxTrackedDevices];
@@ -1040,18 +1044,19 @@ int run_fwd(const FwdArgs& a, cudaStream_t stream) {
 
 template <typename T, bool DZ, bool DROP, bool RAGGED>
 int bwd_rows(const BwdArgs& a, cudaStream_t stream) {
-  // one block of 512 threads an SM: one partial sum a column each
-  return with_shape<T, 512>(a.C, [&](auto shape) {
+  // rows of more than 128 columns: one block of 512 threads an SM, so one
+  // partial sum a column each
+  return with_shape<T, 512, true>(a.C, [&](auto shape) {
     using S = decltype(shape);
     static std::atomic<bool> limit_set[kMaxTrackedDevices];
     static std::atomic<int> resident[kMaxTrackedDevices];
     constexpr int kBytes = (DZ ? 3 : 2) * S::VECS * S::BLOCK * 16;
-    constexpr int kStages = stages_for(kBytes, 208 * 1024);
+    constexpr int kStages = stages_for(kBytes, (S::BLOCK <= 256 ? 72 : 208) * 1024);
     // the ring's memory also takes the sums of the block's rows of threads
     static_assert(kStages * kBytes >= S::BLOCK * S::VECS * Vec<T>::kElems * 9,
                   "ring too small for the sums");
-    // rows within a warp have no barrier to share, and two a turn spill
-    constexpr int kRows = kStages > 2 && S::WARPS > 1 ? 2 : 1;
+    // (with 16 elements a thread, two rows of a warp's own a turn spill)
+    constexpr int kRows = kStages > 2 && (S::WARPS > 1 || S::BLOCK <= 256) ? 2 : 1;
     return launch_walk<S>(bwd_kernel<T, S, kStages, kRows, DZ, DROP, RAGGED>, a, kStages * kBytes,
                           kMaxChunks, limit_set, resident, stream);
   });
