@@ -1274,7 +1274,7 @@ extern "C" const char* attn_strerror(int code) {
     case ATTN_OK: return "success";
     case ATTN_ERR_NULL: return "a required pointer is NULL";
     case ATTN_ERR_SHAPE: return "invalid shape or scalar argument";
-    case ATTN_ERR_UNSUPPORTED: return "unsupported head dimension or element type";
+    case ATTN_ERR_UNSUPPORTED: return "unsupported head dimension";
     case ATTN_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case ATTN_ERR_LAUNCH: return "CUDA launch or runtime error";
     case ATTN_ERR_DEVICE_TIMEOUT: return "a kernel timed out waiting on a barrier";

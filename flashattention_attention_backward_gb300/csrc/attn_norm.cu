@@ -18,8 +18,8 @@
 #include <cmath>
 #include <cstdint>
 
+#include "grid_ptx.cuh"
 #include "norm_common.cuh"
-#include "sm103_ptx.cuh"
 
 namespace attn {
 namespace norm {
@@ -126,8 +126,7 @@ __global__ void __launch_bounds__(1024) weights_sum_kernel(BwdArgs a, int chunks
 }
 
 int check(long long rows, int C, int dtype, int wdtype) {
-  if (rows < 0 || C <= 0) return ATTN_ERR_SHAPE;
-  if (!known_dtype(dtype) || !known_dtype(wdtype)) return ATTN_ERR_UNSUPPORTED;
+  if (rows < 0 || C <= 0 || !known_dtype(dtype) || !known_dtype(wdtype)) return ATTN_ERR_SHAPE;
   if (C > (1 << 29) || rows >= (1LL << 40) / C) return ATTN_ERR_TOO_LARGE;
   return ATTN_OK;
 }
@@ -201,8 +200,7 @@ extern "C" int attn_layer_norm(const void* x, const void* gamma, const void* bet
 extern "C" int attn_dropout_add(const void* x, const void* residual, void* y, long long n,
                                 float p_drop, unsigned long long seed, int dtype, void* stream) {
   if (n > 0 && (!x || !y)) return ATTN_ERR_NULL;
-  if (n < 0 || norm::bad_p(p_drop)) return ATTN_ERR_SHAPE;
-  if (!known_dtype(dtype)) return ATTN_ERR_UNSUPPORTED;
+  if (n < 0 || norm::bad_p(p_drop) || !known_dtype(dtype)) return ATTN_ERR_SHAPE;
   if (n >= (1LL << 40)) return ATTN_ERR_TOO_LARGE;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(y)) return ATTN_ERR_ALIGN;
   if (n == 0) return ATTN_OK;

@@ -366,7 +366,7 @@ extern "C" int attn_rotary_frequencies(unsigned long long* turns, float* magnitu
                                        int original_length, double low_turns, double high_turns) {
   if (!turns || !magnitude) return ATTN_ERR_NULL;
   if (rot < 0 || rot % 2 != 0 || !std::isfinite(base) || base < 1.0) return ATTN_ERR_SHAPE;
-  if (scaling < ATTN_ROTARY_PLAIN || scaling > ATTN_ROTARY_RAMP) return ATTN_ERR_UNSUPPORTED;
+  if (scaling < ATTN_ROTARY_PLAIN || scaling > ATTN_ROTARY_RAMP) return ATTN_ERR_SHAPE;
   if (scaling != ATTN_ROTARY_PLAIN && (!std::isfinite(factor) || factor < 1.0))
     return ATTN_ERR_SHAPE;
   if (scaling == ATTN_ROTARY_RAMP &&
@@ -401,7 +401,7 @@ extern "C" int attn_rotary(const void* q, const void* k, void* q_out, void* k_ou
     return ATTN_ERR_NULL;
   int rc = rotary::check_geometry(turns, positions, pos_stride, B, H, H_kv, N, d, rot, magnitude);
   if (rc != ATTN_OK) return rc;
-  if (!known_dtype(dtype)) return ATTN_ERR_UNSUPPORTED;
+  if (!known_dtype(dtype)) return ATTN_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
     return ATTN_ERR_ALIGN;
   rotary::Args a{};

@@ -14,8 +14,8 @@
 #include <atomic>
 #include <type_traits>
 
+#include "grid_ptx.cuh"
 #include "norm_common.cuh"
-#include "sm103_ptx.cuh"
 
 namespace attn {
 namespace norm {

@@ -55,7 +55,7 @@ extern "C" {
 #define ATTN_OK 0
 #define ATTN_ERR_NULL (-1)           /* a required pointer is NULL */
 #define ATTN_ERR_SHAPE (-2)          /* negative size, H % H_kv != 0, bad scale ... */
-#define ATTN_ERR_UNSUPPORTED (-3)    /* head dimension or element type not supported */
+#define ATTN_ERR_UNSUPPORTED (-3)    /* head dimension not supported by this call */
 #define ATTN_ERR_ALIGN (-4)          /* a pointer is not 16-byte aligned */
 #define ATTN_ERR_LAUNCH (-5)         /* CUDA reported an error at launch */
 #define ATTN_ERR_DEVICE_TIMEOUT (-6) /* a kernel gave up waiting (device status) */
@@ -265,7 +265,7 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  * norm, and dropout with a residual. They take bf16, fp16 or fp32 elements
  * (`dtype`; norm weights, biases and their gradients have a type of their
  * own, `wdtype`; row statistics are fp32), compute in fp32 and round each
- * output once. An unknown type code returns ATTN_ERR_UNSUPPORTED. Pointers of
+ * output once. An unknown type code returns ATTN_ERR_SHAPE. Pointers of
  * an empty problem (no rows) may be NULL.
  */
 #define ATTN_BF16 0

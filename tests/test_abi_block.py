@@ -40,7 +40,7 @@ def test_frequencies_refusals(lib):
     f = lib.attn_rotary_frequencies
     assert f(63)[0] == f(-2)[0] == lib.ATTN_ERR_SHAPE
     assert f(64, 0.5)[0] == f(64, NAN)[0] == f(64, INF)[0] == lib.ATTN_ERR_SHAPE
-    assert f(64, 1e4, 4)[0] == f(64, 1e4, -1)[0] == lib.ATTN_ERR_UNSUPPORTED
+    assert f(64, 1e4, 4)[0] == f(64, 1e4, -1)[0] == lib.ATTN_ERR_SHAPE
     for code in (1, 2, 3):
         assert f(64, 1e4, code, 0.5, 4096)[0] == f(64, 1e4, code, NAN, 4096)[0] == \
             lib.ATTN_ERR_SHAPE
@@ -72,7 +72,7 @@ def test_rotary_refusals(lib):
                # inputs may be broadcast, outputs not
                dict(strides=[0] * 12), dict(strides=[0] * 6 + [1024, 512, 64, 512, 64, 0])):
         assert call(**kw) == lib.ATTN_ERR_SHAPE, kw
-    assert call(dtype=3) == call(dtype=-1) == lib.ATTN_ERR_UNSUPPORTED
+    assert call(dtype=3) == call(dtype=-1) == lib.ATTN_ERR_SHAPE
     assert call(N=1 << 30, B=1 << 11) == lib.ATTN_ERR_TOO_LARGE
     assert call(strides=[0, 0, 1 << 40] * 4) == lib.ATTN_ERR_TOO_LARGE
     with pytest.raises(ValueError, match="strides"):
@@ -119,7 +119,7 @@ def test_layer_norm_refusals(lib):
         for name in (needed + " " + others).split():
             assert call(**{name: FAKE + 4}) == lib.ATTN_ERR_ALIGN, name
         assert call(rows=-1) == call(C=0) == call(C=-5) == lib.ATTN_ERR_SHAPE
-        assert call(dtype=3) == call(wdtype=-1) == lib.ATTN_ERR_UNSUPPORTED
+        assert call(dtype=3) == call(wdtype=-1) == lib.ATTN_ERR_SHAPE
         assert call(rows=1 << 40) == call(rows=1 << 30, C=1 << 20) == \
             call(rows=1, C=(1 << 29) + 1) == lib.ATTN_ERR_TOO_LARGE
     assert fwd(eps=-1.0) == fwd(eps=NAN) == fwd(eps=INF) == lib.ATTN_ERR_SHAPE
@@ -159,7 +159,7 @@ def test_dropout_refusals(lib):
             assert call(**{name: FAKE + 2}) == lib.ATTN_ERR_ALIGN, name
         for p in (-0.1, 1.0, 1.5, NAN, INF):
             assert call(p=p) == lib.ATTN_ERR_SHAPE, p
-        assert call(dtype=7) == lib.ATTN_ERR_UNSUPPORTED
+        assert call(dtype=7) == lib.ATTN_ERR_SHAPE
     assert add(residual=FAKE + 2) == fwd(beta=FAKE + 2) == bwd(dz=FAKE + 2) == lib.ATTN_ERR_ALIGN
     assert add(n=-1) == fwd(rows=-1) == bwd(C=0) == lib.ATTN_ERR_SHAPE
     assert fwd(eps=-1e-5) == lib.ATTN_ERR_SHAPE
