@@ -96,7 +96,9 @@ __global__ void __launch_bounds__(kDropThreads)
 
 // Second stage of the weight gradients: a block takes 32 columns, its 32
 // warps every 32nd partial sum of each (kept in flight eight at a time), and
-// adds the warps' sums in order.
+// adds the warps' sums in order. About 2 us at 4096 columns (152 partial sums
+// each, 5 MB from L2), mostly the launch and the wait for the first stage; its
+// launch overlaps that stage, which saves up to 0.5 us of it.
 __global__ void __launch_bounds__(1024) weights_sum_kernel(BwdArgs a, int chunks) {
   __shared__ float part[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
