@@ -215,6 +215,11 @@ __device__ __forceinline__ void store_row_vec(T* p, const float (&f)[E], bool ed
 __device__ __forceinline__ void copy_async16(uint32_t smem, const void* global) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(global) : "memory");
 }
+// The first `bytes` of them, zeros behind.
+__device__ __forceinline__ void copy_async16(uint32_t smem, const void* global, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(global), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void copy_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -248,9 +253,6 @@ struct Walk {
   static_assert(STAGES % R == 0 && kAhead >= 0, "a turn's rows lie side by side in the ring");
   uint4* ring;        // this thread's slots: [STAGES][NT][VECS], BLOCK apart
   const T* from[NT];  // vector 0 of the next row to copy
-  const T* end[NT];   // behind the tensors (RAGGED)
-  bool tail;          // the thread's last row is at the tensors' end (RAGGED; the one
-                      // before it, at least eight rows earlier, is not)
   int edges;          // bits: vectors that reach over the row's ends (RAGGED)
   long long stride;   // elements between this thread's rows
   long long e;        // element of the turn's first row's vector 0
@@ -270,18 +272,12 @@ struct Walk {
     stride = step * C;
     left = split.whole + (row < split.rest);
     to_copy = left;
-    // a row's last vector ends less than E elements behind the row; that is
-    // within the tensor unless fewer than E elements follow the row
-    tail = RAGGED && left > 0 && (rows - 1 - (row + (left - 1) * step)) * C < E;
     edges = 0;
 #pragma unroll
     for (int j = 0; j < S::VECS; ++j)
       if (RAGGED && inside(j) && (column(j) < 0 || column(j) + E > C)) edges |= 1 << j;
 #pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      from[q] = static_cast<const T*>(src[q]) + e;
-      end[q] = static_cast<const T*>(src[q]) + rows * C;
-    }
+    for (int q = 0; q < NT; ++q) from[q] = static_cast<const T*>(src[q]) + e;
 #pragma unroll
     for (int j = 0; j < S::VECS; ++j)
       if (!inside(j))
@@ -318,12 +314,11 @@ struct Walk {
           for (int q = 0; q < NT; ++q) {
             uint4* slot = to + (q * S::VECS + j) * S::BLOCK;
             const T* p = from[q] + offset(j);
-            if (!RAGGED || !(tail && to_copy == 1 && edge(j)) || p + E <= end[q]) {
+            if (RAGGED)  // not behind the row, which may be the tensor's last
+              copy_async16(ptx::smem_u32(slot), p,
+                           min(C - column(j), E) * static_cast<int>(sizeof(T)));
+            else
               copy_async16(ptx::smem_u32(slot), p);
-            } else {  // the tensor ends inside the vector
-              T* v = reinterpret_cast<T*>(slot);
-              for (int i = 0; i < E; ++i) v[i] = p + i < end[q] ? p[i] : from_f32<T>(0.f);
-            }
           }
         }
       }
@@ -338,27 +333,25 @@ struct Walk {
     fill = fill == (STAGES - 1) * kStage ? 0 : fill + kStage;
   }
   // starts the next copies and waits for the turn's N rows (R of them, fewer
-  // in the last turn); of the first `trimmed` tensors, what lies outside a row
-  // becomes zero
+  // in the last turn); of the first `trimmed` tensors, what the first vector
+  // has of the row before becomes zero
   template <int N>
   __device__ __forceinline__ void arrive(int trimmed) {
 #pragma unroll
     for (int k = 0; k < N; ++k) copy_next();
     copy_wait<kAhead>();
+    if (RAGGED && column(0) < 0) {
+      uint32_t m[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int j = 0; j < S::VECS; ++j) {
-      if (edge(j)) {
-        uint32_t m[4] = {0u, 0u, 0u, 0u};
+      for (int i = 0; i < E; ++i)
+        if (column(0) + i >= 0)
+          m[i * 4 / E] |= sizeof(T) == 4 ? 0xffffffffu : (i % 2 == 0 ? 0xffffu : 0xffff0000u);
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (static_cast<unsigned>(column(j) + i) < static_cast<unsigned>(C))
-            m[i * 4 / E] |= sizeof(T) == 4 ? 0xffffffffu : (i % 2 == 0 ? 0xffffu : 0xffff0000u);
-        for (int k = 0; k < N; ++k)
-          for (int q = 0; q < trimmed; ++q) {
-            uint4& v = ring[take + k * kStage + (q * S::VECS + j) * S::BLOCK];
-            v = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
-          }
-      }
+      for (int k = 0; k < N; ++k)
+        for (int q = 0; q < trimmed; ++q) {
+          uint4& v = ring[take + k * kStage + q * S::VECS * S::BLOCK];
+          v = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
+        }
     }
   }
   // vector j of tensor q of the turn's k-th row
