@@ -261,7 +261,7 @@ struct Walk {
   int t, shift, C;
   int fill, take;     // where the stages begin
 
-  __device__ __forceinline__ Walk(uint4* smem, const void* const (&src)[NT], long long rows, int C_,
+  __device__ __forceinline__ Walk(uint4* smem, const void* const (&src)[NT], int C_,
                                   const Split& split)
       : ring(smem + threadIdx.x), C(C_), fill(0), take(0) {
     row = static_cast<long long>(blockIdx.x) / S::CTAS * S::ROWS + threadIdx.x / S::TPR;
@@ -432,9 +432,9 @@ __device__ __forceinline__ void row_sums(float (&v)[R], float* part) {
 // ADD: with a residual, and z written.
 // Bound by HBM: 8192 x 4096 bf16 takes 23.3 us for 134 MB (5.8 TB/s), with
 // residual and dropout 48.8 us for 269 MB (5.5 TB/s; half of the cycles issue,
-// and dropping costs 1 us of it). Two rows a turn took 2 us less than one, and
-// two blocks of 256 threads with the weights in registers (128 a thread) less
-// than three or four with fewer registers (80: 66 us with dropout, 49 without).
+// and dropping costs 1 us of it). One row a turn took 3 us more, and three
+// blocks of 256 threads at 80 registers, not two at 128, 66 us with dropout and
+// the same without.
 template <typename T, typename S, int STAGES, int R, bool ADD, bool DROP, bool RAGGED>
 __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
     fwd_kernel(FwdArgs a, Split split) {
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
   const void* src[NT];
   src[0] = a.x;
   if (ADD) src[NT - 1] = a.residual;
-  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.rows, a.C, split);
+  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.C, split);
   const float inv_C = 1.0f / static_cast<float>(a.C);
   uint64_t gamma[VECS][P], beta[VECS][P];
   __shared__ __align__(16) float stages[RAGGED ? S::BLOCK / 32 : 1][32 * E];
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 3 : 1)
   src[0] = a.dy;
   src[1] = a.z;
   if (DZ) src[NT - 1] = a.dz;
-  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.rows, a.C, split);
+  Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.C, split);
   const float inv_C = 1.0f / static_cast<float>(a.C);
   // the statistics of the rows to come, one turn ahead
   float mu_next[R], r_next[R];

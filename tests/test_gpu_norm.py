@@ -316,6 +316,25 @@ def test_a_bad_row_stays_alone():
     assert torch.equal(dx[fine], ref[fine]) and torch.isnan(dx[[4, 6]]).all()
 
 
+@pytest.mark.parametrize("rows,C", [(40000, 64), (20000, 100), (3000, 1024), (700, 4096),
+                                    (700, 3001), (400, 9000)])
+def test_bad_rows_among_many(rows, C):
+    """The same where threads take several rows, some of them together."""
+    x, dy, gamma, beta = _make(rows, C, BF, F4, 5)
+    good, m, r = runner.layer_norm(x, gamma, beta)
+    ref, _, _ = runner.layer_norm_backward(dy, x, gamma, m, r)
+    bad = torch.arange(3, rows, 7, device=DEV)
+    fine = torch.ones(rows, dtype=torch.bool, device=DEV)
+    fine[bad] = False
+    x2 = x.clone()
+    x2[bad, (bad * 5) % C] = float("nan")
+    y, mean, rstd = runner.layer_norm(x2, gamma, beta)
+    assert torch.equal(y[fine], good[fine]) and torch.isnan(y[bad]).all()
+    assert torch.equal(mean[fine], m[fine]) and torch.equal(rstd[fine], r[fine])
+    dx, _, _ = runner.layer_norm_backward(dy, x2, gamma, mean, rstd)
+    assert torch.equal(dx[fine], ref[fine]) and torch.isnan(dx[bad]).all()
+
+
 @pytest.mark.parametrize("C", [64, 1001, 4096, 20000])
 def test_nothing_outside_is_written(C):
     rows = 5
