@@ -153,7 +153,7 @@ int backward(const BwdArgs& a, int dtype, cudaStream_t stream) {
     chunks = with_dtype(dtype, [&](auto t) { return run_bwd<decltype(t)>(a, stream); });
     if (chunks < 0) return chunks;
   }
-  if (!weights) return ATTN_OK;
+  if (!weights || (a.rows > 0 && chunks == 0)) return ATTN_OK;
   // launched while the first stage still runs (its launch is then behind it);
   // it waits for that stage's results on the device
   cudaLaunchAttribute early;

@@ -34,6 +34,20 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t rank, flo
       : "memory");
 }
 
+// Reads from the place that `addr` has in the shared memory of the cluster's
+// block `rank`.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // Lets a dependent grid be launched when all blocks have come here or ended.
 __device__ __forceinline__ void grid_dependency_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

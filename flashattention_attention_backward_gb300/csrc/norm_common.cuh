@@ -40,7 +40,8 @@ struct BwdArgs {
   const float *mean, *rstd;
   void *dx, *dres;  // dx: behind the dropout, or NULL; dres: dz itself
   void *dgamma, *dbeta;
-  float* workspace;
+  float* workspace;  // NULL: no weight gradients
+  int finish;        // the grid is one cluster, which finishes the weight gradients itself
   long long rows;
   int C, wdtype;
   Drop drop;
@@ -48,7 +49,8 @@ struct BwdArgs {
 
 // One of each per element type (attn_norm_bf16.cu, _fp16.cu, _fp32.cu);
 // rows > 0. The backward returns the number of partial sums a column that it
-// left in the workspace (0 without a workspace), or a negative error.
+// left in the workspace (0: none are wanted, or they are added up already), or a
+// negative error.
 template <typename T>
 int run_fwd(const FwdArgs& a, cudaStream_t stream);
 template <typename T>

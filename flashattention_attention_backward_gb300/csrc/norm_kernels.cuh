@@ -29,6 +29,8 @@ struct Shape {
   static constexpr int ROWS = BLOCK / TPR_;  // rows of a block at a time
   static constexpr int WARPS = (TPR_ > 32 ? TPR_ / 32 : 1) * CTAS_;  // warps per row
   static constexpr int LANES = TPR_ > 32 ? 32 : TPR_;  // lanes of a warp per row
+  // the backward of few rows may be one cluster that needs no second launch
+  static constexpr bool FINISH = TPR_ < 32 && BLOCK <= 256;
   static_assert(CTAS_ == 1 || BLOCK / TPR_ == 1, "a cluster has one row");
 };
 
@@ -627,7 +629,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 3 : 1)
   constexpr int NT = DZ ? 3 : 2;
   ptx::grid_dependency_launch();  // the second stage's launch, which waits for this grid's end
   // a block behind the last row (the grid comes in eights)
-  if (split.whole == 0 && blockIdx.x / S::CTAS * S::ROWS >= split.rest) return;
+  if (split.whole == 0 && blockIdx.x / S::CTAS * S::ROWS >= split.rest && !(S::FINISH && a.finish)) return;
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float parts[S::ROWS][2][2 * R * S::WARPS];
   auto& part = parts[S::WARPS > 1 ? threadIdx.x / S::TPR : 0];
@@ -754,7 +756,9 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 3 : 1)
   // threads to the ring's memory, where each column is added up over them in
   // order; straight to the workspace where there is one row of threads. RAGGED:
   // a thread's columns are at no vector's place and go one by one, a word of
-  // distance behind every eight so that the lanes' banks differ.
+  // distance behind every eight so that the lanes' banks differ. Where the grid
+  // is one cluster, its blocks then add theirs up, each a part of the columns:
+  // few rows need no second launch.
   float* const out = a.workspace + 2LL * (blockIdx.x / S::CTAS) * a.C;
   float* const sums = reinterpret_cast<float*>(ring);
   constexpr bool kGather = S::ROWS > 1 || (RAGGED && S::CTAS == 1);
@@ -791,7 +795,28 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 3 : 1)
                       ? S::ROWS
                       : static_cast<int>(split.rest - first);
     __syncthreads();
-    if (!RAGGED) {
+    if (S::FINISH && a.finish != 0) {
+      for (int i = threadIdx.x; i < 2 * a.C; i += BLOCK) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) v += sums[k * size + place(i)];
+        sums[place(i)] = v;  // column i is this thread's alone
+      }
+      ptx::cluster_barrier();
+      for (int i = blockIdx.x * BLOCK + threadIdx.x; i < 2 * a.C; i += gridDim.x * BLOCK) {
+        float part[8], v = 0.f;  // (a cluster has eight blocks at most)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          part[k] = k < static_cast<int>(gridDim.x)
+                        ? ptx::ld_cluster_f32(ptx::smem_u32(sums + place(i)), k)
+                        : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += part[k];
+        void* const to = i < a.C ? a.dgamma : a.dbeta;
+        if (to != nullptr) store_as(to, i < a.C ? i : i - a.C, a.wdtype, v);
+      }
+      ptx::cluster_barrier();  // no block leaves while another reads its sums
+    } else if (!RAGGED) {
       for (int i = threadIdx.x; i < a.C / 2; i += BLOCK) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -1007,6 +1032,30 @@ int launch_walk(Kernel kern, const Args& a, int smem, long long most,
   return static_cast<int>(std::min(n, (a.rows + S::ROWS - 1) / S::ROWS));
 }
 
+// Launches a walking kernel as one cluster of `blocks` blocks; 0, or a negative
+// error.
+template <typename S, typename Kernel, typename Args>
+int launch_cluster(Kernel kern, const Args& a, int smem, int blocks,
+                   std::atomic<bool> (&limit_set)[kMaxTrackedDevices], cudaStream_t stream) {
+  if (!set_smem_limit_once(kern, smem, limit_set)) return ATTN_ERR_LAUNCH;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = static_cast<unsigned>(blocks);
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(static_cast<unsigned>(blocks));
+  config.blockDim = dim3(S::BLOCK);
+  config.dynamicSmemBytes = static_cast<size_t>(smem);
+  config.stream = stream;
+  config.attrs = &cluster;
+  config.numAttrs = 1;
+  const long long places = static_cast<long long>(blocks) * S::ROWS;
+  const Split split{static_cast<int>(a.rows / places), a.rows % places};
+  if (cudaLaunchKernelEx(&config, kern, a, split) != cudaSuccess)
+    return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
+  return 0;
+}
+
 // Stages of a ring whose stage has `bytes`: what `room` has place for, in
 // pairs, up to eight.
 constexpr int stages_for(int bytes, int room) {
@@ -1060,8 +1109,20 @@ int bwd_rows(const BwdArgs& a, cudaStream_t stream) {
                   "ring too small for the sums");
     // (with 16 elements a thread, two rows of a warp's own a turn spill)
     constexpr int kRows = kStages > 2 && (S::WARPS > 1 || S::BLOCK <= 256) ? 2 : 1;
-    return launch_walk<S>(bwd_kernel<T, S, kStages, kRows, DZ, DROP, RAGGED>, a, kStages * kBytes,
-                          kMaxChunks, limit_set, resident, stream);
+    const auto kern = bwd_kernel<T, S, kStages, kRows, DZ, DROP, RAGGED>;
+    // Weight gradients of up to eight blocks' rows of one turn: one cluster
+    // finishes them itself (500 rows of 64 columns 3.2 us, 4.1 with the second
+    // launch; 100 of 100 3.9 and 4.7). From 512 columns on reading the other
+    // blocks' sums costs as much as that launch, or more (32 of 4096 9.0 and
+    // 6.6).
+    if (S::FINISH && a.workspace != nullptr && a.rows <= 8LL * S::ROWS * kRows) {
+      BwdArgs b = a;
+      b.finish = 1;
+      int blocks = 1;  // RAGGED: where threads take two rows, a multiple of 8 rows apart
+      while (blocks < 8 && blocks * S::ROWS < a.rows) blocks *= 2;
+      return launch_cluster<S>(kern, b, kStages * kBytes, blocks, limit_set, stream);
+    }
+    return launch_walk<S>(kern, a, kStages * kBytes, kMaxChunks, limit_set, resident, stream);
   });
 }
 
