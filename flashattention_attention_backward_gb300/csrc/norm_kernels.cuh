@@ -629,7 +629,9 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 3 : 1)
   constexpr int NT = DZ ? 3 : 2;
   ptx::grid_dependency_launch();  // the second stage's launch, which waits for this grid's end
   // a block behind the last row (the grid comes in eights)
-  if (split.whole == 0 && blockIdx.x / S::CTAS * S::ROWS >= split.rest && !(S::FINISH && a.finish)) return;
+  if (split.whole == 0 && blockIdx.x / S::CTAS * S::ROWS >= split.rest &&
+      !(S::FINISH && a.finish != 0))
+    return;
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float parts[S::ROWS][2][2 * R * S::WARPS];
   auto& part = parts[S::WARPS > 1 ? threadIdx.x / S::TPR : 0];
