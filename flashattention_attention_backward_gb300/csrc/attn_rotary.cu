@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "element.cuh"
+#include "grid_ptx.cuh"
 
 namespace attn {
 namespace rotary {
@@ -68,6 +69,7 @@ __device__ __forceinline__ void angle(long long p, unsigned long long f, float& 
 // rot): one thread per column pair (or copied column) of a row.
 template <typename TQ, typename TK, typename TO>
 __global__ void __launch_bounds__(256) rotary_any_kernel(Args p) {
+  ptx::grid_dependency_wait();
   const int items = p.half + (p.d - 2 * p.half);
   const int heads = p.side[0].heads + p.side[1].heads;
   const long long total = static_cast<long long>(p.B) * p.N * heads * items;
@@ -135,9 +137,9 @@ struct Group {
 // lanes have neighbour groups, so that requests are whole sectors (with two
 // neighbouring groups a lane the interleaved d = 64 case took 14.8 us, not
 // 14.0). The angles cost about as much as four heads' arithmetic; the loads
-// and stores are what bounds it: B=2 H=32 H_kv=8 N=4096 d=128 bf16 takes 27.8
-// us for 168 MB (6.0 TB/s), the finalize step of that shape 36.5 us for 235 MB
-// (6.4 TB/s).
+// and stores are what bounds it: B=2 H=32 H_kv=8 N=4096 d=128 bf16 takes 27.4
+// us for 168 MB (6.1 TB/s), the finalize step of that shape 36.0 us for 235 MB
+// (6.5 TB/s).
 template <typename TI, typename TO, int U, bool INTERLEAVED>
 __device__ __forceinline__ void rotate_heads(const Args& p, const Side& s, int h0, int h1,
                                              long long b, long long n, int item) {
@@ -243,6 +245,7 @@ __device__ __forceinline__ void rotate_heads(const Args& p, const Side& s, int h
 template <typename TQ, typename TK, typename TO, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
     rotary_kernel(Args p, int items, int per, int q_groups, long long tokens) {
+  ptx::grid_dependency_wait();
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   long long token, b, n;
   int item;
@@ -294,9 +297,9 @@ int launch(const Args& a, cudaStream_t stream) {
   if (!whole_groups<TO>(a)) {
     const long long total = static_cast<long long>(a.B) * a.N * heads * (a.d - a.half);
     const long long want = (total + 255) / 256, cap = sms * 8LL;
-    rotary_any_kernel<TQ, TK, TO>
-        <<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream>>>(a);
-    return launch_status();
+    return launch_overlapped(rotary_any_kernel<TQ, TK, TO>,
+                             dim3(static_cast<unsigned>(want < cap ? want : cap)), 256, 0, 0,
+                             stream, a);
   }
   constexpr int E = Vec<TO>::kElems;
   const int items = a.interleaved ? (a.d + 2 * E - 1) / (2 * E)
@@ -310,11 +313,9 @@ int launch(const Args& a, cudaStream_t stream) {
   while (per > 1 && blocks * (groups(0) + groups(1)) < sms * 8LL) per /= 2;
   const int qg = groups(0), kg = groups(1);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(qg + kg));
-  if (a.interleaved)
-    rotary_kernel<TQ, TK, TO, true><<<grid, kThreads, 0, stream>>>(a, items, per, qg, tokens);
-  else
-    rotary_kernel<TQ, TK, TO, false><<<grid, kThreads, 0, stream>>>(a, items, per, qg, tokens);
-  return launch_status();
+  return launch_overlapped(
+      a.interleaved ? rotary_kernel<TQ, TK, TO, true> : rotary_kernel<TQ, TK, TO, false>, grid,
+      kThreads, 0, 0, stream, a, items, per, qg, tokens);
 }
 
 // Checks shared by the two calls.

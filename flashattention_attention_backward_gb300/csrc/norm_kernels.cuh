@@ -433,13 +433,14 @@ __device__ __forceinline__ void row_sums(float (&v)[R], float* part) {
 // which loses nothing to cancellation and costs one barrier a turn of R rows.
 // ADD: with a residual, and z written.
 // Bound by HBM: 8192 x 4096 bf16 takes 23.3 us for 134 MB (5.8 TB/s), with
-// residual and dropout 48.8 us for 269 MB (5.5 TB/s; half of the cycles issue,
+// residual and dropout 48.2 us for 269 MB (5.5 TB/s; half of the cycles issue,
 // and dropping costs 1 us of it). One row a turn took 3 us more, and three
 // blocks of 256 threads at 80 registers, not two at 128, 66 us with dropout and
 // the same without.
 template <typename T, typename S, int STAGES, int R, bool ADD, bool DROP, bool RAGGED>
 __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
     fwd_kernel(FwdArgs a, Split split) {
+  ptx::grid_dependency_wait();
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, P = E / 2, NT = ADD ? 2 : 1;
   constexpr int kLanes = S::LANES, kWarps = S::WARPS;
   // a block behind the last row (the grid comes in eights)
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
 // gradients, from the ring again. DZ: with a dz to add.
 // 8192 x 4096 bf16: 36.3 us for 201 MB, of which 31.6 the rows' gradients (6.4
 // TB/s) and the rest the weights' (their second stage, and the partial sums);
-// with dz and dropout 58.2 us for 336 MB (5.8 TB/s), bound by issue and the
+// with dz and dropout 58.4 us for 336 MB (5.8 TB/s), bound by issue and the
 // multiply pipe (59 % of the cycles issue) about as much as by HBM. A row at a
 // time took 45 and 69 us; 64 registers for twice the threads 44 and 82.
 template <typename T, typename S, int STAGES, int R, bool DZ, bool DROP, bool RAGGED>
@@ -627,6 +628,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 3 : 1)
     bwd_kernel(BwdArgs a, Split split) {
   constexpr int E = Vec<T>::kElems, VECS = S::VECS, BLOCK = S::BLOCK, P = E / 2;
   constexpr int NT = DZ ? 3 : 2;
+  ptx::grid_dependency_wait();
   ptx::grid_dependency_launch();  // the second stage's launch, which waits for this grid's end
   // a block behind the last row (the grid comes in eights)
   if (split.whole == 0 && blockIdx.x / S::CTAS * S::ROWS >= split.rest &&
@@ -997,23 +999,22 @@ int launch_walk(Kernel kern, const Args& a, int smem, long long most,
                 std::atomic<bool> (&limit_set)[kMaxTrackedDevices],
                 std::atomic<int> (&resident)[kMaxTrackedDevices], cudaStream_t stream) {
   if (!set_smem_limit_once(kern, smem, limit_set)) return ATTN_ERR_LAUNCH;
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = S::CTAS;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t config{};
-  config.gridDim = dim3(S::CTAS);
-  config.blockDim = dim3(S::BLOCK);
-  config.dynamicSmemBytes = static_cast<size_t>(smem);
-  config.stream = stream;
-  config.attrs = &cluster;
-  config.numAttrs = S::CTAS > 1 ? 1 : 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_LAUNCH;
   const bool tracked = dev >= 0 && dev < kMaxTrackedDevices;
   int at_once = tracked ? resident[dev].load(std::memory_order_relaxed) : 0;
   if (at_once <= 0) {
     if (S::CTAS > 1) {
+      cudaLaunchAttribute cluster;
+      cluster.id = cudaLaunchAttributeClusterDimension;
+      cluster.val.clusterDim.x = S::CTAS;
+      cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+      cudaLaunchConfig_t config{};
+      config.gridDim = dim3(S::CTAS);
+      config.blockDim = dim3(S::BLOCK);
+      config.dynamicSmemBytes = static_cast<size_t>(smem);
+      config.attrs = &cluster;
+      config.numAttrs = 1;
       if (cudaOccupancyMaxActiveClusters(&at_once, kern, &config) != cudaSuccess)
         return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
     } else {
@@ -1027,10 +1028,10 @@ int launch_walk(Kernel kern, const Args& a, int smem, long long most,
   }
   long long n = std::max(8LL, std::min<long long>(at_once, most) / 8 * 8);
   n = std::min(n, ((a.rows + S::ROWS - 1) / S::ROWS + 7) / 8 * 8);
-  config.gridDim = dim3(static_cast<unsigned>(n * S::CTAS));
   const Split split{static_cast<int>(a.rows / (n * S::ROWS)), a.rows % (n * S::ROWS)};
-  if (cudaLaunchKernelEx(&config, kern, a, split) != cudaSuccess)
-    return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
+  const int rc = launch_overlapped(kern, dim3(static_cast<unsigned>(n * S::CTAS)), S::BLOCK, smem,
+                                   S::CTAS > 1 ? S::CTAS : 0, stream, a, split);
+  if (rc != ATTN_OK) return rc;
   return static_cast<int>(std::min(n, (a.rows + S::ROWS - 1) / S::ROWS));
 }
 
@@ -1040,22 +1041,10 @@ template <typename S, typename Kernel, typename Args>
 int launch_cluster(Kernel kern, const Args& a, int smem, int blocks,
                    std::atomic<bool> (&limit_set)[kMaxTrackedDevices], cudaStream_t stream) {
   if (!set_smem_limit_once(kern, smem, limit_set)) return ATTN_ERR_LAUNCH;
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = static_cast<unsigned>(blocks);
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t config{};
-  config.gridDim = dim3(static_cast<unsigned>(blocks));
-  config.blockDim = dim3(S::BLOCK);
-  config.dynamicSmemBytes = static_cast<size_t>(smem);
-  config.stream = stream;
-  config.attrs = &cluster;
-  config.numAttrs = 1;
   const long long places = static_cast<long long>(blocks) * S::ROWS;
   const Split split{static_cast<int>(a.rows / places), a.rows % places};
-  if (cudaLaunchKernelEx(&config, kern, a, split) != cudaSuccess)
-    return (void)cudaGetLastError(), ATTN_ERR_LAUNCH;
-  return 0;
+  return launch_overlapped(kern, dim3(static_cast<unsigned>(blocks)), S::BLOCK, smem, blocks,
+                           stream, a, split);
 }
 
 // Stages of a ring whose stage has `bytes`: what `room` has place for, in

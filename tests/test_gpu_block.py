@@ -172,3 +172,76 @@ def test_chain_captured():
         assert torch.equal(out[name], want[name]), name
     for name in ("dx", "dg1", "db1"):  # behind dQ, whose atomics come in any order
         assert rel_fro(_np(out[name]), _np(want[name])) <= CHAIN, name
+
+
+class _Mixed:
+    """Calls behind one another, behind a fill and a copy, and behind the join of
+    two streams: each must find the results of what stands before it."""
+
+    def __init__(self, rows, C):
+        g = torch.Generator(device=DEV).manual_seed(rows + C)
+        self.src = torch.randint(-8, 8, (rows, C), device=DEV, generator=g).float()
+        self.gamma = torch.randn(C, device=DEV, generator=g)
+        self.x, self.z, self.out, self.dx = (torch.zeros_like(self.src) for _ in range(4))
+        self.dgamma, self.dbeta = (torch.zeros(C, device=DEV) for _ in range(2))
+
+    def run(self, main, other, between=lambda: None):
+        x = self.x
+        with torch.cuda.stream(main):
+            x.zero_()
+            x.copy_(self.src)
+            between()
+            y = runner.dropout_add(x, self.src)
+            between()
+            forked = torch.cuda.Event()
+            forked.record(main)
+        with torch.cuda.stream(other):
+            other.wait_event(forked)
+            side = runner.dropout_add(y)
+            between()
+            joined = torch.cuda.Event()
+            joined.record(other)
+        with torch.cuda.stream(main):
+            self.out.zero_()
+            main.wait_event(joined)
+            between()
+            z = runner.dropout_add(side, y)
+            between()
+            norm, mean, rstd = runner.layer_norm(z, self.gamma, self.gamma)
+            between()
+            dx, dgamma, dbeta = runner.layer_norm_backward(z, norm, self.gamma, mean, rstd)
+            between()
+            self.dx.copy_(runner.dropout_add(dx, norm))
+            self.z.copy_(z)
+            self.out.copy_(norm)
+            self.dgamma.copy_(dgamma)
+            self.dbeta.copy_(dbeta)
+
+    def results(self):
+        return [t.clone() for t in (self.z, self.out, self.dx, self.dgamma, self.dbeta)]
+
+
+@pytest.mark.parametrize("rows,C", [(1, 1), (40, 64), (300, 1001), (64, 10000), (3, 20000)])
+def test_calls_wait_for_what_stands_before(rows, C):
+    """Back to back and in a graph the same bits as with a wait after each call."""
+    m = _Mixed(rows, C)
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    m.run(main, other, between=torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    assert torch.equal(m.z, 4 * m.src)  # sums of small integers: exact
+    want = m.results()
+    for _ in range(20):
+        m.run(main, other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(m.results(), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        m.run(main, other)
+    for t in (m.z, m.out, m.dx, m.dgamma, m.dbeta):
+        t.fill_(7)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(m.results(), want))
