@@ -3,6 +3,13 @@ C ABI in stream order: forward (O, LSE), then preprocess -> attn_bwd ->
 finalize, and the operators around them (rotary positions, layer norm,
 dropout with a residual). No arithmetic happens here; torch provides memory
 and streams.
+
+Streams: a call runs on `stream` (a torch stream, another object with a
+`cuda_stream` handle, or a handle), by default the current one of its tensors'
+device. What it allocates belongs to that stream, and its results may also be
+used and dropped on the stream that was current at the call. Its inputs have to
+be ready on `stream`, and stay alive until it has read them (hold them, or
+`record_stream`), as with torch's own operations on a side stream.
 """
 import torch
 
@@ -51,8 +58,49 @@ def _check_lse(lse, B, H, N, device):
         raise ValueError("lse must be a contiguous float32 [B, H, N] tensor on the inputs' device")
 
 
-def _stream(stream):
-    return stream if stream is not None else torch.cuda.current_stream()
+class _On:
+    """The stream of a call on a device's tensors: current inside the context,
+    as the device is. Memory allocated there comes from that stream's own
+    blocks, so no work queued on another stream still reads what the call
+    writes. Tensors handed back go through `made`."""
+
+    def __init__(self, stream, device):
+        current = torch.cuda.current_stream(device)
+        if stream is None:
+            stream = current
+        elif not isinstance(stream, torch.cuda.Stream):
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
+            stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
+                torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError("the stream is on %s, the tensors are on %s" % (stream.device, device))
+        self.stream = stream
+        self.caller = None if stream == current else current
+        self._context = torch.cuda.device(device) if self.caller is None else \
+            torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._context.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self._context.__exit__(*exc)
+
+    def made(self, *tensors):
+        """Tells torch's allocator that the stream current at the call may use
+        these tensors too: their memory is not handed out again before what is
+        queued there when they are dropped has run."""
+        self._record(self.caller, tensors)
+
+    def given(self, *tensors):
+        """The same of the call's stream and the caller's own tensors."""
+        self._record(self.stream, tensors)
+
+    def _record(self, stream, tensors):
+        if self.caller is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
 
 
 def forward(q, k, v, scale, causal, softcap=0.0, stream=None, impl="tc", dropout=None,
@@ -64,34 +112,39 @@ def forward(q, k, v, scale, causal, softcap=0.0, stream=None, impl="tc", dropout
     B, H, H_kv, N, d = _dims(q, k, v)
     if v.shape != k.shape:
         raise ValueError("v must have the shape of k")
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    args = (B, H, H_kv, N, d, scale, causal, softcap)
     if dropout is not None:
         fn = {"tc": attn_fwd_dropout, "ref": attn_fwd_ref_dropout}[impl]
-        check(fn(q, k, v, o, lse, B, H, H_kv, N, d, scale, causal, softcap, dropout[0],
-                 dropout[1], _stream(stream)))
-        return o, lse
-    if window is not None:
+        args += (dropout[0], dropout[1])
+    elif window is not None:
         fn = {"tc": attn_fwd_local, "ref": attn_fwd_ref_local}[impl]
-        check(fn(q, k, v, o, lse, B, H, H_kv, N, d, scale, causal, softcap, window[0], window[1],
-                 _stream(stream)))
-        return o, lse
-    fn = {"tc": attn_fwd, "ref": attn_fwd_ref}[impl]
-    check(fn(q, k, v, o, lse, B, H, H_kv, N, d, scale, causal, softcap, _stream(stream)))
+        args += (window[0], window[1])
+    else:
+        fn = {"tc": attn_fwd, "ref": attn_fwd_ref}[impl]
+    with _On(stream, q.device) as on:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        check(fn(q, k, v, o, lse, *args, on.stream))
+        on.made(o, lse)
     return o, lse
 
 
 class BackwardBuffers:
-    """Outputs and scratch of one backward problem, reusable across calls."""
+    """Outputs and scratch of one backward problem, reusable across calls
+    (calls that may run at the same time need their own). `stream`: the one that
+    will use them, by default the current one."""
 
-    def __init__(self, q, k):
+    def __init__(self, q, k, stream=None):
         B, H, H_kv, N, d = _dims(q, k)
         dev = q.device
-        self.dq = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
-        self.dk = torch.empty((B, H_kv, N, d), dtype=torch.bfloat16, device=dev)
-        self.dv = torch.empty((B, H_kv, N, d), dtype=torch.bfloat16, device=dev)
-        self.dq_accum = torch.empty((B, H, N, d), dtype=torch.float32, device=dev)
-        self.dpsum = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+        with _On(stream, dev) as on:
+            self.dq = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
+            self.dk = torch.empty((B, H_kv, N, d), dtype=torch.bfloat16, device=dev)
+            self.dv = torch.empty((B, H_kv, N, d), dtype=torch.bfloat16, device=dev)
+            self.dq_accum = torch.empty((B, H, N, d), dtype=torch.float32, device=dev)
+            self.dpsum = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+            on.made(self.dq, self.dk, self.dv, self.dq_accum, self.dpsum)
+        self.dq_partials = None  # of the deterministic form, made by its first call
 
 
 def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=None,
@@ -111,11 +164,31 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
         positions, pos_stride = _check_rotary(rotary, positions, B, N, d, q.device)
     elif positions is not None:
         raise ValueError("positions are those of a rotary")
-    s = _stream(stream)
-    if bufs is None:
-        bufs = BackwardBuffers(q, k)
-
-    def finalize():
+    if dropout is None and window is not None and deterministic:
+        raise ValueError("the local window has no deterministic variant")
+    with _On(stream, q.device) as on:
+        s = on.stream
+        if bufs is None:
+            bufs = BackwardBuffers(q, k)
+            on.made(bufs.dq, bufs.dk, bufs.dv)
+        shape = (B, H, H_kv, N, d, scale, causal, softcap, bufs.dpsum)
+        if deterministic and dropout is None:
+            _deterministic_dq_dk_dv(q, k, v, o, do, lse, bufs, shape, s)
+            check(attn_bwd_finalize_partials(bufs.dq_partials, bufs.dq, scale, B, H, N, d, causal,
+                                             s))
+            if rotary is not None:
+                check(attn_rotary(bufs.dq, bufs.dk, bufs.dq, bufs.dk, rotary.turns, positions,
+                                  pos_stride, B, H, H_kv, N, d, rotary.rot, rotary.magnitude,
+                                  rotary.interleaved, True, ATTN_BF16, None, s))
+            return bufs.dq, bufs.dk, bufs.dv
+        check(attn_bwd_preprocess(o, do, bufs.dpsum, bufs.dq_accum, B, H, N, d, s))
+        tensors = (q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv)
+        if dropout is not None:
+            check(attn_bwd_dropout(*tensors, *shape, dropout[0], dropout[1], s))
+        elif window is not None:
+            check(attn_bwd_local(*tensors, *shape, window[0], window[1], s))
+        else:
+            check(attn_bwd(*tensors, *shape, s))
         if rotary is None:
             check(attn_bwd_finalize(bufs.dq_accum, bufs.dq, scale, B, H, N, d, s))
         else:
@@ -125,60 +198,23 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
                                            s))
         return bufs.dq, bufs.dk, bufs.dv
 
-    if dropout is not None:
-        check(attn_bwd_preprocess(o, do, bufs.dpsum, bufs.dq_accum, B, H, N, d, s))
-        check(attn_bwd_dropout(q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv, B, H, H_kv,
-                               N, d, scale, causal, softcap, bufs.dpsum, dropout[0], dropout[1],
-                               s))
-        return finalize()
-    if window is not None:
-        if deterministic:
-            raise ValueError("the local window has no deterministic variant")
-        check(attn_bwd_preprocess(o, do, bufs.dpsum, bufs.dq_accum, B, H, N, d, s))
-        check(attn_bwd_local(q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv, B, H, H_kv, N,
-                             d, scale, causal, softcap, bufs.dpsum, window[0], window[1], s))
-        return finalize()
-    if not deterministic:
-        check(attn_bwd_preprocess(o, do, bufs.dpsum, bufs.dq_accum, B, H, N, d, s))
-        check(attn_bwd(q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv, B, H, H_kv, N, d,
-                       scale, causal, softcap, bufs.dpsum, s))
-        return finalize()
+
+def _deterministic_dq_dk_dv(q, k, v, o, do, lse, bufs, shape, s):
+    """dQ's partial tiles, dK and dV; the partials' buffer grows with the problem."""
+    B, H, _, N, d, _, causal = shape[:7]
     nbytes = attn_bwd_dq_partials_bytes(B, H, N, d, causal)
     if nbytes < 0:
         check(int(nbytes))
-    if getattr(bufs, "dq_partials", None) is None or bufs.dq_partials.numel() * 4 < nbytes:
+    partials = getattr(bufs, "dq_partials", None)
+    if partials is None or partials.numel() * 4 < nbytes:
         bufs.dq_partials = torch.empty(max(nbytes // 4, 4), dtype=torch.float32, device=q.device)
+    bufs.dq_partials.record_stream(s)  # a later call's larger one may replace it
     check(attn_bwd_preprocess(o, do, bufs.dpsum, None, B, H, N, d, s))
-    check(attn_bwd_deterministic(q, k, v, o, do, lse, bufs.dq_partials, bufs.dk, bufs.dv, B, H,
-                                 H_kv, N, d, scale, causal, softcap, bufs.dpsum, s))
-    check(attn_bwd_finalize_partials(bufs.dq_partials, bufs.dq, scale, B, H, N, d, causal, s))
-    if rotary is not None:
-        check(attn_rotary(bufs.dq, bufs.dk, bufs.dq, bufs.dk, rotary.turns, positions, pos_stride,
-                          B, H, H_kv, N, d, rotary.rot, rotary.magnitude, rotary.interleaved, True,
-                          ATTN_BF16, None, s))
-    return bufs.dq, bufs.dk, bufs.dv
+    check(attn_bwd_deterministic(q, k, v, o, do, lse, bufs.dq_partials, bufs.dk, bufs.dv, *shape,
+                                 s))
 
 
 # ------------------------------------------------ around the attention call
-def _stream_of(stream, device):
-    """The caller's stream, or the current one of the tensors' device."""
-    return stream if stream is not None else torch.cuda.current_stream(device)
-
-
-def _made_for(stream, device, *tensors):
-    """Tells torch's allocator that tensors which it made on the current
-    stream are used on the caller's, so that it does not hand their memory
-    out again before that work is done."""
-    if stream is None:
-        return
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    if stream != torch.cuda.current_stream(device):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
 def _check_cuda(device, **tensors):
     for name, t in tensors.items():
         if t is not None and (t.device != device or t.device.type != "cuda"):
@@ -241,26 +277,28 @@ def rotary(q, k, plan, positions=None, adjoint=False, out=None, stream=None):
         raise ValueError("k has shape %s, expected [%d, heads, %d, %d]" % (tuple(k.shape), B, N, d))
     if q.dtype not in _DTYPES or (k is not None and k.dtype != q.dtype):
         raise ValueError("q and k must both be bfloat16, float16 or float32")
-    if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
-    for x, y in ((q, out[0]), (k, out[1])):
+    given = (None, None) if out is None else out
+    for x, y in ((q, given[0]), (k, given[1])):
         if x is None:
             continue
-        if y is None or y.shape != x.shape or y.dtype != x.dtype:
+        if out is not None and (y is None or y.shape != x.shape or y.dtype != x.dtype):
             raise ValueError("out must have the shapes and dtype of q and k")
-        if d > 1 and (x.stride(3) != 1 or y.stride(3) != 1):
+        if d > 1 and (x.stride(3) != 1 or (y is not None and y.stride(3) != 1)):
             raise ValueError("rows must be contiguous")
-    _check_cuda(q.device, q=q, k=k, q_out=out[0], k_out=out[1])
-    _made_for(stream, q.device, *out)
+    _check_cuda(q.device, q=q, k=k, q_out=given[0], k_out=given[1])
     positions, pos_stride = _check_rotary(plan, positions, B, N, d, q.device)
-    parts = [q, q if k is None else k, out[0], out[0] if k is None else out[1]]
-    strides = [v for t in parts for v in t.stride()[:3]]
-    with torch.cuda.device(q.device):
+    with _On(stream, q.device) as on:
+        if out is None:
+            out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                   None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
+            on.made(*out)
+        else:
+            on.given(*out)
+        parts = [q, q if k is None else k, out[0], out[0] if k is None else out[1]]
+        strides = [v for t in parts for v in t.stride()[:3]]
         check(attn_rotary(q, k, out[0], out[1], plan.turns, positions, pos_stride, B, H,
                           0 if k is None else k.shape[1], N, d, plan.rot, plan.magnitude,
-                          plan.interleaved, adjoint, _DTYPES[q.dtype], strides,
-                          _stream_of(stream, q.device)))
+                          plan.interleaved, adjoint, _DTYPES[q.dtype], strides, on.stream))
     return out
 
 
@@ -295,12 +333,12 @@ def _row_stats(x):
 def layer_norm(x, gamma=None, beta=None, eps=1e-5, stream=None):
     """(y, mean, rstd) of x [..., C] (attn_layer_norm)."""
     rows, C, code, wcode = _norm_dims(x, gamma, beta)
-    y = torch.empty_like(x)
-    mean, rstd = _row_stats(x)
-    _made_for(stream, x.device, y, mean, rstd)
-    with torch.cuda.device(x.device):
+    with _On(stream, x.device) as on:
+        y = torch.empty_like(x)
+        mean, rstd = _row_stats(x)
         check(attn_layer_norm(x, gamma, beta, y, mean, rstd, rows, C, eps, code, wcode,
-                              _stream_of(stream, x.device)))
+                              on.stream))
+        on.made(y, mean, rstd)
     return y, mean, rstd
 
 
@@ -332,12 +370,12 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, weight_grads=True, stream=None
     _check_like(x, dy=dy)
     _check_cuda(x.device, dy=dy)
     _check_stats(x, mean, rstd)
-    dx = torch.empty_like(x)
-    dgamma, dbeta, workspace = _weight_grads(x, gamma, weight_grads, rows, C, x.dtype)
-    _made_for(stream, x.device, dx, dgamma, dbeta, workspace)
-    with torch.cuda.device(x.device):
+    with _On(stream, x.device) as on:
+        dx = torch.empty_like(x)
+        dgamma, dbeta, workspace = _weight_grads(x, gamma, weight_grads, rows, C, x.dtype)
         check(attn_layer_norm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, rows, C,
-                                  code, wcode, _stream_of(stream, x.device)))
+                                  code, wcode, on.stream))
+        on.made(dx, dgamma, dbeta)
     return dx, dgamma, dbeta
 
 
@@ -348,11 +386,11 @@ def dropout_add(x, residual=None, dropout=(0.0, 0), stream=None):
         raise ValueError("expected a bfloat16, float16 or float32 tensor, got %s" % x.dtype)
     _check_like(x, x=x, residual=residual)
     _check_cuda(x.device, x=x, residual=residual)
-    y = torch.empty_like(x)
-    _made_for(stream, x.device, y)
-    with torch.cuda.device(x.device):
+    with _On(stream, x.device) as on:
+        y = torch.empty_like(x)
         check(attn_dropout_add(x, residual, y, x.numel(), dropout[0], dropout[1],
-                               _DTYPES[x.dtype], _stream_of(stream, x.device)))
+                               _DTYPES[x.dtype], on.stream))
+        on.made(y)
     return y
 
 
@@ -362,13 +400,12 @@ def dropout_add_norm(x, residual, gamma=None, beta=None, eps=1e-5, dropout=(0.0,
     rows, C, code, wcode = _norm_dims(x, gamma, beta)
     _check_like(x, residual=residual)
     _check_cuda(x.device, residual=residual)
-    z, y = torch.empty_like(x), torch.empty_like(x)
-    mean, rstd = _row_stats(x)
-    _made_for(stream, x.device, z, y, mean, rstd)
-    with torch.cuda.device(x.device):
+    with _On(stream, x.device) as on:
+        z, y = torch.empty_like(x), torch.empty_like(x)
+        mean, rstd = _row_stats(x)
         check(attn_dropout_add_norm(x, residual, gamma, beta, z, y, mean, rstd, rows, C, eps,
-                                    dropout[0], dropout[1], code, wcode,
-                                    _stream_of(stream, x.device)))
+                                    dropout[0], dropout[1], code, wcode, on.stream))
+        on.made(z, y, mean, rstd)
     return z, y, mean, rstd
 
 
@@ -381,12 +418,12 @@ def dropout_add_norm_backward(dy, dz, z, gamma, mean, rstd, dropout=(0.0, 0), we
     _check_like(z, dy=dy, dz=dz)
     _check_cuda(z.device, dy=dy, dz=dz)
     _check_stats(z, mean, rstd)
-    dres = torch.empty_like(z)
-    dx = torch.empty_like(z) if dropout[0] != 0 else None
-    dgamma, dbeta, workspace = _weight_grads(z, gamma, weight_grads, rows, C, z.dtype)
-    _made_for(stream, z.device, dx, dres, dgamma, dbeta, workspace)
-    with torch.cuda.device(z.device):
+    with _On(stream, z.device) as on:
+        dres = torch.empty_like(z)
+        dx = torch.empty_like(z) if dropout[0] != 0 else None
+        dgamma, dbeta, workspace = _weight_grads(z, gamma, weight_grads, rows, C, z.dtype)
         check(attn_dropout_add_norm_bwd(dy, dz, z, gamma, mean, rstd, dx, dres, dgamma, dbeta,
                                         workspace, rows, C, dropout[0], dropout[1], code, wcode,
-                                        _stream_of(stream, z.device)))
+                                        on.stream))
+        on.made(dx, dres, dgamma, dbeta)
     return (dres if dx is None else dx), dres, dgamma, dbeta
