@@ -1,0 +1,135 @@
+"""Layer norm of rows beyond the kernels that keep a row on chip (more than
+16384 columns, or a few less where 16 bytes do not divide them), where the mean
+is far above the spread, against the 64-bit oracle.
+
+Tolerances, u = 2^-24. A term takes part in at most D = 54 + C / 2^19 additions
+(8 columns, 16 on each of two levels in a thread, C / 2^19 on the third,
+13 over the block and one to spare), so a sum is off by at most D u times its
+terms' magnitudes.
+With m the first reading's mean, e = (D + 1) u mean|x| its error, d = x - m and
+mean|d| <= mean|x - mu| + e:
+  rest = mean(d):  er = (D + 3) u mean|d| (u |d| from d itself);
+  mean = m + rest: er + u |mean|;
+  variance = mean(d^2) - rest^2: dv = (D + 7) u mean(d^2) + 2 e er + u e^2;
+  rstd: relative dr = dv / (2 (var + eps)) + 3 u, where dv is small beside var
+      + eps (asserted);
+  y: |gamma| r (u |d| + er + u |x - mu|) + |gamma h| (dr + 2 u) + u (|y| + |beta|).
+Rounding to the output type adds half a step, or half its smallest subnormal.
+"""
+import numpy as np
+import pytest
+import torch
+
+from flashattention_attention_backward_gb300 import runner
+from oracle import dropout, layer_norm
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+EPS = float(np.float32(1e-5))
+DEV = torch.device("cuda:0")
+BF, HF, F4 = torch.bfloat16, torch.float16, torch.float32
+TINY = {BF: 2.0 ** -134, HF: 2.0 ** -25, F4: 2.0 ** -149}
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _within(name, got, want, tol):
+    g = _np(got)
+    tol = tol + np.abs(want) * (torch.finfo(got.dtype).eps / 2 * (1 + 1e-6)) + TINY[got.dtype]
+    err = np.abs(g - want)
+    assert not np.isnan(err).any(), name
+    w = np.unravel_index((err - tol).argmax(), err.shape)
+    assert (err <= tol).all(), "%s at %s: error %.3e, allowed %.3e" % (name, w, err[w], tol[w])
+
+
+def _rows(kind, C, dtype, seed=1):
+    g = torch.Generator().manual_seed(seed + C)
+    noise = torch.randn(C, generator=g)
+    ramp = torch.arange(C).float() % 64 / 64
+    x = {"constant": torch.stack((torch.full((C,), 1000.3), torch.full((C,), -7.1))),
+         "far": torch.stack((1000.3 + 0.01 * noise, -4096 + ramp)),
+         "plain": torch.stack((1.5 * noise + 0.25, 1e-4 * noise))}[kind]
+    return x.to(dtype).to(DEV)
+
+
+def _check(x64, ex, gamma, beta, y, mean, rstd):
+    """ex: error of the elements before the norm."""
+    C = x64.shape[1]
+    D = 54 + C / 2 ** 19
+    want, m, r = layer_norm(x64, gamma, beta, EPS)
+    off = np.abs(x64 - m[:, None])
+    e = (D + 1) * U * np.abs(x64).mean(1) + ex.mean(1)
+    d = off.mean(1) + e
+    er = (D + 3) * U * d + ex.mean(1)
+    square = (off ** 2).mean(1) + e ** 2
+    dv = (D + 7) * U * square + 2 * e * er + U * e ** 2 + 2 * (off * ex).mean(1) + (ex ** 2).mean(1)
+    assert (dv < 0.01 / r ** 2).all()
+    dr = dv * r ** 2 / 2 * 1.02 + 3 * U
+    _within("mean", mean, m, er + U * np.abs(m))
+    _within("rstd", rstd, r, r * dr)
+    g = np.ones(C) if gamma is None else np.abs(gamma)
+    b = 0.0 if beta is None else np.abs(beta)
+    h = off * r[:, None]
+    tol = g * r[:, None] * (U * (off + e[:, None]) + er[:, None] + ex + U * off) + \
+        g * h * (dr[:, None] + 2 * U) + U * (np.abs(want) + b)
+    _within("y", y, want, tol)
+
+
+@pytest.mark.parametrize("dtype", [F4, HF, BF])
+@pytest.mark.parametrize("kind", ["constant", "far", "plain"])
+@pytest.mark.parametrize("C", [16383, 16385, 16392, 40000, 131071, 1 << 20])
+def test_mean_far_above_the_spread(C, kind, dtype):
+    x = _rows(kind, C, dtype)
+    y, mean, rstd = runner.layer_norm(x, None, None, EPS)
+    _check(_np(x), np.zeros(x.shape), None, None, y, mean, rstd)
+    if kind == "constant":
+        assert torch.equal(mean, x[:, 0].float()) and (y == 0).all()
+    g = torch.Generator().manual_seed(C)
+    gamma = (1 + 0.2 * torch.randn(C, generator=g)).to(DEV)
+    beta = (0.2 * torch.randn(C, generator=g)).to(DEV)
+    y, mean, rstd = runner.layer_norm(x, gamma, beta, EPS)
+    _check(_np(x), np.zeros(x.shape), _np(gamma), _np(beta), y, mean, rstd)
+
+
+@pytest.mark.parametrize("p", [0.0, 0.2])
+@pytest.mark.parametrize("C", [16385, 131072])
+def test_with_a_residual(C, p):
+    """The sum's mean is far above its spread by the residual."""
+    x, res = _rows("plain", C, F4) * 0.01, _rows("far", C, F4)
+    z, y, mean, rstd = runner.dropout_add_norm(x, res, None, None, EPS, (p, 77))
+    dropped = dropout(_np(x), p, 77)
+    want = dropped + _np(res)
+    ex = 2 * U * np.abs(dropped) + U * np.abs(want)
+    _within("z", z, want, ex)
+    # the statistics are those of the rounded sum, which is z itself in 32 bits
+    _check(_np(z), np.zeros(z.shape), None, None, y, mean, rstd)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_bad_row_stays_alone(bad):
+    x = _rows("plain", 20000, BF).repeat(3, 1)
+    good, m, r = runner.layer_norm(x)
+    x2 = x.clone()
+    x2[2, 19999] = bad
+    y, mean, rstd = runner.layer_norm(x2)
+    fine = [0, 1, 3, 4, 5]
+    assert torch.equal(y[fine], good[fine]) and torch.equal(mean[fine], m[fine])
+    assert torch.equal(rstd[fine], r[fine]) and torch.isnan(y[2]).all()
+    assert torch.isnan(mean[2]) if bad != bad else float(mean[2]) == bad
+
+
+def test_statistics_of_neighbouring_lengths():
+    """A row with one column more goes to other kernels; its mean and its root
+    are the same but for both bounds' roundings."""
+    x = _rows("far", 16385, F4)
+    _, m, r = runner.layer_norm(x[:, :16384].contiguous())
+    x2 = x[:, :16384].repeat(1, 2).contiguous()  # the same mean and variance
+    _, m2, r2 = runner.layer_norm(x2)
+    # one block's tree on chip: at most 16 + 10 additions and four products deep
+    size = np.abs(_np(x)).mean(1)
+    assert (np.abs(_np(m) - _np(m2)) <= 32 * U * size).all()
+    spread = _np(r2) ** -2
+    assert (np.abs(_np(r) / _np(r2) - 1) <= 40 * U + (32 * U * size) ** 2 / spread).all()
