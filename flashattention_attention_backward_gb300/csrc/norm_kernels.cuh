@@ -950,30 +950,34 @@ __global__ void __launch_bounds__(kThreads, 8) fwd_wide_kernel(FwdArgs a) {
   }
 }
 
+// The same of the backward, with the statistics given; its roundings are written
+// out, so that they do not depend on which of the outputs are wanted. 1024 x
+// 32768 bf16 with the weights' gradients: 201 us (floor 30).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) bwd_wide_kernel(BwdArgs a) {
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* dz = static_cast<const T*>(a.dz);
-  const T* z = static_cast<const T*>(a.z);
+__global__ void __launch_bounds__(kThreads, 8) bwd_wide_kernel(BwdArgs a) {
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const long long base = row * a.C;
+    const T* const dy = static_cast<const T*>(a.dy) + base;
+    const T* const z = static_cast<const T*>(a.z) + base;
+    const T* const dz = a.dz != nullptr ? static_cast<const T*>(a.dz) + base : nullptr;
     const float mu = a.mean[row], r = a.rstd[row];
     auto grad = [&](int c) {
-      const float g = to_f32(dy[base + c]);
-      return a.gamma != nullptr ? g * load_as(a.gamma, c, a.wdtype) : g;
+      const float g = to_f32(dy[c]);
+      return a.gamma != nullptr ? __fmul_rn(g, load_as(a.gamma, c, a.wdtype)) : g;
     };
-    float s = 0.f, t = 0.f;
+    auto normed = [&](int c) { return __fmul_rn(to_f32(z[c]) - mu, r); };
+    float sums[2];
+    wide_sums<true>(
+        a.C,
+        [&](int c, float (&v)[2]) {
+          v[0] = grad(c);
+          v[1] = __fmul_rn(v[0], normed(c));
+        },
+        sums);
+    const float s = sums[0] / a.C, t = sums[1] / a.C;
     for (int c = threadIdx.x; c < a.C; c += kThreads) {
-      const float g = grad(c), h = (to_f32(z[base + c]) - mu) * r;
-      s += g;
-      t = fmaf(g, h, t);
-    }
-    s = block_sum(s) / a.C;
-    t = block_sum(t) / a.C;
-    for (int c = threadIdx.x; c < a.C; c += kThreads) {
-      const float g = grad(c), h = (to_f32(z[base + c]) - mu) * r;
-      float v = r * (g - s - h * t);
-      if (dz != nullptr) v += to_f32(dz[base + c]);
+      float v = __fmul_rn(r, fmaf(-normed(c), t, grad(c) - s));
+      if (dz != nullptr) v = __fadd_rn(v, to_f32(dz[c]));
       if (a.dres != nullptr) static_cast<T*>(a.dres)[base + c] = from_f32<T>(v);
       if (a.dx != nullptr) {
         if (a.drop.on) v = kept(base + c, a.drop) ? v * a.drop.inv_keep : 0.f;

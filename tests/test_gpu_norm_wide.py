@@ -14,6 +14,11 @@ mean|d| <= mean|x - mu| + e:
   rstd: relative dr = dv / (2 (var + eps)) + 3 u, where dv is small beside var
       + eps (asserted);
   y: |gamma| r (u |d| + er + u |x - mu|) + |gamma h| (dr + 2 u) + u (|y| + |beta|).
+Backward, with the statistics given, h = (x - mean) rstd, g = dy gamma, s and t
+the means of g and g h:
+  h: eh = u rstd |x - mean| + 2 u |h|, g: u |g|;
+  s: (D + 2) u mean|g|, t: (D + 4) u mean|g h| + mean(|g| eh);
+  dx: rstd (2 u |g| + es + |h| et + |t| eh + 6 u (|g| + |s| + |h t|)) + u |dx|.
 Rounding to the output type adds half a step, or half its smallest subnormal.
 """
 import numpy as np
@@ -21,7 +26,7 @@ import pytest
 import torch
 
 from flashattention_attention_backward_gb300 import runner
-from oracle import dropout, layer_norm
+from oracle import dropout, layer_norm, layer_norm_backward
 
 pytestmark = pytest.mark.gpu
 
@@ -39,7 +44,11 @@ def _np(t):
 def _within(name, got, want, tol):
     g = _np(got)
     tol = tol + np.abs(want) * (torch.finfo(got.dtype).eps / 2 * (1 + 1e-6)) + TINY[got.dtype]
-    err = np.abs(g - want)
+    # values beyond the type's range round to infinity
+    most = torch.finfo(got.dtype).max
+    beyond = np.isinf(g) & (np.sign(g) == np.sign(want)) & (np.abs(want) + tol > most)
+    assert not (~np.isinf(g) & (np.abs(want) - tol > most)).any(), name
+    err = np.where(beyond, 0.0, np.abs(np.where(beyond, 0.0, g) - want * ~beyond))
     assert not np.isnan(err).any(), name
     w = np.unravel_index((err - tol).argmax(), err.shape)
     assert (err <= tol).all(), "%s at %s: error %.3e, allowed %.3e" % (name, w, err[w], tol[w])
@@ -133,3 +142,34 @@ def test_statistics_of_neighbouring_lengths():
     assert (np.abs(_np(m) - _np(m2)) <= 32 * U * size).all()
     spread = _np(r2) ** -2
     assert (np.abs(_np(r) / _np(r2) - 1) <= 40 * U + (32 * U * size) ** 2 / spread).all()
+
+
+@pytest.mark.parametrize("dtype", [F4, HF, BF])
+@pytest.mark.parametrize("kind", ["constant", "far", "plain"])
+@pytest.mark.parametrize("C", [16383, 16385, 40000, 131071, 1 << 20])
+def test_gradients_far_from_zero(C, kind, dtype):
+    """dy's mean far above its spread: dx is a small difference of its terms."""
+    D = 54 + C / 2 ** 19
+    dy, x = _rows(kind, C, dtype), _rows("plain", C, dtype, seed=3)
+    gen = torch.Generator().manual_seed(C)
+    gamma = (1 + 0.2 * torch.randn(C, generator=gen)).to(DEV)
+    _, mean, rstd = runner.layer_norm(x, None, None, EPS)
+    for w in (None, gamma):
+        dx, dgamma, dbeta = runner.layer_norm_backward(dy, x, w, mean, rstd)
+        w64 = np.ones(C) if w is None else _np(w)
+        want, dg, db = layer_norm_backward(_np(dy), _np(x), w64, _np(mean), _np(rstd))
+        r = _np(rstd)[:, None]
+        off = np.abs(_np(x) - _np(mean)[:, None])
+        h, g = off * r, np.abs(_np(dy) * w64)
+        signed = (_np(x) - _np(mean)[:, None]) * r
+        s = np.abs((_np(dy) * w64).mean(1, keepdims=True))
+        t = np.abs((_np(dy) * w64 * signed).mean(1, keepdims=True))
+        eh = U * r * off + 2 * U * h
+        es = (D + 2) * U * g.mean(1, keepdims=True)
+        et = (D + 4) * U * (g * h).mean(1, keepdims=True) + (g * eh).mean(1, keepdims=True)
+        tol = r * (2 * U * g + es + h * et + t * eh + 6 * U * (g + s + h * t)) + U * np.abs(want)
+        _within("dx", dx, want, tol)
+        # two rows: a column's sum is two terms
+        terms = np.abs(_np(dy)) * (h + eh)
+        _within("dgamma", dgamma, dg, 8 * U * terms.sum(0))
+        _within("dbeta", dbeta, db, 2 * U * np.abs(_np(dy)).sum(0))
