@@ -425,15 +425,27 @@ __device__ __forceinline__ void row_sums(float (&v)[R], float* part) {
   for (int i = 0; i < R; ++i) v[i] = R == 1 ? sum : __shfl_sync(0xffffffffu, sum, i * kGroup);
 }
 
+// s / n, rounded to nearest (Markstein, 1990: a product with the rounded
+// reciprocal, corrected by its exact remainder); infinities and NaN stay.
+__device__ __forceinline__ float quotient(float s, float n, float inv_n) {
+  const float q = s * inv_n;
+  const float nearest = fmaf(fmaf(-q, n, s), inv_n, q);
+  return fabsf(q) < __int_as_float(0x7f800000) ? nearest : q;
+}
+
 // Forward: a row (its sum with the residual, behind the dropout) is held in
 // fp32 registers, in pairs (one instruction for two columns). A warp takes the
 // mean of its part and the squares about that; parts of n_w elements are
 // joined by
 //   mu = sum n_w mu_w / C,  sum of squares = sum (q_w + n_w (mu_w - mu)^2),
 // which loses nothing to cancellation and costs one barrier a turn of R rows.
+// Means are quotients, not products with 1 / C: a row of equal values whose sums
+// are exact has that value as its mean, and y = beta. The root's reciprocal is the
+// hardware's, 2 steps of 2^-24 to 2^-23: rounded to nearest (__frsqrt_rn) the
+// forward takes 1 to 5 % longer (60000 x 333 31.6 us, 30.0).
 // ADD: with a residual, and z written.
-// Bound by HBM: 8192 x 4096 bf16 takes 23.3 us for 134 MB (5.8 TB/s), with
-// residual and dropout 48.2 us for 269 MB (5.5 TB/s; half of the cycles issue,
+// Bound by HBM: 8192 x 4096 bf16 takes 22.7 us for 134 MB (5.9 TB/s), with
+// residual and dropout 49.2 us for 269 MB (5.5 TB/s; half of the cycles issue,
 // and dropping costs 1 us of it). One row a turn took 3 us more, and three
 // blocks of 256 threads at 80 registers, not two at 128, 66 us with dropout and
 // the same without.
@@ -455,7 +467,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
   src[0] = a.x;
   if (ADD) src[NT - 1] = a.residual;
   Walk<T, S, STAGES, R, NT, RAGGED> w(ring, src, a.C, split);
-  const float inv_C = 1.0f / static_cast<float>(a.C);
+  const float C = static_cast<float>(a.C), inv_C = 1.0f / C;
   uint64_t gamma[VECS][P], beta[VECS][P];
   __shared__ __align__(16) float stages[RAGGED ? S::BLOCK / 32 : 1][32 * E];
   float* const stage = stages[RAGGED ? threadIdx.x / 32 : 0];
@@ -512,13 +524,12 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
       mu[k] = ptx::f2_lo(s2) + ptx::f2_hi(s2);
     }
     if (kWarps > 1 && N > 1) {
-      const float sum = warp_sums<N>(mu);
+      const float mean = quotient(warp_sums<N>(mu), count, inv_count);
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        mu[k] = __shfl_sync(0xffffffffu, sum, k * (32 / N)) * inv_count;
+      for (int k = 0; k < N; ++k) mu[k] = __shfl_sync(0xffffffffu, mean, k * (32 / N));
     } else {
 #pragma unroll
-      for (int k = 0; k < N; ++k) mu[k] = lane_sum<kLanes>(mu[k]) * inv_count;
+      for (int k = 0; k < N; ++k) mu[k] = quotient(lane_sum<kLanes>(mu[k]), count, inv_count);
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -567,7 +578,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
         p[i] = part[parity][first + i * kGroup];
         total = fmaf(n[i * kGroup], p[i].x, total);
       }
-      total = lane_sum<kGroup>(total) * inv_C;
+      total = quotient(lane_sum<kGroup>(total), C, inv_C);
 #pragma unroll
       for (int i = 0; i < kWarps / kGroup; ++i) {
         const float d = p[i].x - total, c = n[i * kGroup];
