@@ -17,8 +17,8 @@ __all__ = [
     "AttnError", "check", "library", "attn_fwd", "attn_fwd_ref", "attn_bwd_preprocess", "attn_bwd",
     "attn_bwd_finalize", "attn_bwd_noalloc", "attn_device_status", "attn_strerror",
     "attn_selftest_wait_timeout", "attn_bwd_dq_partials_bytes", "attn_bwd_deterministic",
-    "attn_bwd_finalize_partials", "attn_fwd_ref_dropout", "attn_bwd_dropout", "attn_fwd_local",
-    "attn_fwd_ref_local", "attn_bwd_local", "attn_fwd_dropout", "attn_rotary_frequencies",
+    "attn_bwd_finalize_partials", "attn_bwd_sum_partials", "attn_fwd_ref_dropout",
+    "attn_bwd_dropout", "attn_fwd_local", "attn_fwd_ref_local", "attn_bwd_local", "attn_fwd_dropout", "attn_rotary_frequencies",
     "attn_rotary", "attn_bwd_finalize_rotary", "attn_layer_norm", "attn_layer_norm_bwd",
     "attn_layer_norm_bwd_workspace_bytes", "attn_dropout_add", "attn_dropout_add_norm",
     "attn_dropout_add_norm_bwd", "ATTN_BF16", "ATTN_FP16", "ATTN_FP32", "ATTN_ROTARY_PLAIN",
@@ -64,6 +64,7 @@ _SIGNATURES = {
     "attn_bwd_deterministic": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F,
                                _P, _P],
     "attn_bwd_finalize_partials": [_P, _P, _F, _I, _I, _I, _I, _I, _P],
+    "attn_bwd_sum_partials": [_P, _P, _I, _I, _I, _I, _I, _P],
     "attn_fwd_ref_dropout": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _F,
                              ctypes.c_ulonglong, _P],
     "attn_bwd_dropout": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _P,
@@ -234,6 +235,11 @@ def attn_bwd_deterministic(q, k, v, o, dO, lse, dq_partials, dk, dv, B, H, H_kv,
 def attn_bwd_finalize_partials(dq_partials, dq, scale, B, H, N, d, causal, stream=None):
     return library().attn_bwd_finalize_partials(_ptr(dq_partials), _ptr(dq), scale, B, H, N, d,
                                                 int(causal), _stream(stream))
+
+
+def attn_bwd_sum_partials(dq_partials, dq_accum, B, H, N, d, causal, stream=None):
+    return library().attn_bwd_sum_partials(_ptr(dq_partials), _ptr(dq_accum), B, H, N, d,
+                                           int(causal), _stream(stream))
 
 
 def attn_rotary_frequencies(rot, base=10000.0, scaling=ATTN_ROTARY_PLAIN, factor=1.0,

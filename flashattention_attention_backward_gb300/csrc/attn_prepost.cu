@@ -13,7 +13,8 @@
 //  * finalize_partials (deterministic dQ): dq = bf16(tau * sum over key
 //    blocks n, in increasing n, of the stored partial tiles dS_mn K_n of
 //    query block m) ("反向传播算法详解" §6.4: a fixed order of the
-//    additions makes dQ reproducible bit for bit).
+//    additions makes dQ reproducible bit for bit); sum_partials leaves that
+//    sum in fp32, without tau, for a last step that does more than round.
 // Both grids are a multiple of the SM count and grid-stride over the rows.
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -154,10 +155,12 @@ __host__ __device__ inline long long pairs_per_head(int blocks, bool causal) {
 }
 
 // One thread per 4 consecutive dQ elements of a row: the partials of its
-// query block are added in increasing key-block order.
+// query block are added in increasing key-block order. Out: bf16 (with the
+// scale), or float (the sum itself).
+template <typename Out>
 __global__ void __launch_bounds__(kThreads)
-    finalize_partials_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ dq,
-                             float scale, long long rows, int N, int d, int blocks, int causal) {
+    finalize_partials_kernel(const float* __restrict__ part, Out* __restrict__ dq, float scale,
+                             long long rows, int N, int d, int blocks, int causal) {
   const long long n4 = rows * (d / 4);
   const long long stride = static_cast<long long>(gridDim.x) * kThreads;
   const long long P = pairs_per_head(blocks, causal != 0);
@@ -179,6 +182,10 @@ __global__ void __launch_bounds__(kThreads)
       acc.z += a.z;
       acc.w += a.w;
     }
+    if (sizeof(Out) == 4) {
+      reinterpret_cast<float4*>(dq)[i] = acc;
+      continue;
+    }
     __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * scale, acc.y * scale);
     __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * scale, acc.w * scale);
     uint2 u;
@@ -193,6 +200,24 @@ inline unsigned grid_for(long long work_items, int items_per_block) {
   const int sms = sm_count();
   const long long cap = static_cast<long long>(sms > 0 ? sms : 1) * 8;
   return static_cast<unsigned>(want < cap ? (want > 0 ? want : 1) : cap);
+}
+
+// The host side of the two calls on partials.
+template <typename Out>
+int finalize_partials(const float* dq_partials, void* dq, float scale, int B, int H, int N, int d,
+                      int causal, void* stream) {
+  if (!dq_partials || !dq) return ATTN_ERR_NULL;
+  int rc = check_shape(B, H, H > 0 ? 1 : 0, N, d);
+  if (rc != ATTN_OK) return rc;
+  if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale)) return ATTN_ERR_SHAPE;
+  if (!aligned16(dq_partials) || !aligned16(dq)) return ATTN_ERR_ALIGN;
+  const long long rows = static_cast<long long>(B) * H * N;
+  if (rows == 0) return ATTN_OK;
+  const unsigned grid = grid_for(rows * (d / 4), kThreads);
+  finalize_partials_kernel<<<grid, kThreads, 0, as_stream(stream)>>>(
+      dq_partials, static_cast<Out*>(dq), scale, rows, N, d, (N + 127) / 128, causal != 0 ? 1 : 0);
+  return launch_status();
 }
 
 }  // namespace prepost
@@ -260,17 +285,12 @@ extern "C" long long attn_bwd_dq_partials_bytes(int B, int H, int N, int d, int 
 
 extern "C" int attn_bwd_finalize_partials(const float* dq_partials, void* dq, float scale, int B,
                                           int H, int N, int d, int causal, void* stream) {
-  if (!dq_partials || !dq) return ATTN_ERR_NULL;
-  int rc = check_shape(B, H, H > 0 ? 1 : 0, N, d);
-  if (rc != ATTN_OK) return rc;
-  if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
-  if (!std::isfinite(scale)) return ATTN_ERR_SHAPE;
-  if (!aligned16(dq_partials) || !aligned16(dq)) return ATTN_ERR_ALIGN;
-  const long long rows = static_cast<long long>(B) * H * N;
-  if (rows == 0) return ATTN_OK;
-  const unsigned grid = prepost::grid_for(rows * (d / 4), prepost::kThreads);
-  prepost::finalize_partials_kernel<<<grid, prepost::kThreads, 0, as_stream(stream)>>>(
-      dq_partials, static_cast<__nv_bfloat16*>(dq), scale, rows, N, d, (N + 127) / 128,
-      causal != 0 ? 1 : 0);
-  return launch_status();
+  return prepost::finalize_partials<__nv_bfloat16>(dq_partials, dq, scale, B, H, N, d, causal,
+                                                   stream);
+}
+
+extern "C" int attn_bwd_sum_partials(const float* dq_partials, float* dq_accum, int B, int H,
+                                     int N, int d, int causal, void* stream) {
+  return prepost::finalize_partials<float>(dq_partials, dq_accum, 1.0f, B, H, N, d, causal,
+                                           stream);
 }

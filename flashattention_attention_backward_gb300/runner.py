@@ -17,7 +17,7 @@ from . import (ATTN_BF16, ATTN_FP16, ATTN_FP32, ATTN_ROTARY_BASE, ATTN_ROTARY_LI
                ATTN_ROTARY_PLAIN, ATTN_ROTARY_RAMP, attn_bwd, attn_bwd_deterministic,
                attn_bwd_dq_partials_bytes, attn_bwd_dropout, attn_bwd_finalize,
                attn_bwd_finalize_partials, attn_bwd_finalize_rotary, attn_bwd_local,
-               attn_bwd_preprocess, attn_dropout_add, attn_dropout_add_norm,
+               attn_bwd_preprocess, attn_bwd_sum_partials, attn_dropout_add, attn_dropout_add_norm,
                attn_dropout_add_norm_bwd, attn_fwd, attn_fwd_dropout, attn_fwd_local,
                attn_fwd_ref, attn_fwd_ref_dropout, attn_fwd_ref_local, attn_layer_norm,
                attn_layer_norm_bwd, attn_layer_norm_bwd_workspace_bytes, attn_rotary,
@@ -154,8 +154,9 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
     finalize_partials (dQ identical bit for bit from run to run). window =
     (left, right) runs attn_bwd_local in place of attn_bwd. rotary = the
     Rotary that q and k came from (with the same positions): dQ and dK are
-    then the gradients of what went into it (attn_bwd_finalize_rotary in
-    place of attn_bwd_finalize)."""
+    then the gradients of what went into it, each rounded once
+    (attn_bwd_finalize_rotary in place of attn_bwd_finalize, and behind
+    attn_bwd_sum_partials in the deterministic form)."""
     B, H, H_kv, N, d = _dims(q, k, v, o, do)
     if v.shape != k.shape or o.shape != q.shape or do.shape != q.shape:
         raise ValueError("v must have the shape of k, and o, dO that of q")
@@ -174,21 +175,20 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
         shape = (B, H, H_kv, N, d, scale, causal, softcap, bufs.dpsum)
         if deterministic and dropout is None:
             _deterministic_dq_dk_dv(q, k, v, o, do, lse, bufs, shape, s)
-            check(attn_bwd_finalize_partials(bufs.dq_partials, bufs.dq, scale, B, H, N, d, causal,
-                                             s))
-            if rotary is not None:
-                check(attn_rotary(bufs.dq, bufs.dk, bufs.dq, bufs.dk, rotary.turns, positions,
-                                  pos_stride, B, H, H_kv, N, d, rotary.rot, rotary.magnitude,
-                                  rotary.interleaved, True, ATTN_BF16, None, s))
-            return bufs.dq, bufs.dk, bufs.dv
-        check(attn_bwd_preprocess(o, do, bufs.dpsum, bufs.dq_accum, B, H, N, d, s))
-        tensors = (q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv)
-        if dropout is not None:
-            check(attn_bwd_dropout(*tensors, *shape, dropout[0], dropout[1], s))
-        elif window is not None:
-            check(attn_bwd_local(*tensors, *shape, window[0], window[1], s))
+            if rotary is None:
+                check(attn_bwd_finalize_partials(bufs.dq_partials, bufs.dq, scale, B, H, N, d,
+                                                 causal, s))
+                return bufs.dq, bufs.dk, bufs.dv
+            check(attn_bwd_sum_partials(bufs.dq_partials, bufs.dq_accum, B, H, N, d, causal, s))
         else:
-            check(attn_bwd(*tensors, *shape, s))
+            check(attn_bwd_preprocess(o, do, bufs.dpsum, bufs.dq_accum, B, H, N, d, s))
+            tensors = (q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv)
+            if dropout is not None:
+                check(attn_bwd_dropout(*tensors, *shape, dropout[0], dropout[1], s))
+            elif window is not None:
+                check(attn_bwd_local(*tensors, *shape, window[0], window[1], s))
+            else:
+                check(attn_bwd(*tensors, *shape, s))
         if rotary is None:
             check(attn_bwd_finalize(bufs.dq_accum, bufs.dq, scale, B, H, N, d, s))
         else:

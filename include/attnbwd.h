@@ -225,6 +225,13 @@ int attn_bwd_deterministic(const void* q, const void* k, const void* v, const vo
                            int causal, float softcap, const float* dpsum, void* stream);
 int attn_bwd_finalize_partials(const float* dq_partials, void* dq, float scale, int B, int H,
                                int N, int d, int causal, void* stream);
+/*
+ * attn_bwd_sum_partials: the same sum left in fp32 and without the factor tau,
+ * dq_accum [B,H,N,d] (overwritten): attn_bwd's accumulator in a fixed order of
+ * additions, for attn_bwd_finalize_rotary, which rounds once.
+ */
+int attn_bwd_sum_partials(const float* dq_partials, float* dq_accum, int B, int H, int N, int d,
+                          int causal, void* stream);
 
 /*
  * attn_bwd_finalize: dq = bf16(scale * dq_accum) ([FA-v1-bwd] eq. 7: the
@@ -333,8 +340,8 @@ int attn_rotary(const void* q, const void* k, void* q_out, void* k_out,
  * attn_bwd_finalize_rotary: attn_bwd_finalize for a backward whose q and k
  * came out of attn_rotary, with the adjoint of that call, in one launch:
  *   dq = bf16(R^T (scale * dq_accum)),  dk_out = bf16(R^T dk).
- * In:  dq_accum [B,H,N,d] fp32, dk [B,H_kv,N,d] bf16 (from attn_bwd and its
- *      forms), both contiguous; turns, positions, pos_stride, rot, magnitude,
+ * In:  dq_accum [B,H,N,d] fp32 (from attn_bwd and its forms, or from
+ *      attn_bwd_sum_partials), dk [B,H_kv,N,d] bf16, both contiguous; turns, positions, pos_stride, rot, magnitude,
  *      interleaved as given to attn_rotary.
  * Out: dq, dk_out bf16; dk_out may be dk if it is contiguous. strides: HOST
  *      array of 6 element strides, (batch, head, row) of dq and dk_out; NULL:
