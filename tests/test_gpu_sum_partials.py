@@ -36,14 +36,14 @@ def _summed(partials, B, H, N, d, causal):
     for m in range(M):
         for n in range(m + 1 if causal else M):
             tile = t[:, :, m * (m + 1) // 2 + n if causal else m * M + n]
-            out[:, :, m * 128:m * 128 + 128] += tile
-            size[:, :, m * 128:m * 128 + 128] += np.abs(tile)
+            out[:, :, m * 128:(m + 1) * 128] += tile
+            size[:, :, m * 128:(m + 1) * 128] += np.abs(tile)
     return out[:, :, :N], size[:, :, :N]
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("d,N,causal,interleaved", [(64, 200, True, True), (128, 300, True, False),
-                                                    (64, 257, False, False), (256, 130, True, True)])
+@pytest.mark.parametrize("d,N,causal,interleaved", [
+    (64, 200, True, True), (128, 300, True, False), (64, 257, False, False), (256, 130, True, True)])
 def test_deterministic_dq_is_rounded_once(d, N, causal, interleaved):
     """dQ against the 64-bit rotation of the call's own partial tiles. A sum over
     M key blocks is off by M u of its terms' magnitudes, the scale and the rotation
