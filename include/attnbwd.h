@@ -374,9 +374,11 @@ int attn_layer_norm(const void* x, const void* gamma, const void* beta, void* y,
  *   dgamma = sum over rows of dy h, dbeta = sum over rows of dy.
  * In:  dy, x [rows, C] dtype; gamma [C] wdtype or NULL (1); mean, rstd [rows].
  * Out: dx [rows, C] dtype (may be dy or x); dgamma, dbeta [C] wdtype,
- *      overwritten (either may be NULL: not wanted). They are summed in an
- *      order that depends on rows, C and the GPU's SM count alone: the same
- *      bits every time. rows = 0 gives zeros.
+ *      overwritten (either may be NULL: not wanted). They are summed in a fixed
+ *      order: the same call (rows, C, types, which optional arrays are given, on
+ *      the same kind of GPU) gives the same bits every time. The order differs
+ *      between calls that differ in these, and from that of
+ *      attn_dropout_add_norm_bwd. rows = 0 gives zeros.
  * workspace: attn_layer_norm_bwd_workspace_bytes(rows, C) bytes of device
  *      memory, whose contents need no preparation and mean nothing after; may
  *      be NULL if dgamma and dbeta are. Calls that may run at the same time

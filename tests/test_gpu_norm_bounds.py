@@ -252,3 +252,26 @@ def test_equal_values(C, dtype):
     z, y, mean, _ = runner.dropout_add_norm(half, half, gamma, beta, 1e-5)
     assert torch.equal(z, x) and torch.equal(mean, v.float())
     assert torch.equal(y, beta.expand_as(y))
+
+
+@pytest.mark.parametrize("dtype", [F4, BF])
+@pytest.mark.parametrize("rows,C", [(256, 64), (257, 64), (400, 64), (512, 64), (513, 64),
+                                    (129, 128), (300, 1001), (700, 4096)])
+def test_weight_gradients_repeat(rows, C, dtype):
+    """The same call, the same bits, at row counts where the joined form and the
+    plain one choose different grids; between the forms only the order of a
+    column's additions differs."""
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    dy, dz, z = (torch.randn(rows, C, generator=g, device=DEV).to(dtype) for _ in range(3))
+    gamma, _ = _weights(C, F4)
+    _, mean, rstd = runner.layer_norm(z)
+    plain = runner.layer_norm_backward(dy, z, gamma, mean, rstd)
+    h = (_np(z) - _np(mean)[:, None]) * _np(rstd)[:, None]
+    size = np.stack((np.abs(_np(dy) * h).sum(0), np.abs(_np(dy)).sum(0)))
+    for extra, p in ((None, 0.0), (dz, 0.0), (dz, 0.3)):
+        args = (dy, extra, z, gamma, mean, rstd, (p, 5))
+        one, two = (runner.dropout_add_norm_backward(*args) for _ in range(2))
+        assert all(torch.equal(a, b) for a, b in zip(one, two))
+        # two orders of at most rows + 4 roundings a term each
+        for a, b, s in zip(one[2:], plain[1:], size):
+            assert (np.abs(_np(a) - _np(b)) <= 2 * (rows + 4) * U * s).all()
