@@ -66,25 +66,30 @@ class _On:
 
     def __init__(self, stream, device):
         current = torch.cuda.current_stream(device)
-        if stream is None:
-            stream = current
-        elif not isinstance(stream, torch.cuda.Stream):
-            handle = stream if isinstance(stream, int) else stream.cuda_stream
-            stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
-                torch.cuda.default_stream(device)
-        if stream.device != device:
-            raise ValueError("the stream is on %s, the tensors are on %s" % (stream.device, device))
-        self.stream = stream
-        self.caller = None if stream == current else current
-        self._context = torch.cuda.device(device) if self.caller is None else \
-            torch.cuda.stream(stream)
+        self.stream, self.caller, self._context = current, None, None
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                handle = stream if isinstance(stream, int) else stream.cuda_stream
+                stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
+                    torch.cuda.default_stream(device)
+            if stream.device != device:
+                raise ValueError("the stream is on %s, the tensors are on %s"
+                                 % (stream.device, device))
+            if stream != current:
+                self.stream, self.caller = stream, current
+                self._context = torch.cuda.stream(stream)
+                return
+        if torch.cuda.current_device() != device.index:
+            self._context = torch.cuda.device(device)
 
     def __enter__(self):
-        self._context.__enter__()
+        if self._context is not None:
+            self._context.__enter__()
         return self
 
     def __exit__(self, *exc):
-        return self._context.__exit__(*exc)
+        if self._context is not None:
+            self._context.__exit__(*exc)
 
     def made(self, *tensors):
         """Tells torch's allocator that the stream current at the call may use
@@ -168,13 +173,13 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
     if dropout is None and window is not None and deterministic:
         raise ValueError("the local window has no deterministic variant")
     with _On(stream, q.device) as on:
-        s = on.stream
-        if bufs is None:
+        s, kept = on.stream, bufs is not None
+        if not kept:
             bufs = BackwardBuffers(q, k)
             on.made(bufs.dq, bufs.dk, bufs.dv)
         shape = (B, H, H_kv, N, d, scale, causal, softcap, bufs.dpsum)
         if deterministic and dropout is None:
-            _deterministic_dq_dk_dv(q, k, v, o, do, lse, bufs, shape, s)
+            _deterministic_dq_dk_dv(q, k, v, o, do, lse, bufs, kept, shape, s)
             if rotary is None:
                 check(attn_bwd_finalize_partials(bufs.dq_partials, bufs.dq, scale, B, H, N, d,
                                                  causal, s))
@@ -199,8 +204,9 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
         return bufs.dq, bufs.dk, bufs.dv
 
 
-def _deterministic_dq_dk_dv(q, k, v, o, do, lse, bufs, shape, s):
-    """dQ's partial tiles, dK and dV; the partials' buffer grows with the problem."""
+def _deterministic_dq_dk_dv(q, k, v, o, do, lse, bufs, kept, shape, s):
+    """dQ's partial tiles, dK and dV; the partials' buffer grows with the problem
+    (kept: it outlives the call)."""
     B, H, _, N, d, _, causal = shape[:7]
     nbytes = attn_bwd_dq_partials_bytes(B, H, N, d, causal)
     if nbytes < 0:
@@ -208,7 +214,8 @@ def _deterministic_dq_dk_dv(q, k, v, o, do, lse, bufs, shape, s):
     partials = getattr(bufs, "dq_partials", None)
     if partials is None or partials.numel() * 4 < nbytes:
         bufs.dq_partials = torch.empty(max(nbytes // 4, 4), dtype=torch.float32, device=q.device)
-    bufs.dq_partials.record_stream(s)  # a later call's larger one may replace it
+    if kept:  # a later call's larger one may replace it
+        bufs.dq_partials.record_stream(s)
     check(attn_bwd_preprocess(o, do, bufs.dpsum, None, B, H, N, d, s))
     check(attn_bwd_deterministic(q, k, v, o, do, lse, bufs.dq_partials, bufs.dk, bufs.dv, *shape,
                                  s))

@@ -38,6 +38,7 @@ def fake(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: streams[-1])
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     for name in ("empty", "empty_like"):
         def make(*args, _of=getattr(torch, name), **kwargs):
             t = _of(*args, **kwargs)
