@@ -140,16 +140,19 @@ class BackwardBuffers:
     will use them, by default the current one."""
 
     def __init__(self, q, k, stream=None):
-        B, H, H_kv, N, d = _dims(q, k)
-        dev = q.device
-        with _On(stream, dev) as on:
-            self.dq = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
-            self.dk = torch.empty((B, H_kv, N, d), dtype=torch.bfloat16, device=dev)
-            self.dv = torch.empty((B, H_kv, N, d), dtype=torch.bfloat16, device=dev)
-            self.dq_accum = torch.empty((B, H, N, d), dtype=torch.float32, device=dev)
-            self.dpsum = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+        dims = _dims(q, k)
+        with _On(stream, q.device) as on:
+            self._allocate(*dims, q.device)
             on.made(self.dq, self.dk, self.dv, self.dq_accum, self.dpsum)
+
+    def _allocate(self, B, H, H_kv, N, d, dev):
+        self.dq = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
+        self.dk = torch.empty((B, H_kv, N, d), dtype=torch.bfloat16, device=dev)
+        self.dv = torch.empty((B, H_kv, N, d), dtype=torch.bfloat16, device=dev)
+        self.dq_accum = torch.empty((B, H, N, d), dtype=torch.float32, device=dev)
+        self.dpsum = torch.empty((B, H, N), dtype=torch.float32, device=dev)
         self.dq_partials = None  # of the deterministic form, made by its first call
+        return self
 
 
 def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=None,
@@ -175,7 +178,7 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
     with _On(stream, q.device) as on:
         s, kept = on.stream, bufs is not None
         if not kept:
-            bufs = BackwardBuffers(q, k)
+            bufs = object.__new__(BackwardBuffers)._allocate(B, H, H_kv, N, d, q.device)
             on.made(bufs.dq, bufs.dk, bufs.dv)
         shape = (B, H, H_kv, N, d, scale, causal, softcap, bufs.dpsum)
         if deterministic and dropout is None:
