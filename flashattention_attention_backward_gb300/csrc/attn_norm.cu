@@ -40,9 +40,10 @@ inline Drop make_drop(float p, unsigned long long seed) {
 // generator call per 4 elements) are drawn behind them, and only then are the
 // loads waited for (with their elements widened before, 8192 x 4096 bf16 with a
 // residual took 48 us, not 32: 6.3 TB/s). Two groups a thread measured the
-// same. Without a residual the generator's multiplies bound it: a call has 19
-// of 32 x 32 to 64 bits, which issue every fourth cycle, and the kernel draws
-// 1.1e12 words a second of the 1.6e12 of a loop that does nothing else.
+// same. Without a residual (29.9 us, floor 20) the generator's multiplies count as
+// much as HBM: a call has 19 of 32 x 32 to 64 bits, which issue every fourth
+// cycle, and the kernel draws 1.1e12 words a second of the 1.6e12 of a loop that
+// does nothing else; multiplies and loads overlap in part.
 constexpr int kDropThreads = 128;
 
 template <typename T, bool DROP>

@@ -445,7 +445,7 @@ __device__ __forceinline__ float quotient(float s, float n, float inv_n) {
 // forward takes 1 to 5 % longer (60000 x 333 31.6 us, 30.0).
 // ADD: with a residual, and z written.
 // Bound by HBM: 8192 x 4096 bf16 takes 22.7 us for 134 MB (5.9 TB/s), with
-// residual and dropout 49.2 us for 269 MB (5.5 TB/s; half of the cycles issue,
+// residual and dropout 49.1 us for 269 MB (5.5 TB/s; half of the cycles issue,
 // and dropping costs 1 us of it). One row a turn took 3 us more, and three
 // blocks of 256 threads at 80 registers, not two at 128, 66 us with dropout and
 // the same without.
@@ -629,9 +629,9 @@ __global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
 // weights' gradients, whose column sums stay in registers over all of the
 // thread's rows; then, with the sums joined over the rows' threads, the rows'
 // gradients, from the ring again. DZ: with a dz to add.
-// 8192 x 4096 bf16: 36.3 us for 201 MB, of which 31.6 the rows' gradients (6.4
+// 8192 x 4096 bf16: 36.8 us for 201 MB, of which 31.6 the rows' gradients (6.4
 // TB/s) and the rest the weights' (their second stage, and the partial sums);
-// with dz and dropout 58.4 us for 336 MB (5.8 TB/s), bound by issue and the
+// with dz and dropout 58.5 us for 336 MB (5.8 TB/s), bound by issue and the
 // multiply pipe (59 % of the cycles issue) about as much as by HBM. A row at a
 // time took 45 and 69 us; 64 registers for twice the threads 44 and 82.
 template <typename T, typename S, int STAGES, int R, bool DZ, bool DROP, bool RAGGED>
@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 8) fwd_wide_kernel(FwdArgs a) {
 
 // The same of the backward, with the statistics given; its roundings are written
 // out, so that they do not depend on which of the outputs are wanted. 1024 x
-// 32768 bf16 with the weights' gradients: 201 us (floor 30).
+// 32768 bf16 with the weights' gradients: 204 us (floor 30).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 8) bwd_wide_kernel(BwdArgs a) {
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -1035,7 +1035,7 @@ inline unsigned grid_for(long long want) {
 
 // f(Shape) for the row length: up to 16 elements a thread, so that weights and
 // the backward's sums stay in registers. The widest rows take a cluster of two
-// blocks for it (2048 x 16384 bf16: forward 40 us, backward 67 us; with one
+// blocks for it (2048 x 16384 bf16: forward 40 us, backward 58 us; with one
 // block and 32 elements a thread 45 and 72 us, with the weights read again for
 // each row 44 and 97 us). Blocks have at least LEAST threads.
 template <typename T, int LEAST, bool BACKWARD, typename F>
