@@ -173,3 +173,25 @@ def test_gradients_far_from_zero(C, kind, dtype):
         terms = np.abs(_np(dy)) * (h + eh)
         _within("dgamma", dgamma, dg, 8 * U * terms.sum(0))
         _within("dbeta", dbeta, db, 2 * U * np.abs(_np(dy)).sum(0))
+
+
+def test_offsets_past_32_bits():
+    """33 rows of 2^26 columns: the last begins 2^31 elements behind the first."""
+    rows, C = 33, 1 << 26
+    x = torch.empty(rows, C, dtype=BF, device=DEV)
+    ramp = (torch.arange(4096, device=DEV) % 256).to(BF).repeat(C // 4096)
+    x[:] = ramp
+    x[-1] = -2 * ramp
+    y, mean, rstd = runner.layer_norm(x)
+    # 256 values of equal number: mean 127.5, variance (256^2 - 1) / 12
+    D = 54 + C / 2 ** 19
+    for row, f in ((0, 1), (17, 1), (32, -2)):
+        sd = np.sqrt(f * f * (256 ** 2 - 1) / 12 + EPS)
+        assert abs(float(mean[row]) - f * 127.5) <= 2 * U * abs(f) * 127.5 + (D + 3) * U * sd
+        assert abs(float(rstd[row]) * sd - 1) <= (D + 12) * U
+        want = f * (np.arange(256) - 127.5) / sd
+        _within("y", y[row, -256:], want, (D + 16) * U * np.abs(want) + 4 * U)
+    dx, _, _ = runner.layer_norm_backward(y, x, None, mean, rstd, weight_grads=False)
+    # dy = y is h: g - mean(g) - h mean(g h) = 0 but for y's rounding to bf16
+    h = np.abs(_np(y[-1, :256]))
+    assert (np.abs(_np(dx[-1, -256:])) <= 2 * float(rstd[-1]) * 2.0 ** -8 * (h + h.max())).all()

@@ -203,3 +203,37 @@ def test_stream_handles():
         y = runner.layer_norm(x, stream=stream)[0]
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.gpu
+def test_captured_on_a_joined_stream():
+    """A call on another stream inside a capture that forks to it and joins it
+    again; its memory belongs to the graph, and replays follow new contents."""
+    dev = torch.device("cuda:0")
+    x, dy = (torch.randn(300, 1024, device=dev).to(BF) for _ in range(2))
+    w = torch.ones(1024, device=dev)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    runner.layer_norm_backward(dy, x, w, *runner.layer_norm(x, w, w)[1:])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        t = runner.dropout_add(x, dy)
+        side.wait_stream(main)
+        y, mean, rstd = runner.layer_norm(t, w, w, stream=side)
+        dx, dgamma, dbeta = runner.layer_norm_backward(dy, t, w, mean, rstd, stream=side)
+        main.wait_stream(side)
+        out = runner.dropout_add(dx, y)
+        # dropped inside the capture, used again by what follows it
+        del t, dx
+        last = runner.dropout_add(out, y)
+    for scale in (1.0, 0.5):
+        x.mul_(scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        t2 = runner.dropout_add(x, dy)
+        y2, m2, r2 = runner.layer_norm(t2, w, w)
+        dx2, dg2, db2 = runner.layer_norm_backward(dy, t2, w, m2, r2)
+        out2 = runner.dropout_add(dx2, y2)
+        for a, b in ((y, y2), (dgamma, dg2), (dbeta, db2), (out, out2),
+                     (last, runner.dropout_add(out2, y2))):
+            assert torch.equal(a, b)
