@@ -137,7 +137,8 @@ def forward(q, k, v, scale, causal, softcap=0.0, stream=None, impl="tc", dropout
 class BackwardBuffers:
     """Outputs and scratch of one backward problem, reusable across calls
     (calls that may run at the same time need their own). `stream`: the one that
-    will use them, by default the current one."""
+    will use them, by default the current one; a call on another stream has to be
+    ordered behind it first, as with any tensor made there."""
 
     def __init__(self, q, k, stream=None):
         dims = _dims(q, k)
