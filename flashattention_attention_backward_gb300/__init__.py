@@ -18,7 +18,9 @@ __all__ = [
     "attn_bwd_finalize", "attn_bwd_noalloc", "attn_device_status", "attn_strerror",
     "attn_selftest_wait_timeout", "attn_bwd_dq_partials_bytes", "attn_bwd_deterministic",
     "attn_bwd_finalize_partials", "attn_bwd_sum_partials", "attn_fwd_ref_dropout",
-    "attn_bwd_dropout", "attn_fwd_local", "attn_fwd_ref_local", "attn_bwd_local", "attn_fwd_dropout", "attn_rotary_frequencies",
+    "attn_bwd_dropout", "attn_fwd_local", "attn_fwd_ref_local", "attn_bwd_local",
+    "attn_fwd_sinks", "attn_fwd_ref_sinks", "attn_bwd_sinks", "attn_fwd_dropout",
+    "attn_rotary_frequencies",
     "attn_rotary", "attn_bwd_finalize_rotary", "attn_layer_norm", "attn_layer_norm_bwd",
     "attn_layer_norm_bwd_workspace_bytes", "attn_dropout_add", "attn_dropout_add_norm",
     "attn_dropout_add_norm_bwd", "ATTN_BF16", "ATTN_FP16", "ATTN_FP32", "ATTN_ROTARY_PLAIN",
@@ -76,6 +78,10 @@ _SIGNATURES = {
     "attn_fwd_ref_local": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _I, _I, _P],
     "attn_bwd_local": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _P,
                        _I, _I, _P],
+    "attn_fwd_sinks": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _I, _I, _I, _P],
+    "attn_fwd_ref_sinks": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _I, _I, _I, _P],
+    "attn_bwd_sinks": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _F, _P,
+                       _I, _I, _I, _P],
     "attn_rotary_frequencies": [ctypes.POINTER(_U), ctypes.POINTER(_F), _I, _D, _I, _D, _I, _D,
                                 _D],
     "attn_rotary": [_P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P, _P],
@@ -219,6 +225,29 @@ def attn_bwd_local(q, k, v, o, dO, lse, dq_accum, dk, dv, B, H, H_kv, N, d, scal
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(dq_accum), _ptr(dk),
         _ptr(dv), B, H, H_kv, N, d, scale, int(causal), softcap, _ptr(dpsum), int(window_left),
         int(window_right), _stream(stream))
+
+
+def attn_fwd_sinks(q, k, v, o, lse, B, H, H_kv, N, d, scale, causal, softcap, window_left,
+                   window_right, sinks, stream=None):
+    return library().attn_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, H_kv, N,
+                                    d, scale, int(causal), softcap, int(window_left),
+                                    int(window_right), int(sinks), _stream(stream))
+
+
+def attn_fwd_ref_sinks(q, k, v, o, lse, B, H, H_kv, N, d, scale, causal, softcap, window_left,
+                       window_right, sinks, stream=None):
+    return library().attn_fwd_ref_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H,
+                                        H_kv, N, d, scale, int(causal), softcap,
+                                        int(window_left), int(window_right), int(sinks),
+                                        _stream(stream))
+
+
+def attn_bwd_sinks(q, k, v, o, dO, lse, dq_accum, dk, dv, B, H, H_kv, N, d, scale, causal,
+                   softcap, dpsum, window_left, window_right, sinks, stream=None):
+    return library().attn_bwd_sinks(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(dq_accum), _ptr(dk),
+        _ptr(dv), B, H, H_kv, N, d, scale, int(causal), softcap, _ptr(dpsum), int(window_left),
+        int(window_right), int(sinks), _stream(stream))
 
 
 def attn_bwd_dq_partials_bytes(B, H, N, d, causal):

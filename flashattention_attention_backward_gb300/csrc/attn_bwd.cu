@@ -141,10 +141,9 @@ struct Params {
   Dropout drop; // kernel template flag DROP: keep mask of philox.cuh
   float scale;
   float softcap;
-  // visibility band: key j is visible to query i iff
-  // i - win_left <= j <= i + win_right (the causal mask is win_right = 0;
-  // an unbounded side holds N)
-  int win_left, win_right;
+  // key j is visible to query i iff j <= i + win_right and
+  // (j >= i - win_left or j < sinks) (see Band)
+  int win_left, win_right, sinks;
 };
 
 // One unit of work: a block of 128 keys of one KV head of one batch entry,
@@ -166,8 +165,9 @@ __device__ __forceinline__ int unit_of(int r, int n_units) {
 }
 
 // The query blocks a key block meets are those holding a query of its
-// visibility band: queries n0 - win_right .. n0 + 127 + win_left. The band
-// always holds the diagonal, so every unit has at least one tile per head.
+// visibility band: queries n0 - win_right .. n0 + 127 + win_left, or all from
+// n0 - win_right on if the block holds sinks. The band always holds the
+// diagonal, so every unit has at least one tile per head.
 __device__ __forceinline__ void unit_work(const Params& p, int u, Work& w) {
   const int per_nb = p.H_kv * p.B;
   w.n_block = u / per_nb;
@@ -177,7 +177,8 @@ __device__ __forceinline__ void unit_work(const Params& p, int u, Work& w) {
   w.G = p.H / p.H_kv;
   const int n0 = w.n_block * kBc;
   w.m_start = max(0, n0 - p.win_right) / kBr;
-  const int m_end = min(p.m_blocks - 1, (n0 + kBc - 1 + p.win_left) / kBr);
+  const int m_end =
+      n0 < p.sinks ? p.m_blocks - 1 : min(p.m_blocks - 1, (n0 + kBc - 1 + p.win_left) / kBr);
   w.per_head = m_end - w.m_start + 1;
   w.T = w.G * w.per_head;
 }
@@ -185,8 +186,8 @@ __device__ __forceinline__ void unit_work(const Params& p, int u, Work& w) {
 // A tile needs the elementwise mask unless every (query, key) pair in it is
 // inside the band and inside the sequence.
 __device__ __forceinline__ bool tile_masked(const Params& p, int m0, int n0) {
-  return n0 + kBc - 1 - m0 > p.win_right || m0 + kBr - 1 - n0 > p.win_left || n0 + kBc > p.N ||
-         m0 + kBr > p.N;
+  return n0 + kBc - 1 - m0 > p.win_right || n0 + kBc > p.N || m0 + kBr > p.N ||
+         (m0 + kBr - 1 - n0 > p.win_left && n0 + kBc > p.sinks);
 }
 
 struct Ctx {
@@ -552,6 +553,7 @@ __device__ __forceinline__ bool softmax_tile(const Ctx& c, const Params& p, uint
   // phase), for this thread's 64 columns as 32 pairs
   uint64_t pk[32];
   uint32_t km[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // dropout keep bits of the 64 columns
+  const int left = key < p.sinks ? p.N : p.win_left;  // how far back this key is seen
 
   // ---- P = exp(S - LSE) -> bf16 P^T in tensor memory
   if (!wait(c, BAR_S_FULL, t & 1)) return false;
@@ -616,7 +618,7 @@ __device__ __forceinline__ bool softmax_tile(const Ctx& c, const Params& p, uint
           if (MASKED) {
             const int q = m0 + half * 64 + pass * kCols + j + h2;
             const bool ok =
-                key < p.N && q < p.N && key - q <= p.win_right && q - key <= p.win_left;
+                key < p.N && q < p.N && key - q <= p.win_right && q - key <= left;
             pr[h2] = ok ? pr[h2] : 0.f;
             kp[h2] = ok ? kp[h2] : 0.f;
           }
@@ -1105,19 +1107,20 @@ int dispatch(const Maps& m, const Params& p, cudaStream_t s, int d, bool cs, boo
 int run(const void* q, const void* k, const void* v, const void* dO, const float* lse,
         float* dq_target, void* dk, void* dv, int B, int H, int H_kv, int N, int d, float scale,
         int causal, float softcap, const float* dpsum, void* stream, bool det, float p_drop = 0.f,
-        unsigned long long seed = 0, int window_left = -1, int window_right = -1,
+        unsigned long long seed = 0, int window_left = -1, int window_right = -1, int sinks = 0,
         int (*before_launch)(void*) = nullptr, void* before_ctx = nullptr) {
   if (!q || !k || !v || !dO || !lse || !dq_target || !dk || !dv || !dpsum) return ATTN_ERR_NULL;
   int rc = check_shape(B, H, H_kv, N, d);
   if (rc != ATTN_OK) return rc;
   if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;  // d = 256: its own kernel
   if (!std::isfinite(scale) || scale == 0.f || std::isnan(softcap)) return ATTN_ERR_SHAPE;
-  if (!(p_drop >= 0.f && p_drop < 1.f)) return ATTN_ERR_SHAPE;
+  if (!(p_drop >= 0.f && p_drop < 1.f) || sinks < 0) return ATTN_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dO) || !aligned16(lse) ||
       !aligned16(dq_target) || !aligned16(dk) || !aligned16(dv) || !aligned16(dpsum))
     return ATTN_ERR_ALIGN;
   if (B == 0 || H == 0 || N == 0) return ATTN_OK;
   if (d == 256 && before_launch != nullptr) return ATTN_ERR_UNSUPPORTED;
+  const Band band = band_of(N, causal, window_left, window_right, sinks);
   if (d == 256) {
     // dQ partials: one tile of 128 query rows per (query block, key block)
     // pair, as for d <= 128
@@ -1125,8 +1128,8 @@ int run(const void* q, const void* k, const void* v, const void* dO, const float
     const long long pairs256 = causal ? mb * (mb + 1) / 2 : mb * nb;
     if (det && static_cast<long long>(B) * H * pairs256 > 0x7fffffffLL) return ATTN_ERR_TOO_LARGE;
     return bwd256_run(q, k, v, dO, lse, dq_target, dk, dv, B, H, H_kv, N, scale, causal, softcap,
-                      dpsum, window_left, window_right, det, static_cast<int>(pairs256), p_drop,
-                      seed, as_stream(stream));
+                      dpsum, band, det, static_cast<int>(pairs256), p_drop, seed,
+                      as_stream(stream));
   }
 
   Params p;
@@ -1149,10 +1152,9 @@ int run(const void* q, const void* k, const void* v, const void* dO, const float
   p.scale = scale;
   const bool cap = softcap > 0.f;
   p.softcap = cap ? softcap : 0.f;
-  // a negative or wider-than-N side of the window is unbounded (N); the
-  // causal mask bounds the right side at 0
-  p.win_left = (window_left < 0 || window_left > N) ? N : window_left;
-  p.win_right = causal ? 0 : ((window_right < 0 || window_right > N) ? N : window_right);
+  p.win_left = band.left;
+  p.win_right = band.right;
+  p.sinks = band.sinks;
   const bool drop = p_drop > 0.f;
   p.drop.seed_lo = static_cast<uint32_t>(seed);
   p.drop.seed_hi = static_cast<uint32_t>(seed >> 32);
@@ -1216,6 +1218,16 @@ extern "C" int attn_bwd_local(const void* q, const void* k, const void* v, const
                   dpsum, stream, false, 0.f, 0, window_left, window_right);
 }
 
+extern "C" int attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o,
+                              const void* dO, const float* lse, float* dq_accum, void* dk,
+                              void* dv, int B, int H, int H_kv, int N, int d, float scale,
+                              int causal, float softcap, const float* dpsum, int window_left,
+                              int window_right, int sinks, void* stream) {
+  (void)o;
+  return bwd::run(q, k, v, dO, lse, dq_accum, dk, dv, B, H, H_kv, N, d, scale, causal, softcap,
+                  dpsum, stream, false, 0.f, 0, window_left, window_right, sinks);
+}
+
 extern "C" int attn_bwd_deterministic(const void* q, const void* k, const void* v,
                                       const void* o, const void* dO, const float* lse,
                                       float* dq_partials, void* dk, void* dv, int B, int H,
@@ -1233,7 +1245,7 @@ int bwd_run_hooked(const void* q, const void* k, const void* v, const void* dO, 
                    float scale, int causal, float softcap, const float* dpsum, void* stream,
                    int (*before_launch)(void*), void* ctx) {
   return bwd::run(q, k, v, dO, lse, dq_accum, dk, dv, B, H, H_kv, N, d, scale, causal, softcap,
-                  dpsum, stream, false, 0.f, 0, -1, -1, before_launch, ctx);
+                  dpsum, stream, false, 0.f, 0, -1, -1, 0, before_launch, ctx);
 }
 
 }  // namespace attn

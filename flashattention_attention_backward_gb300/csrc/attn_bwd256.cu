@@ -132,9 +132,9 @@ struct Params {
   int m_blocks;  // blocks of 64 queries
   float scale;
   float softcap;
-  // key j is visible to query i iff i - win_left <= j <= i + win_right (the
-  // causal mask is win_right = 0; an unbounded side holds N)
-  int win_left, win_right;
+  // key j is visible to query i iff j <= i + win_right and
+  // (j >= i - win_left or j < sinks) (see Band)
+  int win_left, win_right, sinks;
   // DET: dQ tiles go to partials [B*H*pairs, 128, 256]; the pair of query
   // block m (128 rows) and key block n is m (m + 1) / 2 + n (causal) or
   // m * n_blocks + n, and a 64-query tile fills rows (m0 mod 128) .. + 63
@@ -161,7 +161,8 @@ __device__ __forceinline__ Work work_of(const Params& p) {
   w.G = p.H / p.H_kv;
   const int n0 = w.n_block * kBc;
   w.m_start = max(0, n0 - p.win_right) / kBr;
-  const int m_end = min(p.m_blocks - 1, (n0 + kBc - 1 + p.win_left) / kBr);
+  const int m_end =
+      n0 < p.sinks ? p.m_blocks - 1 : min(p.m_blocks - 1, (n0 + kBc - 1 + p.win_left) / kBr);
   w.per_head = m_end - w.m_start + 1;  // >= 1: the band holds the diagonal
   w.T = w.G * w.per_head;
   return w;
@@ -211,8 +212,8 @@ __device__ __forceinline__ void wait_drain(const Ctx& c, int bar, uint32_t parit
 }
 
 __device__ __forceinline__ bool tile_masked(const Params& p, int m0, int n0) {
-  return n0 + kBc - 1 - m0 > p.win_right || m0 + kBr - 1 - n0 > p.win_left || n0 + kBc > p.N ||
-         m0 + kBr > p.N;
+  return n0 + kBc - 1 - m0 > p.win_right || n0 + kBc > p.N || m0 + kBr > p.N ||
+         (m0 + kBr - 1 - n0 > p.win_left && n0 + kBc > p.sinks);
 }
 
 // ------------------------------------------------------------------ producer
@@ -449,7 +450,8 @@ __device__ __forceinline__ void softmax_tile(const Params& p, uint8_t* smem, uin
           for (int e = 0; e < 2; ++e) {
             const int q = m0 + j + e;
             const bool ok =
-                key < p.N && q < p.N && key - q <= p.win_right && q - key <= p.win_left;
+                key < p.N && q < p.N && key - q <= p.win_right &&
+                q - key <= (key < p.sinks ? p.N : p.win_left);
             pr[e] = ok ? pr[e] : 0.f;
             kp[e] = ok ? kp[e] : 0.f;
           }
@@ -808,8 +810,8 @@ int bwd256_status(int* status, bool clear) {
 // workspace (`pairs` tiles per query head), else the dQ accumulator.
 int bwd256_run(const void* q, const void* k, const void* v, const void* dO, const float* lse,
                float* dq_target, void* dk, void* dv, int B, int H, int H_kv, int N, float scale,
-               int causal, float softcap, const float* dpsum, int window_left, int window_right,
-               bool det, int pairs, float p_drop, unsigned long long seed, cudaStream_t s) {
+               int causal, float softcap, const float* dpsum, const Band& band, bool det,
+               int pairs, float p_drop, unsigned long long seed, cudaStream_t s) {
   using namespace bwd256;
   Params p;
   p.lse = lse;
@@ -823,8 +825,9 @@ int bwd256_run(const void* q, const void* k, const void* v, const void* dO, cons
   p.scale = scale;
   const bool cap = softcap > 0.f;
   p.softcap = cap ? softcap : 0.f;
-  p.win_left = (window_left < 0 || window_left > N) ? N : window_left;
-  p.win_right = causal ? 0 : ((window_right < 0 || window_right > N) ? N : window_right);
+  p.win_left = band.left;
+  p.win_right = band.right;
+  p.sinks = band.sinks;
   p.pairs = pairs;
   p.causal = causal != 0 ? 1 : 0;
   p.drop.seed_lo = static_cast<uint32_t>(seed);

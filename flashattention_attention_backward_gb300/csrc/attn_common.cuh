@@ -125,6 +125,21 @@ inline bool encode_f32_3d(CUtensorMap* map, const void* base, int d, int rows, l
   return r == CUDA_SUCCESS;
 }
 
+// Bounds of the visibility mask as the kernels take them: key j is visible to
+// query i iff j <= i + right and (j >= i - left or j < sinks). A negative or
+// wider-than-N side of the window is unbounded (N); the causal mask bounds the
+// right side at 0; without a left bound the first keys need no exception.
+struct Band {
+  int left, right, sinks;
+};
+inline Band band_of(int N, int causal, int window_left, int window_right, int sinks) {
+  Band b;
+  b.left = (window_left < 0 || window_left > N) ? N : window_left;
+  b.right = causal ? 0 : ((window_right < 0 || window_right > N) ? N : window_right);
+  b.sinks = b.left >= N ? 0 : (sinks < N ? sinks : N);
+  return b;
+}
+
 // Dropout threshold and scale for drop probability p in (0, 1): a 32-bit
 // word keeps its element iff word >= round(p * 2^32).
 inline uint32_t dropout_threshold(float p) {
@@ -147,8 +162,8 @@ int bwd256_status(int* status, bool clear);
 // partials workspace of `pairs` tiles per query head, else the accumulator.
 int bwd256_run(const void* q, const void* k, const void* v, const void* dO, const float* lse,
                float* dq_target, void* dk, void* dv, int B, int H, int H_kv, int N, float scale,
-               int causal, float softcap, const float* dpsum, int window_left, int window_right,
-               bool det, int pairs, float p_drop, unsigned long long seed, cudaStream_t s);
+               int causal, float softcap, const float* dpsum, const Band& band, bool det,
+               int pairs, float p_drop, unsigned long long seed, cudaStream_t s);
 
 // attn_bwd (d = 64 or 128) with a hook: before_launch(ctx) runs after every
 // argument check and tensor-map encoding has passed and right before the main

@@ -139,10 +139,9 @@ struct Params {
   int tiles;  // query tiles per head (blocks of 128 queries)
   float scale;
   float softcap;
-  // visibility band: key j is visible to query i iff
-  // i - win_left <= j <= i + win_right (the causal mask is win_right = 0;
-  // an unbounded side holds N)
-  int win_left, win_right;
+  // key j is visible to query i iff j <= i + win_right and
+  // (j >= i - win_left or j < sinks) (see Band)
+  int win_left, win_right, sinks;
   Dropout drop;  // kernel template flag DROP: keep mask of philox.cuh
 };
 
@@ -194,7 +193,11 @@ __device__ __forceinline__ void wait_drain(const Ctx& c, int bar, uint32_t parit
 // block across the CTA's tiles (global block index g), the per-tile ones one
 // phase per tile.
 struct Tile {
-  int bh, kvh, m0, j0, nt;
+  int bh, kvh, m0;
+  // its nt key blocks: the first ns of the sequence (those that hold sinks and
+  // lie before the band), then j0, j0 + 1, ... of the band
+  int j0, ns, nt;
+  __device__ __forceinline__ int block(int t) const { return t < ns ? t : j0 + t - ns; }
 };
 
 __device__ __forceinline__ int cta_tile(int r, int n_tiles) {
@@ -216,7 +219,8 @@ __device__ __forceinline__ Tile tile_of(const Params& p, int idx) {
   const int last_block = (p.N + kBn - 1) / kBn - 1;
   t.j0 = max(0, t.m0 - p.win_left) / kBn;
   const int j_end = min(last_block, (t.m0 + kBm - 1 + p.win_right) / kBn);
-  t.nt = j_end - t.j0 + 1;  // >= 1: the band holds the diagonal
+  t.ns = min(t.j0, (p.sinks + kBn - 1) / kBn);
+  t.nt = t.ns + j_end - t.j0 + 1;  // >= 1: the band holds the diagonal
   return t;
 }
 
@@ -267,7 +271,7 @@ __device__ void loader_role(const Ctx& c, const Params& p, uint32_t sbase,
         mbar_arrive_expect_tx(bar_addr(c, bar_full + st), kTileBytes);
         for (int cb = 0; cb < kBoxes; ++cb)
           tma_load_3d_hint(base + st * kTileBytes + cb * 16384, tkv, bar_addr(c, bar_full + st),
-                           64 * cb, (tl.j0 + t) * kBn, tl.kvh, keep);
+                           64 * cb, tl.block(t) * kBn, tl.kvh, keep);
       }
       __syncwarp();
     }
@@ -357,21 +361,32 @@ __device__ void mma_role(const Ctx& c, const Params& p, uint32_t sbase, uint32_t
 }
 
 // ------------------------------------------------------------------ softmax
+// Bit e of word e / 32 set where key key0 + e (e < 64) is visible to qrow:
+// one test per element, whatever bounds the mask.
+__device__ __forceinline__ uint2 visible_bits(const Params& p, int key0, int qrow) {
+  auto below = [](int n) {  // bits 0 .. n - 1
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+  };
+  const unsigned long long v =
+      below(min(p.N - 1, qrow + p.win_right) - key0 + 1) &
+      (~below(qrow - p.win_left - key0) | below(p.sinks - key0));
+  return make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+}
+__device__ __forceinline__ bool bit_of(uint2 bits, int e) {
+  return ((e < 32 ? bits.x : bits.y) >> (e & 31)) & 1u;
+}
+
 // Row maximum over 64 keys (key0 .. key0 + 63, S columns src .. src + 63)
 // of raw scores; with tau > 0 the logit grows with the score, softcap
 // included. MASKED chunks (a band's edge, the sequence's end) leave
 // invisible keys out.
 template <bool MASKED>
-__device__ __forceinline__ float chunk_max_regs(const Params& p, const uint32_t (&raw)[64],
-                                                int key0, int qrow) {
+__device__ __forceinline__ float chunk_max_regs(const uint32_t (&raw)[64], uint2 visible) {
   float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
   for (int e = 0; e < 64; ++e) {
     float s = __uint_as_float(raw[e]);
-    if (MASKED) {
-      const int key = key0 + e;
-      if (!(key < p.N && key - qrow <= p.win_right && qrow - key <= p.win_left)) s = -INFINITY;
-    }
+    if (MASKED && !bit_of(visible, e)) s = -INFINITY;
     if (e & 1)
       m1 = fmaxf(m1, s);
     else
@@ -384,18 +399,13 @@ __device__ __forceinline__ float chunk_max_regs(const Params& p, const uint32_t 
 // set to -inf, so that the unmasked maximum and P code (exp2(-inf) = 0) then
 // serve the block too. A separate masked copy of that code runs once per
 // tile and was found cold in the instruction cache every time.
-__device__ __forceinline__ void mask_scores(const Params& p, uint32_t (&raw)[64], int key0,
-                                            int qrow) {
-  // key0 + e is visible iff lo <= e <= hi
-  const int hi = min(p.N - 1, qrow + p.win_right) - key0;
-  const int lo = qrow - p.win_left - key0;
+__device__ __forceinline__ void mask_scores(uint32_t (&raw)[64], uint2 visible) {
 #pragma unroll
   for (int e = 0; e < 64; ++e)
-    if (e < lo || e > hi) raw[e] = 0xff800000u;  // -inf
+    if (!bit_of(visible, e)) raw[e] = 0xff800000u;  // -inf
 }
 
-// P = 2^(x - shift) of 64 keys (key0 .. key0 + 63, S columns src .. src +
-// 63) as bf16 pairs in columns dst .. dst + 31; returns their sum of P (fp32,
+// P = 2^(x - shift) of 64 keys (S columns src .. src + 63) as bf16 pairs in columns dst .. dst + 31; returns their sum of P (fp32,
 // before rounding and before dropout). With DROP the bf16 values are
 // P o Z / (1 - p), Z the keep mask whose bit j of kb0 (kb1) belongs to key
 // key0 + j (key0 + 32 + j): the exponent carries log2(1 / (1 - p)), so exp2
@@ -405,7 +415,7 @@ __device__ __forceinline__ void mask_scores(const Params& p, uint32_t (&raw)[64]
 // written.
 template <bool SOFTCAP, bool MASKED, bool DROP>
 __device__ __forceinline__ float chunk_p_regs(const Params& p, const uint32_t (&raw)[64],
-                                              uint32_t dst, int key0, int qrow, float c_log2,
+                                              uint32_t dst, uint2 visible, float c_log2,
                                               float cap_in, float cap_out, float shift,
                                               uint32_t kb0, uint32_t kb1) {
   const uint64_t c2v = f2_make(SOFTCAP ? cap_in : c_log2, SOFTCAP ? cap_in : c_log2);
@@ -433,10 +443,8 @@ __device__ __forceinline__ float chunk_p_regs(const Params& p, const uint32_t (&
       }
       float y0 = f2_lo(y2), y1 = f2_hi(y2);
       if (MASKED) {
-        const int key = key0 + 2 * u;
-        if (!(key < p.N && key - qrow <= p.win_right && qrow - key <= p.win_left)) y0 = -INFINITY;
-        if (!(key + 1 < p.N && key + 1 - qrow <= p.win_right && qrow - key - 1 <= p.win_left))
-          y1 = -INFINITY;
+        if (!bit_of(visible, 2 * u)) y0 = -INFINITY;
+        if (!bit_of(visible, 2 * u + 1)) y1 = -INFINITY;
       }
       const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
       sum2 = f2_add(sum2, f2_make(p0, p1));
@@ -495,7 +503,7 @@ __device__ void mask_role(const Ctx& c, const Params& p, uint8_t* smem) {
     for (int t = 0; t < tl.nt; ++t, ++g) {
       const int slot = g & 1;
       if (g >= 2 && !wait(c, BAR_MASK_EMPTY + slot, ((g >> 1) - 1) & 1)) return;
-      const uint32_t k0 = static_cast<uint32_t>((tl.j0 + t) * kBn + 16 * mw);
+      const uint32_t k0 = static_cast<uint32_t>(tl.block(t) * kBn + 16 * mw);
       uint32_t bits[4] = {0u, 0u, 0u, 0u};
       constexpr int kNB = 8;  // calls in flight
 #pragma unroll 1
@@ -567,7 +575,7 @@ __device__ void softmax_role(const Ctx& c, const Params& p, uint8_t* smem, uint3
     float m_used = -INFINITY, l = 0.f;
     for (int t = 0; t < nt; ++t) {
       const int gb = g + t;  // this block over the CTA's tiles
-      const int n0 = (tl.j0 + t) * kBn;
+      const int n0 = tl.block(t) * kBn;
       const int key0 = n0 + 64 * h;
       const uint32_t tS = tmem + lane_base + (gb & 1) * 128;
       const uint32_t src = tS + 64 * h;
@@ -600,13 +608,15 @@ __device__ void softmax_role(const Ctx& c, const Params& p, uint8_t* smem, uint3
         for (int e = 0; e < 64; ++e) raw[e] = 0u;
       }
       const bool masked =
-          n0 + kBn - 1 - m0 > p.win_right || m0 + kBm - 1 - n0 > p.win_left || n0 + kBn > p.N;
+          n0 + kBn - 1 - m0 > p.win_right || n0 + kBn > p.N ||
+          (m0 + kBm - 1 - n0 > p.win_left && n0 + kBn > p.sinks);
       // without the softcap, hidden keys become -inf scores (tanh would make
       // -inf a finite logit, so the softcap keeps its masked code)
-      if (!SOFTCAP && masked) mask_scores(p, raw, key0, qrow);
+      const uint2 visible = masked ? visible_bits(p, key0, qrow) : make_uint2(~0u, ~0u);
+      if (!SOFTCAP && masked) mask_scores(raw, visible);
       const bool mask_code = SOFTCAP && masked;
-      const float hmax = mask_code ? chunk_max_regs<true>(p, raw, key0, qrow)
-                                   : chunk_max_regs<false>(p, raw, key0, qrow);
+      const float hmax = mask_code ? chunk_max_regs<true>(raw, visible)
+                                   : chunk_max_regs<false>(raw, visible);
       float* slot = xmax + (gb & 1) * 256;
       slot[h * 128 + r] = hmax;
       ok = named_bar_and(kBarBoth, 256, ok && got);
@@ -660,10 +670,10 @@ __device__ void softmax_role(const Ctx& c, const Params& p, uint8_t* smem, uint3
       }
       const float shift = m_used > -INFINITY ? m_used : 0.f;
       const uint32_t dst = tS + 64 * h;  // keys 0-63 -> columns 0-31, 64-127 -> 64-95
-      l += mask_code ? chunk_p_regs<SOFTCAP, true, DROP>(p, raw, dst, key0, qrow, c_log2, cap_in,
+      l += mask_code ? chunk_p_regs<SOFTCAP, true, DROP>(p, raw, dst, visible, c_log2, cap_in,
                                                          cap_out, shift, kb0, kb1)
-                     : chunk_p_regs<SOFTCAP, false, DROP>(p, raw, dst, key0, qrow, c_log2,
-                                                          cap_in, cap_out, shift, kb0, kb1);
+                     : chunk_p_regs<SOFTCAP, false, DROP>(p, raw, dst, visible, c_log2, cap_in,
+                                                          cap_out, shift, kb0, kb1);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -869,14 +879,14 @@ int dispatch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv
 
 int run(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv,
         int N, int d, float scale, int causal, float softcap, int window_left, int window_right,
-        void* stream, float p_drop = 0.f, unsigned long long seed = 0) {
+        void* stream, float p_drop = 0.f, unsigned long long seed = 0, int sinks = 0) {
   if (!q || !k || !v || !o || !lse) return ATTN_ERR_NULL;
   int rc = check_shape(B, H, H_kv, N, d);
   if (rc != ATTN_OK) return rc;
   if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
   // tau > 0: the kernel takes a row's largest logit at its largest score
   if (!std::isfinite(scale) || !(scale > 0.f) || std::isnan(softcap)) return ATTN_ERR_SHAPE;
-  if (!(p_drop >= 0.f && p_drop < 1.f)) return ATTN_ERR_SHAPE;
+  if (!(p_drop >= 0.f && p_drop < 1.f) || sinks < 0) return ATTN_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
     return ATTN_ERR_ALIGN;
   if (B == 0 || H == 0 || N == 0) return ATTN_OK;
@@ -895,10 +905,10 @@ int run(const void* q, const void* k, const void* v, void* o, float* lse, int B,
   p.scale = scale;
   const bool cap = softcap > 0.f;
   p.softcap = cap ? softcap : 0.f;
-  // a negative or wider-than-N side of the window is unbounded (N); the
-  // causal mask bounds the right side at 0
-  p.win_left = (window_left < 0 || window_left > N) ? N : window_left;
-  p.win_right = causal ? 0 : ((window_right < 0 || window_right > N) ? N : window_right);
+  const Band band = band_of(N, causal, window_left, window_right, sinks);
+  p.win_left = band.left;
+  p.win_right = band.right;
+  p.sinks = band.sinks;
   p.drop.seed_lo = static_cast<uint32_t>(seed);
   p.drop.seed_hi = static_cast<uint32_t>(seed >> 32);
   p.drop.threshold = dropout_threshold(p_drop);
@@ -925,6 +935,14 @@ extern "C" int attn_fwd_local(const void* q, const void* k, const void* v, void*
                               float softcap, int window_left, int window_right, void* stream) {
   return fwdtc::run(q, k, v, o, lse, B, H, H_kv, N, d, scale, causal, softcap, window_left,
                     window_right, stream);
+}
+
+extern "C" int attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                              int B, int H, int H_kv, int N, int d, float scale, int causal,
+                              float softcap, int window_left, int window_right, int sinks,
+                              void* stream) {
+  return fwdtc::run(q, k, v, o, lse, B, H, H_kv, N, d, scale, causal, softcap, window_left,
+                    window_right, stream, 0.f, 0, sinks);
 }
 
 extern "C" int attn_fwd_dropout(const void* q, const void* k, const void* v, void* o, float* lse,

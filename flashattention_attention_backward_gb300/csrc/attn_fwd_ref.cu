@@ -43,10 +43,9 @@ struct Params {
   int q_blocks;
   float scale;
   float softcap;  // <= 0: disabled
-  // visibility band: key j is visible to query i iff
-  // i - win_left <= j <= i + win_right (causal: win_right = 0; an unbounded
-  // side holds N)
-  int win_left, win_right;
+  // key j is visible to query i iff j <= i + win_right and
+  // (j >= i - win_left or j < sinks) (see Band)
+  int win_left, win_right, sinks;
   int dropout;    // 0: off; else the keep mask of philox.cuh scales P in O = P V
   Dropout drop;
 };
@@ -110,7 +109,10 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_ref_kernel(const Params p) 
   const int n_tiles = (p.N + kBN - 1) / kBN;
   const int first_tile = max(0, m0 - p.win_left) / kBN;
   const int last_tile = min(n_tiles - 1, (m0 + kBM - 1 + p.win_right) / kBN);
-  for (int kt = first_tile; kt <= last_tile; ++kt) {
+  // tiles of the first `sinks` keys that lie before the band, then the band's
+  const int sink_tiles = min(first_tile, (p.sinks + kBN - 1) / kBN);
+  for (int t = 0; t < sink_tiles + last_tile - first_tile + 1; ++t) {
+    const int kt = t < sink_tiles ? t : first_tile + t - sink_tiles;
     const int n0 = kt * kBN;
     __syncthreads();  // previous tile's sKt / sV / sP reads are done
     for (int idx = tid; idx < kBN * (D / 8); idx += kThreads) {
@@ -173,7 +175,8 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_ref_kernel(const Params p) 
         const int key = n0 + tx * 4 + j;
         float s = acc[i][j] * p.scale;
         if (p.softcap > 0.f) s = p.softcap * tanhf(s / p.softcap);
-        const bool ok = key < p.N && key - qrow <= p.win_right && qrow - key <= p.win_left;
+        const bool ok = key < p.N && key - qrow <= p.win_right &&
+                        (qrow - key <= p.win_left || key < p.sinks);
         z[j] = ok ? s : -CUDART_INF_F;
         mx = fmaxf(mx, z[j]);
       }
@@ -261,13 +264,14 @@ namespace fwd {
 
 int run(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv,
         int N, int d, float scale, int causal, float softcap, float p_drop,
-        unsigned long long seed, void* stream, int window_left = -1, int window_right = -1) {
+        unsigned long long seed, void* stream, int window_left = -1, int window_right = -1,
+        int sinks = 0) {
   if (!q || !k || !v || !o || !lse) return ATTN_ERR_NULL;
   int rc = check_shape(B, H, H_kv, N, d);
   if (rc != ATTN_OK) return rc;
   if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
   if (!std::isfinite(scale) || scale == 0.f || std::isnan(softcap)) return ATTN_ERR_SHAPE;
-  if (!(p_drop >= 0.f && p_drop < 1.f)) return ATTN_ERR_SHAPE;
+  if (!(p_drop >= 0.f && p_drop < 1.f) || sinks < 0) return ATTN_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
     return ATTN_ERR_ALIGN;
   if (B == 0 || H == 0 || N == 0) return ATTN_OK;
@@ -284,9 +288,10 @@ int run(const void* q, const void* k, const void* v, void* o, float* lse, int B,
   p.q_blocks = (N + kBM - 1) / kBM;
   p.scale = scale;
   p.softcap = softcap > 0.f ? softcap : 0.f;
-  // a negative or wider-than-N side of the window is unbounded (N)
-  p.win_left = (window_left < 0 || window_left > N) ? N : window_left;
-  p.win_right = causal ? 0 : ((window_right < 0 || window_right > N) ? N : window_right);
+  const Band band = band_of(N, causal, window_left, window_right, sinks);
+  p.win_left = band.left;
+  p.win_right = band.right;
+  p.sinks = band.sinks;
   p.dropout = p_drop > 0.f ? 1 : 0;
   p.drop.seed_lo = static_cast<uint32_t>(seed);
   p.drop.seed_hi = static_cast<uint32_t>(seed >> 32);
@@ -323,4 +328,12 @@ extern "C" int attn_fwd_ref_local(const void* q, const void* k, const void* v, v
                                   void* stream) {
   return fwd::run(q, k, v, o, lse, B, H, H_kv, N, d, scale, causal, softcap, 0.f, 0ull, stream,
                   window_left, window_right);
+}
+
+extern "C" int attn_fwd_ref_sinks(const void* q, const void* k, const void* v, void* o,
+                                  float* lse, int B, int H, int H_kv, int N, int d, float scale,
+                                  int causal, float softcap, int window_left, int window_right,
+                                  int sinks, void* stream) {
+  return fwd::run(q, k, v, o, lse, B, H, H_kv, N, d, scale, causal, softcap, 0.f, 0ull, stream,
+                  window_left, window_right, sinks);
 }

@@ -17,9 +17,10 @@ from . import (ATTN_BF16, ATTN_FP16, ATTN_FP32, ATTN_ROTARY_BASE, ATTN_ROTARY_LI
                ATTN_ROTARY_PLAIN, ATTN_ROTARY_RAMP, attn_bwd, attn_bwd_deterministic,
                attn_bwd_dq_partials_bytes, attn_bwd_dropout, attn_bwd_finalize,
                attn_bwd_finalize_partials, attn_bwd_finalize_rotary, attn_bwd_local,
-               attn_bwd_preprocess, attn_bwd_sum_partials, attn_dropout_add, attn_dropout_add_norm,
-               attn_dropout_add_norm_bwd, attn_fwd, attn_fwd_dropout, attn_fwd_local,
-               attn_fwd_ref, attn_fwd_ref_dropout, attn_fwd_ref_local, attn_layer_norm,
+               attn_bwd_preprocess, attn_bwd_sinks, attn_bwd_sum_partials, attn_dropout_add,
+               attn_dropout_add_norm, attn_dropout_add_norm_bwd, attn_fwd, attn_fwd_dropout,
+               attn_fwd_local, attn_fwd_ref, attn_fwd_ref_dropout, attn_fwd_ref_local,
+               attn_fwd_ref_sinks, attn_fwd_sinks, attn_layer_norm,
                attn_layer_norm_bwd, attn_layer_norm_bwd_workspace_bytes, attn_rotary,
                attn_rotary_frequencies, check)
 
@@ -109,18 +110,23 @@ class _On:
 
 
 def forward(q, k, v, scale, causal, softcap=0.0, stream=None, impl="tc", dropout=None,
-            window=None):
+            window=None, sinks=0):
     """O [B,H,N,d] bf16 and LSE [B,H,N] fp32: attn_fwd (tensor cores, impl
     "tc") or attn_fwd_ref (plain fp32, impl "ref"). dropout = (p_drop, seed)
     runs attn_fwd_dropout or attn_fwd_ref_dropout; window = (left, right) runs
-    attn_fwd_local or attn_fwd_ref_local."""
+    attn_fwd_local or attn_fwd_ref_local, with sinks = n (the first n keys stay
+    visible to the left of the window) attn_fwd_sinks or attn_fwd_ref_sinks."""
     B, H, H_kv, N, d = _dims(q, k, v)
     if v.shape != k.shape:
         raise ValueError("v must have the shape of k")
+    window = _check_sinks(sinks, window, dropout)
     args = (B, H, H_kv, N, d, scale, causal, softcap)
     if dropout is not None:
         fn = {"tc": attn_fwd_dropout, "ref": attn_fwd_ref_dropout}[impl]
         args += (dropout[0], dropout[1])
+    elif sinks:
+        fn = {"tc": attn_fwd_sinks, "ref": attn_fwd_ref_sinks}[impl]
+        args += (window[0], window[1], sinks)
     elif window is not None:
         fn = {"tc": attn_fwd_local, "ref": attn_fwd_ref_local}[impl]
         args += (window[0], window[1])
@@ -132,6 +138,15 @@ def forward(q, k, v, scale, causal, softcap=0.0, stream=None, impl="tc", dropout
         check(fn(q, k, v, o, lse, *args, on.stream))
         on.made(o, lse)
     return o, lse
+
+
+def _check_sinks(sinks, window, dropout):
+    """The window of a call with sinks (unbounded if there is none)."""
+    if sinks < 0:
+        raise ValueError("sinks must not be negative")
+    if sinks and dropout is not None:
+        raise ValueError("sinks have no dropout variant")
+    return (-1, -1) if sinks and window is None else window
 
 
 class BackwardBuffers:
@@ -157,11 +172,13 @@ class BackwardBuffers:
 
 
 def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=None,
-             deterministic=False, dropout=None, window=None, rotary=None, positions=None):
+             deterministic=False, dropout=None, window=None, rotary=None, positions=None,
+             sinks=0):
     """dQ, dK, dV (bf16) via preprocess -> attn_bwd -> finalize, or, with
     deterministic=True, preprocess -> attn_bwd_deterministic ->
     finalize_partials (dQ identical bit for bit from run to run). window =
-    (left, right) runs attn_bwd_local in place of attn_bwd. rotary = the
+    (left, right) runs attn_bwd_local in place of attn_bwd, with sinks = n
+    attn_bwd_sinks. rotary = the
     Rotary that q and k came from (with the same positions): dQ and dK are
     then the gradients of what went into it, each rounded once
     (attn_bwd_finalize_rotary in place of attn_bwd_finalize, and behind
@@ -174,6 +191,7 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
         positions, pos_stride = _check_rotary(rotary, positions, B, N, d, q.device)
     elif positions is not None:
         raise ValueError("positions are those of a rotary")
+    window = _check_sinks(sinks, window, dropout)
     if dropout is None and window is not None and deterministic:
         raise ValueError("the local window has no deterministic variant")
     with _On(stream, q.device) as on:
@@ -194,6 +212,8 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
             tensors = (q, k, v, o, do, lse, bufs.dq_accum, bufs.dk, bufs.dv)
             if dropout is not None:
                 check(attn_bwd_dropout(*tensors, *shape, dropout[0], dropout[1], s))
+            elif sinks:
+                check(attn_bwd_sinks(*tensors, *shape, window[0], window[1], sinks, s))
             elif window is not None:
                 check(attn_bwd_local(*tensors, *shape, window[0], window[1], s))
             else:

@@ -24,8 +24,9 @@
  *  * Query head h uses KV head h / (H / H_kv) (H must be a multiple of H_kv).
  *  * d must be 64 or 128 for the allocation-free backward; 64, 128 or 256
  *    for every other forward and backward call (attn_fwd, attn_fwd_ref and
- *    their local and dropout forms, attn_bwd, attn_bwd_local,
- *    attn_bwd_dropout, attn_bwd_deterministic, attn_bwd_finalize_partials);
+ *    their local, sinks and dropout forms, attn_bwd, attn_bwd_local,
+ *    attn_bwd_sinks, attn_bwd_dropout, attn_bwd_deterministic,
+ *    attn_bwd_finalize_partials);
  *    preprocess and finalize accept any d that is a multiple of 4. Other
  *    values return ATTN_ERR_UNSUPPORTED.
  *  * Every pointer must be 16-byte aligned (the kernels use TMA and 16-byte
@@ -156,6 +157,35 @@ int attn_bwd_local(const void* q, const void* k, const void* v, const void* o, c
                    const float* lse, float* dq_accum, void* dk, void* dv, int B, int H, int H_kv,
                    int N, int d, float scale, int causal, float softcap, const float* dpsum,
                    int window_left, int window_right, void* stream);
+
+/*
+ * A local window whose first keys stay visible (sinks): key j is visible to
+ * query i iff
+ *     j <= i + window_right and (j >= i - window_left or j < sinks),
+ * and, if causal != 0, also j <= i: the left bound does not hide the first
+ * `sinks` keys of the sequence. The pages have no counterpart; the mask lets
+ * a cache of a long sequence drop all but its first and last keys (Xiao et
+ * al., "Efficient streaming language models with attention sinks", 2024).
+ * sinks >= 0 (ATTN_ERR_SHAPE otherwise); sinks = 0, or no left bound, is the
+ * local call, the same bits.
+ *
+ * attn_fwd_sinks, attn_fwd_ref_sinks: attn_fwd_local / attn_fwd_ref_local
+ *   under that mask; a CTA visits the key blocks that hold sinks and those of
+ *   its queries' band.
+ * attn_bwd_sinks: attn_bwd_local under that mask; a key block that holds sinks
+ *   visits every query block from its own on. Run it with attn_bwd_preprocess
+ *   and attn_bwd_finalize as attn_bwd.
+ */
+int attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
+                   int H_kv, int N, int d, float scale, int causal, float softcap,
+                   int window_left, int window_right, int sinks, void* stream);
+int attn_fwd_ref_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                       int H, int H_kv, int N, int d, float scale, int causal, float softcap,
+                       int window_left, int window_right, int sinks, void* stream);
+int attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                   const float* lse, float* dq_accum, void* dk, void* dv, int B, int H, int H_kv,
+                   int N, int d, float scale, int causal, float softcap, const float* dpsum,
+                   int window_left, int window_right, int sinks, void* stream);
 
 /*
  * attn_bwd_preprocess: D = rowsum(dO o O) ([FA-v1-bwd] §2.4 eq. 6;
