@@ -24,6 +24,7 @@ __all__ = [
     "attn_rotary", "attn_bwd_finalize_rotary", "attn_layer_norm", "attn_layer_norm_bwd",
     "attn_layer_norm_bwd_workspace_bytes", "attn_dropout_add", "attn_dropout_add_norm",
     "attn_dropout_add_norm_bwd", "ATTN_BF16", "ATTN_FP16", "ATTN_FP32", "ATTN_ROTARY_PLAIN",
+    "attn_cache_append", "attn_cache_fwd", "attn_cache_fwd_workspace_bytes", "ATTN_ERR_PAGE",
     "ATTN_ROTARY_LINEAR", "ATTN_ROTARY_BASE", "ATTN_ROTARY_RAMP",
     "ATTN_OK", "ATTN_ERR_NULL", "ATTN_ERR_SHAPE", "ATTN_ERR_UNSUPPORTED", "ATTN_ERR_ALIGN",
     "ATTN_ERR_LAUNCH", "ATTN_ERR_DEVICE_TIMEOUT", "ATTN_ERR_DEVICE", "ATTN_ERR_TOO_LARGE",
@@ -38,6 +39,7 @@ ATTN_ERR_LAUNCH = -5
 ATTN_ERR_DEVICE_TIMEOUT = -6
 ATTN_ERR_DEVICE = -7
 ATTN_ERR_TOO_LARGE = -8
+ATTN_ERR_PAGE = -9
 
 ATTN_BF16 = 0
 ATTN_FP16 = 1
@@ -87,6 +89,8 @@ _SIGNATURES = {
     "attn_rotary": [_P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P, _P],
     "attn_bwd_finalize_rotary": [_P, _P, _P, _P, _F, _P, _P, _L, _I, _I, _I, _I, _I, _I, _F, _I,
                                  _P, _P],
+    "attn_cache_append": [_P] * 10 + [_I] * 6 + [_F] + [_I] * 5 + [_P, _P],
+    "attn_cache_fwd": [_P] * 9 + [_I] * 8 + [_F, _I, _F, _I, _I, _I, _P, _P],
     "attn_layer_norm": [_P, _P, _P, _P, _P, _P, _L, _I, _F, _I, _I, _P],
     "attn_layer_norm_bwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _P],
     "attn_dropout_add": [_P, _P, _P, _L, _F, _U, _I, _P],
@@ -121,6 +125,8 @@ def library():
         lib.attn_bwd_dq_partials_bytes.restype = ctypes.c_longlong
         lib.attn_layer_norm_bwd_workspace_bytes.argtypes = [_L, _I]
         lib.attn_layer_norm_bwd_workspace_bytes.restype = ctypes.c_longlong
+        lib.attn_cache_fwd_workspace_bytes.argtypes = [_I] * 5
+        lib.attn_cache_fwd_workspace_bytes.restype = ctypes.c_longlong
         lib.attn_strerror.argtypes = [ctypes.c_int]
         lib.attn_strerror.restype = ctypes.c_char_p
         _lib = lib
@@ -316,6 +322,30 @@ def attn_bwd_finalize_rotary(dq_accum, dq, dk, dk_out, scale, turns, positions, 
     return library().attn_bwd_finalize_rotary(
         _ptr(dq_accum), _ptr(dq), _ptr(dk), _ptr(dk_out), scale, _ptr(turns), _ptr(positions),
         pos_stride, B, H, H_kv, N, d, rot, magnitude, int(interleaved), _strides(strides, 6),
+        _stream(stream))
+
+
+def attn_cache_append(q, k, v, q_out, k_cache, v_cache, turns, starts, lengths, pages, T, B, H,
+                      H_kv, d, rot, magnitude, interleaved, page_size, max_pages, n_pages, dtype,
+                      strides=None, stream=None):
+    return library().attn_cache_append(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(turns),
+        _ptr(starts), _ptr(lengths), _ptr(pages), T, B, H, H_kv, d, rot, magnitude,
+        int(interleaved), page_size, max_pages, n_pages, dtype, _strides(strides, 14),
+        _stream(stream))
+
+
+def attn_cache_fwd_workspace_bytes(T, B, H, H_kv, d):
+    return library().attn_cache_fwd_workspace_bytes(T, B, H, H_kv, d)
+
+
+def attn_cache_fwd(q, k_cache, v_cache, o, lse, starts, lengths, pages, workspace, T, B, H, H_kv,
+                   d, page_size, max_pages, n_pages, scale, causal, softcap, window_left, sinks,
+                   dtype, strides=None, stream=None):
+    return library().attn_cache_fwd(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(starts), _ptr(lengths),
+        _ptr(pages), _ptr(workspace), T, B, H, H_kv, d, page_size, max_pages, n_pages, scale,
+        int(causal), softcap, int(window_left), int(sinks), dtype, _strides(strides, 10),
         _stream(stream))
 
 

@@ -61,6 +61,7 @@
 #include <cuda_bf16.h>
 
 #include "attn_common.cuh"
+#include "cache_common.cuh"
 #include "philox.cuh"
 #include "sm103_ptx.cuh"
 
@@ -1264,7 +1265,12 @@ extern "C" int attn_device_status(int* status, int clear, void* stream) {
   int vf = 0, v256 = 0;  // the forward and d = 256 kernels keep their own words
   if (fwd_status(&vf, clear != 0) != ATTN_OK) return ATTN_ERR_LAUNCH;
   if (bwd256_status(&v256, clear != 0) != ATTN_OK) return ATTN_ERR_LAUNCH;
-  *status = v != 0 ? v : (vf != 0 ? vf : v256);
+  int va = 0, vc = 0;  // so do those over a paged cache
+  if (cache_append_status(&va, clear != 0) != ATTN_OK) return ATTN_ERR_LAUNCH;
+  if (cache_fwd_status(&vc, clear != 0) != ATTN_OK) return ATTN_ERR_LAUNCH;
+  *status = 0;
+  for (const int word : {v, vf, v256, va, vc})
+    if (*status == 0) *status = word;
   return ATTN_OK;
 }
 
@@ -1292,6 +1298,7 @@ extern "C" const char* attn_strerror(int code) {
     case ATTN_ERR_DEVICE_TIMEOUT: return "a kernel timed out waiting on a barrier";
     case ATTN_ERR_DEVICE: return "a kernel detected an internal fault";
     case ATTN_ERR_TOO_LARGE: return "a size exceeds the supported range";
+    case ATTN_ERR_PAGE: return "a slot lies outside the page table or the cache";
     default: return "unknown error code";
   }
 }

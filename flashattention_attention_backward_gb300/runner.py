@@ -1,7 +1,7 @@
 """Convenience wrappers that allocate device memory with torch and call the
 C ABI in stream order: forward (O, LSE), then preprocess -> attn_bwd ->
 finalize, and the operators around them (rotary positions, layer norm,
-dropout with a residual). No arithmetic happens here; torch provides memory
+dropout with a residual, a paged key/value cache). No arithmetic happens here; torch provides memory
 and streams.
 
 Streams: a call runs on `stream` (a torch stream, another object with a
@@ -17,7 +17,8 @@ from . import (ATTN_BF16, ATTN_FP16, ATTN_FP32, ATTN_ROTARY_BASE, ATTN_ROTARY_LI
                ATTN_ROTARY_PLAIN, ATTN_ROTARY_RAMP, attn_bwd, attn_bwd_deterministic,
                attn_bwd_dq_partials_bytes, attn_bwd_dropout, attn_bwd_finalize,
                attn_bwd_finalize_partials, attn_bwd_finalize_rotary, attn_bwd_local,
-               attn_bwd_preprocess, attn_bwd_sinks, attn_bwd_sum_partials, attn_dropout_add,
+               attn_bwd_preprocess, attn_bwd_sinks, attn_bwd_sum_partials, attn_cache_append,
+               attn_cache_fwd, attn_cache_fwd_workspace_bytes, attn_dropout_add,
                attn_dropout_add_norm, attn_dropout_add_norm_bwd, attn_fwd, attn_fwd_dropout,
                attn_fwd_local, attn_fwd_ref, attn_fwd_ref_dropout, attn_fwd_ref_local,
                attn_fwd_ref_sinks, attn_fwd_sinks, attn_layer_norm,
@@ -330,6 +331,123 @@ def rotary(q, k, plan, positions=None, adjoint=False, out=None, stream=None):
         check(attn_rotary(q, k, out[0], out[1], plan.turns, positions, pos_stride, B, H,
                           0 if k is None else k.shape[1], N, d, plan.rot, plan.magnitude,
                           plan.interleaved, adjoint, _DTYPES[q.dtype], strides, on.stream))
+    return out
+
+
+def _check_cache(q, k_cache, v_cache, pages, starts, lengths, dtype):
+    """(B, H_kv, d, page_size, max_pages, n_pages) of a batch over a cache."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be 4-D of one shape "
+                         "([pages, page size, heads, d])")
+    n_pages, page_size, H_kv, d = k_cache.shape
+    if dtype not in (torch.bfloat16, torch.float16) or k_cache.dtype != dtype or \
+            v_cache.dtype != dtype:
+        raise ValueError("the new tokens and the cache must all be bfloat16, or all float16")
+    if d > 1 and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1):
+        raise ValueError("the cache's rows must be contiguous")
+    if pages.dim() != 2 or lengths.shape != (pages.shape[0],) or \
+            starts.shape != (pages.shape[0] + 1,):
+        raise ValueError("pages must be [B, max_pages], lengths [B] and starts [B + 1]")
+    for name, t in (("pages", pages), ("lengths", lengths), ("starts", starts)):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous int32 tensor" % name)
+    if q is not None and (q.dim() != 3 or q.shape[2] != d):
+        raise ValueError("expected rows [T, heads, %d]" % d)
+    if q is not None and d > 1 and q.stride(2) != 1:
+        raise ValueError("rows must be contiguous")
+    _check_cuda(k_cache.device, k_cache=k_cache, v_cache=v_cache, pages=pages, starts=starts,
+                lengths=lengths, q=q)
+    return pages.shape[0], H_kv, d, page_size, pages.shape[1], n_pages
+
+
+def cache_append(q, k, v, k_cache, v_cache, pages, starts, lengths, plan, out=None, stream=None):
+    """The new tokens' keys (rotated by plan, a Rotary, to their positions) and
+    values into a paged cache, and q rotated (attn_cache_append). q [T,H,d] (or
+    None), k, v [T,H_kv,d], strided as long as rows are contiguous, e.g. parts
+    of a packed [T, H + 2 H_kv, d] projection; k_cache, v_cache
+    [pages, page size, H_kv, d] of any strides with contiguous rows; pages int32
+    [B, max_pages], starts int32 [B + 1], lengths int32 [B]. out: written in
+    place of a new tensor for q (may be q). Returns q rotated."""
+    B, H_kv, d, page_size, max_pages, n_pages = _check_cache(
+        q, k_cache, v_cache, pages, starts, lengths, k.dtype)
+    for name, t in (("k", k), ("v", v)):
+        if t.dim() != 3 or tuple(t.shape[1:]) != (H_kv, d) or t.shape[0] != k.shape[0] or \
+                t.dtype != k.dtype:
+            raise ValueError("%s must be [T, %d, %d] of k's dtype" % (name, H_kv, d))
+        if d > 1 and t.stride(2) != 1:
+            raise ValueError("rows must be contiguous")
+    if q is not None and (q.shape[0] != k.shape[0] or q.dtype != k.dtype):
+        raise ValueError("q must have k's rows and dtype")
+    if out is not None:
+        if q is None or out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must have the shape and dtype of q")
+        if d > 1 and out.stride(2) != 1:
+            raise ValueError("rows must be contiguous")
+    if plan.rot > d:
+        raise ValueError("rot = %d exceeds the head dimension %d" % (plan.rot, d))
+    _check_cuda(k.device, k=k, v=v, k_cache=k_cache, out=out, turns=plan.turns)
+    with _On(stream, k.device) as on:
+        if out is not None:
+            on.given(out)
+        elif q is not None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            on.made(out)
+        on.given(k_cache, v_cache)
+        rows = [k if q is None else q, k, v, k if q is None else out]
+        strides = [n for t in rows for n in t.stride()[:2]] + \
+            [n for t in (k_cache, v_cache) for n in t.stride()[:3]]
+        check(attn_cache_append(q, k, v, out, k_cache, v_cache, plan.turns, starts, lengths,
+                                pages, k.shape[0], B, 0 if q is None else q.shape[1], H_kv, d,
+                                plan.rot, plan.magnitude, plan.interleaved, page_size, max_pages,
+                                n_pages, _DTYPES[k.dtype], strides, on.stream))
+    return out
+
+
+def cache_attention(q, k_cache, v_cache, pages, starts, lengths, scale, causal=True, softcap=0.0,
+                    window_left=-1, sinks=0, out=None, workspace=None, stream=None):
+    """(o, lse) of the new tokens' attention over a paged cache that holds their
+    keys and values too (attn_cache_fwd): o [T,H,d] of q's type, lse [T,H] fp32.
+    The cache, pages, starts and lengths are those of cache_append; window_left
+    (negative: no bound) and sinks hide keys as the window and the sinks of
+    forward do. out = (o, lse): written in place of new tensors, whose rows
+    outside starts[0] .. starts[B] - 1 are undefined. workspace: a uint8 tensor of
+    attn_cache_fwd_workspace_bytes, for one call at a time."""
+    B, H_kv, d, page_size, max_pages, n_pages = _check_cache(
+        q, k_cache, v_cache, pages, starts, lengths, q.dtype)
+    T, H = q.shape[:2]
+    if out is not None:
+        if out[0].shape != q.shape or out[0].dtype != q.dtype or (d > 1 and
+                                                                  out[0].stride(2) != 1):
+            raise ValueError("out[0] must have the shape and dtype of q, and contiguous rows")
+        if out[1].shape != (T, H) or out[1].dtype != torch.float32 or \
+                not out[1].is_contiguous():
+            raise ValueError("out[1] must be a contiguous float32 [%d, %d] tensor" % (T, H))
+        _check_cuda(q.device, o=out[0], lse=out[1])
+    nbytes = attn_cache_fwd_workspace_bytes(T, B, H, H_kv, d)
+    if nbytes < 0:
+        check(int(nbytes))
+    if workspace is not None:
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+                workspace.numel() < nbytes:
+            raise ValueError("workspace must be a contiguous uint8 tensor of %d bytes" % nbytes)
+        _check_cuda(q.device, workspace=workspace)
+    with _On(stream, q.device) as on:
+        if out is None:
+            out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                   torch.empty((T, H), dtype=torch.float32, device=q.device))
+            on.made(*out)
+        else:
+            on.given(*out)
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        else:
+            on.given(workspace)
+        strides = [n for t in (q, out[0]) for n in t.stride()[:2]] + \
+            [n for t in (k_cache, v_cache) for n in t.stride()[:3]]
+        check(attn_cache_fwd(q, k_cache, v_cache, out[0], out[1], starts, lengths, pages,
+                             workspace, T, B, H, H_kv, d, page_size, max_pages, n_pages, scale,
+                             causal, softcap, window_left, sinks, _DTYPES[q.dtype], strides,
+                             on.stream))
     return out
 
 

@@ -62,6 +62,7 @@ extern "C" {
 #define ATTN_ERR_DEVICE_TIMEOUT (-6) /* a kernel gave up waiting (device status) */
 #define ATTN_ERR_DEVICE (-7)         /* a kernel detected an internal fault */
 #define ATTN_ERR_TOO_LARGE (-8)      /* a size exceeds what the kernels index */
+#define ATTN_ERR_PAGE (-9)           /* a slot outside the page table or the cache (device status) */
 
 /*
  * attn_fwd_ref: simple GPU forward producing the tensors the backward needs
@@ -462,10 +463,84 @@ int attn_dropout_add_norm_bwd(const void* dy, const void* dz_in, const void* z, 
                               void* stream);
 
 /*
+ * A paged key/value cache and a ragged batch of new tokens
+ * --------------------------------------------------------
+ * k_cache, v_cache: [n_pages, page_size, H_kv, d] (any strides with contiguous
+ * rows of d elements, e.g. [n_pages, H_kv, page_size, d]). The batch holds the
+ * new tokens of B sequences one behind another, as rows of [T, heads, d]:
+ *   starts  [B + 1] int32: sequence b's rows are starts[b] .. starts[b + 1] - 1
+ *           (none if equal; starts never fall). Rows outside
+ *           starts[0] .. starts[B] - 1 belong to none: they are not read, and
+ *           what the calls would write for them stays as it was.
+ *   lengths [B] int32: positions of sequence b, its new tokens the last of
+ *           them: row starts[b] + i stands at position
+ *           lengths[b] - (starts[b + 1] - starts[b]) + i.
+ *   pages   [B, max_pages] int32: position p of sequence b lives in slot
+ *           p mod page_size of page pages[b][p / page_size]. Entries that no
+ *           position in use needs may hold anything. Sequences may share
+ *           pages that no call writes at the time.
+ * All three are DEVICE memory, read by the kernels when they run: a captured
+ * graph replays with whatever they hold then (T, B and max_pages are the
+ * capture's).
+ * A slot that a call needs past max_pages * page_size, or of a page outside
+ * 0 .. n_pages - 1, touches no memory outside the cache: the append leaves it
+ * out, the attention hides keys past the table's end and takes those of such
+ * a page as zeros, and attn_device_status reports ATTN_ERR_PAGE.
+ * bf16 or fp16 (ATTN_ERR_SHAPE otherwise), q, k, v and cache alike.
+ *
+ * attn_cache_append: q_out = R q, and into each new token's slot R k and v,
+ *   in one launch; R as in attn_rotary (turns, rot, magnitude, interleaved)
+ *   at the token's position. rot = 0 copies. v is copied bit by bit.
+ * In:  q [T,H,d], k, v [T,H_kv,d]. Out: q_out [T,H,d] (may be q, with the same
+ *      strides), the slots of the new tokens (two rows must not name one slot).
+ * strides: HOST array of 14 element strides: (token, head) of q, k, v and
+ *      q_out, (page, slot, head) of k_cache and v_cache; NULL: all contiguous.
+ *      They are >= 0, and > 0 for outputs (but for dimensions of one element).
+ * H = 0 leaves q out (q, q_out may be NULL); any d, page_size and H_kv >= 1.
+ * Whole 16-byte groups (d and every stride a multiple of 16 bytes, and rot one
+ * of 32 bytes) run faster than others.
+ */
+int attn_cache_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                      void* v_cache, const unsigned long long* turns, const int* starts,
+                      const int* lengths, const int* pages, int T, int B, int H, int H_kv, int d,
+                      int rot, float magnitude, int interleaved, int page_size, int max_pages,
+                      int n_pages, int dtype, const long long* strides, void* stream);
+
+/*
+ * attn_cache_fwd: attention of the new tokens over the cache (whose slots hold
+ * the new tokens' keys and values too: run attn_cache_append first). The query at
+ * position p of its sequence sees key j iff
+ *     0 <= j < length, j <= p if causal != 0, and
+ *     j >= p - window_left (a negative window_left: no bound) or j < sinks;
+ *   O = softmax(logits) V, LSE = ln sum exp(logits), logits as in attn_fwd.
+ * A row that sees no key gets O = 0, LSE = -infinity.
+ * In:  q [T,H,d]. Out: o [T,H,d], lse [T,H] fp32 contiguous (may be NULL).
+ * Values in slots that no query of a sequence's call sees are never used,
+ * whatever they hold (NaN too). Pages behind the window and past the sinks may
+ * have been given away: their table entries are not read.
+ * strides: HOST array of 10 element strides: (token, head) of q and o, (page,
+ *      slot, head) of k_cache and v_cache; NULL: all contiguous. Multiples of
+ *      8 elements (ATTN_ERR_ALIGN).
+ * d = 64, 128 or 256, page_size a multiple of 8, H / H_kv at most 128
+ * (ATTN_ERR_UNSUPPORTED otherwise); scale > 0, sinks >= 0.
+ * workspace: attn_cache_fwd_workspace_bytes(T, B, H, H_kv, d) bytes of device
+ *      memory, whose contents need no preparation and mean nothing after.
+ *      Calls that may run at the same time (two streams, two captured graphs)
+ *      need one each.
+ * The same call on the same lengths gives the same bits every time.
+ */
+long long attn_cache_fwd_workspace_bytes(int T, int B, int H, int H_kv, int d);
+int attn_cache_fwd(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                   const int* starts, const int* lengths, const int* pages, void* workspace, int T,
+                   int B, int H, int H_kv, int d, int page_size, int max_pages, int n_pages,
+                   float scale, int causal, float softcap, int window_left, int sinks, int dtype,
+                   const long long* strides, void* stream);
+
+/*
  * attn_device_status: waits for `stream`, then reads the library's device
  * status word into *status (0 = no fault; ATTN_ERR_DEVICE_TIMEOUT when a
  * kernel gave up waiting on a barrier; ATTN_ERR_DEVICE for an internal
- * check). clear != 0 resets it to 0. Returns ATTN_OK or a launch error.
+ * check; ATTN_ERR_PAGE when a call over a paged cache met a slot outside it). clear != 0 resets it to 0. Returns ATTN_OK or a launch error.
  */
 int attn_device_status(int* status, int clear, void* stream);
 

@@ -17,9 +17,12 @@ Sources (web pages, cited by title and section):
   * Rotary positions, layer norm and dropout with a residual: written from
     their formulas in ``oracle/rotary.py`` and ``oracle/norm.py``.
 
+  * A paged key/value cache: written from its definition in ``oracle/cache.py``.
+
 Every function here is pinned by ``tests/test_oracle_pins.py`` (hand-derived
 N=2, d=2 example, finite differences against an independent scalar forward,
-invariants and special cases) and ``tests/test_oracle_block_pins.py``.
+invariants and special cases) and ``tests/test_oracle_block_pins.py``
+and ``tests/test_cache_cpu.py``.
 """
 from .attention import (  # noqa: F401
     attention_forward,
@@ -27,6 +30,7 @@ from .attention import (  # noqa: F401
     head_forward,
     head_backward,
 )
+from .cache import cache_append, cache_attention  # noqa: F401
 from .norm import (  # noqa: F401
     dropout,
     element_keep_mask,
