@@ -526,7 +526,7 @@ int attn_cache_append(const void* q, const void* k, const void* v, void* q_out, 
  * workspace: attn_cache_fwd_workspace_bytes(T, B, H, H_kv, d) bytes of device
  *      memory, whose contents need no preparation and mean nothing after.
  *      Calls that may run at the same time (two streams, two captured graphs)
- *      need one each.
+ *      need one each, and a captured call's lives as long as its graph.
  * The same call on the same lengths gives the same bits every time.
  */
 long long attn_cache_fwd_workspace_bytes(int T, int B, int H, int H_kv, int d);

@@ -349,15 +349,16 @@ def test_captured_graph_follows_the_lengths():
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             step()
-        graphs.append((graph, caches, q, out, lengths))
+        # the workspace lives as long as the graph that uses it
+        graphs.append((graph, caches, q, out, lengths, ws))
     g = torch.Generator().manual_seed(9)
     for n in range(8):
         c.qkv.copy_(torch.randn(c.qkv.shape, generator=g).to(BF))
-        for graph, caches, q, out, lengths in graphs:
+        for graph, _, _, _, lengths, _ in graphs:
             lengths.copy_(torch.tensor([L + n + 1 for L in first], dtype=torch.int32))
             graph.replay()
         torch.cuda.synchronize()
-        (_, caches, q, out, lengths), other = graphs[0], graphs[1]
+        (_, caches, q, out, lengths, _), other = graphs[0], graphs[1]
         c.lengths = lengths.cpu().numpy()
         c.caches = caches
         c.check(*out, q=q)
