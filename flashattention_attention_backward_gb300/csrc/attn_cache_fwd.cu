@@ -63,10 +63,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;  // move the shift only when the maximum grows by more
 constexpr long long kWaitLimitCycles = 2000000000LL;  // about one second
 
-// At d = 256 the softmax warps' state does not fit in the 168 registers that 384
-// threads are launched with: setmaxnreg moves registers to them.
-constexpr int kRegsSoftmax256 = 200, kRegsCtl256 = 56;
-static_assert(256 * kRegsSoftmax256 + 128 * kRegsCtl256 <= 384 * 168, "register pool");
+// The softmax warps' state does not fit in the 168 registers that 384 threads are
+// launched with: setmaxnreg moves registers to them from the loaders and the MMA
+// warp.
+constexpr int kRegsSoftmax = 216, kRegsCtl = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsCtl <= 384 * 168, "register pool");
 
 template <int D>
 struct Layout {
@@ -105,8 +106,8 @@ enum Bar {
   BAR_O_DONE = 16,   // P V of a block completed (one phase per key block)
   BAR_O_LAST = 17,   // the tile's last P V completed (one phase per tile)
   BAR_O_FREE = 18,   // + O buffer: the tile's epilogue has read O
-  BAR_V_EDGE = 20,   // copies of a V block some of whose rows are then zeroed
-  BAR_DRAIN = 21,    // abort path only: completion of everything issued
+  BAR_V_EDGE = 20,   // + stage: copies of a V block some of whose rows are then zeroed
+  BAR_DRAIN = 22,    // abort path only: completion of everything issued
 };
 
 __device__ int g_status;
@@ -261,15 +262,16 @@ struct Part {
 };
 
 // Finds the CTA's part (every thread of the CTA calls; `sums` and `part` in
-// shared memory). Warp w sums the blocks of its chunk of the sequences; the warp
-// whose chunk holds the part's first block then looks for it there.
+// shared memory). Warp w sums the blocks of its chunk of the sequences, 32 at a
+// time; the warp whose chunk holds the part's first block then looks for it there
+// (a chunk of up to 32 sequences, so up to 384 in all, is not summed again).
 __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part* part) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int B = p.batch.B;
-  const int chunk = ((B + kWarps - 1) / kWarps + 31) & ~31;
+  const int chunk = (B + kWarps - 1) / kWarps;
   const int first = min(B, warp * chunk), end = min(B, first + chunk);
-  long long sum = 0;
-  for (int b = first; b < end; b += 32) sum += lane_blocks(p, b, end);
+  long long sum = 0, mine = 0;
+  for (int b = first; b < end; b += 32) sum += mine = lane_blocks(p, b, end);
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (lane == 0) sums[warp] = sum * p.H_kv;
@@ -285,7 +287,7 @@ __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part
   if (u0 < total && u0 >= before && u0 < before + sums[warp]) {
     long long at = u0 - before;  // within this warp's chunk
     for (int b = first; b < end; b += 32) {
-      const long long blocks = lane_blocks(p, b, end) * p.H_kv;
+      const long long blocks = (chunk <= 32 ? mine : lane_blocks(p, b, end)) * p.H_kv;
       long long upto = blocks;  // inclusive sum over the lanes
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -337,8 +339,7 @@ __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part
 
 // Walks the tiles of a part; every role has its own.
 struct Walk {
-  int b, kvh, tile, blk, take;
-  long long left;
+  int b, kvh, tile, blk, take, left;
   Seq s;
   Tile t;
   __device__ __forceinline__ void begin(const Params& p, const Part& part) {
@@ -346,11 +347,11 @@ struct Walk {
     kvh = part.kvh;
     tile = part.tile;
     blk = part.blk;
-    left = part.count;
+    left = static_cast<int>(part.count);
     if (left > 0) {
       s = seq_of(p, b);
       t = tile_of(p, s, tile);
-      take = static_cast<int>(min(static_cast<long long>(t.nt - blk), left));
+      take = min(t.nt - blk, left);
     }
   }
   __device__ __forceinline__ void next(const Params& p) {
@@ -367,7 +368,7 @@ struct Walk {
       }
     }
     t = tile_of(p, s, tile);
-    take = static_cast<int>(min(static_cast<long long>(t.nt), left));
+    take = min(t.nt, left);
   }
 };
 
@@ -417,8 +418,41 @@ __device__ __forceinline__ void load_pieces(const Ctx& c, const Params& p, const
   __syncwarp();
 }
 
+// A V block with rows that no row of its tile sees, on its way into stage st.
+struct Edge {
+  int st = -1, n0 = 0, lo = 0, hi = 0, sinks = 0;
+  bool copied = false;  // some of its pieces are loaded
+};
+// Zeroes those rows once the copies have landed and hands the stage over. Bit st of
+// `parity` is that of the stage's next copies.
+template <int D>
+__device__ __forceinline__ bool finish_edge(const Ctx& c, Edge& e, uint32_t& parity,
+                                            uint8_t* ring) {
+  if (e.st < 0) return true;
+  const int lane = threadIdx.x & 31;
+  if (e.copied) {
+    if (!wait_warp(c, BAR_V_EDGE + e.st, (parity >> e.st) & 1)) return false;
+    parity ^= 1u << e.st;
+  }
+  for (int r = lane >> 3; r < kBn; r += 4) {  // 8 lanes a row
+    const int key = e.n0 + r;
+    if (key <= e.hi && (key >= e.lo || key < e.sinks)) continue;
+#pragma unroll
+    for (int cb = 0; cb < D / 64; ++cb)
+      *reinterpret_cast<uint4*>(ring + e.st * Layout<D>::kTileBytes + cb * 16384 + r * 128 +
+                                (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar_addr(c, BAR_V_FULL + e.st));
+  e.st = -1;
+  return true;
+}
+
 // Warp 0: Q of each tile and its K blocks; warp 2: the V blocks. Each ring waits
-// for its own stages, in the order the tensor cores finish them.
+// for its own stages, in the order the tensor cores finish them. A V block whose
+// rows are to be zeroed is finished behind the next block's request, so that its
+// copies' latency does not leave the ring empty.
 template <int D, bool IS_V>
 __device__ void loader_role(const Ctx& c, const Params& p, const Part& part, uint8_t* smem,
                             uint32_t sbase, const CUtensorMap* tq, const CUtensorMap* tkv) {
@@ -428,7 +462,9 @@ __device__ void loader_role(const Ctx& c, const Params& p, const Part& part, uin
   const int bar_full = IS_V ? BAR_V_FULL : BAR_K_FULL;
   const int bar_empty = IS_V ? BAR_V_EMPTY : BAR_K_EMPTY;
   const int ring = IS_V ? L::kV : L::kK;
-  int g = 0, i = 0, edges = 0;  // blocks, tiles and zeroed blocks issued
+  int g = 0, i = 0;  // blocks and tiles issued
+  Edge edge;
+  uint32_t edge_parity = 0;
   bool ok = true;
   Walk w;
   for (w.begin(p, part); ok && w.left > 0; w.next(p), ++i) {
@@ -452,41 +488,37 @@ __device__ void loader_role(const Ctx& c, const Params& p, const Part& part, uin
       const Pieces x = next;
       if (t + 1 < w.take) next = pieces_of(p, w, w.blk + t + 1);
       const int st = g % kS;
+      // with one stage the block before has to be finished first
+      if (IS_V && kS == 1 && !(ok = finish_edge<D>(c, edge, edge_parity, smem + ring))) break;
       if (g >= kS && !(ok = wait_warp(c, bar_empty + st, ((g / kS) - 1) & 1))) break;
       const uint32_t dst = sbase + ring + st * L::kTileBytes;
       const int n0 = w.t.block(w.blk + t) * kBn;
-      const bool edge = IS_V && (n0 + kBn - 1 > w.t.hi || (n0 < w.t.lo && n0 + kBn > w.t.sinks));
-      if (!edge) {
-        load_pieces<D>(c, p, x, w.kvh, dst, tkv, bar_full + st);
-        continue;
+      const bool cut = IS_V && (n0 + kBn - 1 > w.t.hi || (n0 < w.t.lo && n0 + kBn > w.t.sinks));
+      if (!cut || x.needed != 0)
+        load_pieces<D>(c, p, x, w.kvh, dst, tkv, cut ? BAR_V_EDGE + st : bar_full + st);
+      if (IS_V) {
+        if (!(ok = finish_edge<D>(c, edge, edge_parity, smem + ring))) break;
+        if (cut) {
+          edge.st = st;
+          edge.n0 = n0;
+          edge.lo = w.t.lo;
+          edge.hi = w.t.hi;
+          edge.sinks = w.t.sinks;
+          edge.copied = x.needed != 0;
+        }
       }
-      if (x.needed != 0) {
-        load_pieces<D>(c, p, x, w.kvh, dst, tkv, BAR_V_EDGE);
-        if (!(ok = wait_warp(c, BAR_V_EDGE, edges & 1))) break;
-        ++edges;
-      }
-      // rows of V that no row of the tile sees: 8 lanes a row
-      for (int r = lane >> 3; r < kBn; r += 4) {
-        const int key = n0 + r;
-        if (key <= w.t.hi && (key >= w.t.lo || key < w.t.sinks)) continue;
-#pragma unroll
-        for (int cb = 0; cb < D / 64; ++cb)
-          *reinterpret_cast<uint4*>(smem + ring + st * L::kTileBytes + cb * 16384 + r * 128 +
-                                    (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_addr(c, bar_full + st));
     }
   }
-  // When aborting, the copies in flight must land before the CTA exits.
+  if (IS_V && ok) ok = finish_edge<D>(c, edge, edge_parity, smem + ring);
+  // When aborting, the copies in flight must land before the CTA exits (a phase
+  // that was never begun ends the wait by its limit).
   if (!ok || *c.abort) {
-    for (int gg = g - kS < 0 ? 0 : g - kS; gg < g; ++gg)
-      wait_drain(c, bar_full + gg % kS, (gg / kS) & 1);
-    if (IS_V) wait_drain(c, BAR_V_EDGE, edges & 1);
-    if (!IS_V)
-      for (int ii = i + 1 - kS < 0 ? 0 : i + 1 - kS; ii <= i; ++ii)
-        wait_drain(c, BAR_Q_FULL + ii % kS, (ii / kS) & 1);
+    for (int st = 0; st < kS; ++st) {
+      const int uses = (g + kS - st) / kS;  // blocks that went to this stage, or one more
+      wait_drain(c, bar_full + st, (uses > 0 ? uses - 1 : 0) & 1);
+      if (IS_V) wait_drain(c, BAR_V_EDGE + st, (edge_parity >> st) & 1);
+      if (!IS_V) wait_drain(c, BAR_Q_FULL + st, (i / kS) & 1);
+    }
   }
 }
 
@@ -498,9 +530,11 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn_major) {
          ~(std::is_same<T, __half>::value ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// Per tile: S(0); then per key block t, S(t + 1) into the other S buffer (its P(t -
-// 1) was read by P(t - 1) V, issued before), then P(t) V into the tile's O buffer
-// once the softmax has written P(t).
+// S runs one block ahead of P V: S(g + 1) goes into the other S buffer (its P(g -
+// 1) was read by P(g - 1) V, issued before), also where block g + 1 begins the next
+// tile and two Q stages hold both tiles' queries, so that the softmax finds its
+// scores behind the epilogue; then P(g) V into the tile's O buffer once the
+// softmax has written P(g).
 template <typename T, int D>
 __device__ void mma_role(const Ctx& c, const Params& p, const Part& part, uint32_t sbase,
                          uint32_t tmem) {
@@ -511,56 +545,71 @@ __device__ void mma_role(const Ctx& c, const Params& p, const Part& part, uint32
   constexpr uint32_t kIdO = idesc<T>(kBm, D, true);     // O += P V
   auto kmaj = [](int k) { return static_cast<uint32_t>(((k >> 2) * 16384 + (k & 3) * 32) >> 4); };
   auto mnmaj = [](int k) { return static_cast<uint32_t>((2048 * k) >> 4); };
-  bool ok = true;
-  int g = 0;  // blocks of all tiles before
-  int i = 0;
-  Walk w;
-  for (w.begin(p, part); ok && w.left > 0; w.next(p), ++i) {
-    const int nt = w.take;
-    const int qs = i % kS, ob = i % kOB;
-    const uint32_t q_lo = sdesc_lo(sbase + L::kQ + qs * L::kTileBytes, 16);
-    const uint32_t t_o = tmem + 256 + ob * D;
-    auto issue_s = [&](int gb, bool last) -> bool {
-      const int st = gb % kS;
-      if (!wait_warp(c, BAR_K_FULL + st, (gb / kS) & 1)) return false;
-      tc_fence_after();
-      if (leader) {
-        const uint32_t k_lo = sdesc_lo(sbase + L::kK + st * L::kTileBytes, 16);
+  // S of block g of tile i; `first`, `last` of the tile's blocks
+  auto issue_s = [&](int g, int i, bool first, bool last) -> bool {
+    const int st = g % kS, qs = i % kS;
+    if (first && !wait_warp(c, BAR_Q_FULL + qs, (i / kS) & 1)) return false;
+    if (!wait_warp(c, BAR_K_FULL + st, (g / kS) & 1)) return false;
+    tc_fence_after();
+    if (leader) {
+      const uint32_t q_lo = sdesc_lo(sbase + L::kQ + qs * L::kTileBytes, 16);
+      const uint32_t k_lo = sdesc_lo(sbase + L::kK + st * L::kTileBytes, 16);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + (gb & 1) * 128, sdesc_from_lo(q_lo + kmaj(k)),
-                 sdesc_from_lo(k_lo + kmaj(k)), kIdS, k > 0);
-        mma_commit(bar_addr(c, BAR_S_FULL + (gb & 1)));
-        mma_commit(bar_addr(c, BAR_K_EMPTY + st));
-        if (last) mma_commit(bar_addr(c, BAR_Q_EMPTY + qs));
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(tmem + (g & 1) * 128, sdesc_from_lo(q_lo + kmaj(k)), sdesc_from_lo(k_lo + kmaj(k)),
+               kIdS, k > 0);
+      mma_commit(bar_addr(c, BAR_S_FULL + (g & 1)));
+      mma_commit(bar_addr(c, BAR_K_EMPTY + st));
+      if (last) mma_commit(bar_addr(c, BAR_Q_EMPTY + qs));
+    }
+    return true;
+  };
+  bool ok = true;
+  Walk w;
+  w.begin(p, part);
+  if (w.left > 0) {
+    int nt = w.take, next_nt = 0;
+    ok = issue_s(0, 0, true, nt == 1);
+    for (int g = 0, i = 0, t = 0; ok; ++g) {
+      const bool last = t + 1 == nt;
+      bool more = !last;
+      if (last) {
+        w.next(p);
+        more = w.left > 0;
+        next_nt = w.take;
       }
-      return true;
-    };
-    ok = wait_warp(c, BAR_Q_FULL + qs, (i / kS) & 1);
-    if (ok) ok = issue_s(g, nt == 1);
-    for (int t = 0; ok && t < nt; ++t) {
-      const int gb = g + t;
-      if (t + 1 < nt && !(ok = issue_s(gb + 1, t + 2 == nt))) break;
-      if (!(ok = wait_warp(c, BAR_P_FULL + (gb & 1), (gb >> 1) & 1))) break;
-      const int vs = gb % kS;
-      if (!(ok = wait_warp(c, BAR_V_FULL + vs, (gb / kS) & 1))) break;
+      const bool ahead = kS >= 2 || !last;
+      if (more && ahead &&
+          !(ok = issue_s(g + 1, last ? i + 1 : i, last, last ? next_nt == 1 : t + 2 == nt)))
+        break;
+      if (!(ok = wait_warp(c, BAR_P_FULL + (g & 1), (g >> 1) & 1))) break;
+      const int vs = g % kS, ob = i % kOB;
+      if (!(ok = wait_warp(c, BAR_V_FULL + vs, (g / kS) & 1))) break;
       if (t == 0 && i >= kOB && !(ok = wait_warp(c, BAR_O_FREE + ob, ((i / kOB) - 1) & 1)))
         break;
       tc_fence_after();
       if (leader) {
         const uint32_t v_mn = sdesc_lo(sbase + L::kV + vs * L::kTileBytes, 16384);
-        // A = P (pairs in the S buffer of block gb: keys 0-63 in columns 0-31,
+        // A = P (pairs in the S buffer of block g: keys 0-63 in columns 0-31,
         // keys 64-127 in columns 64-95, one half per softmax warpgroup)
 #pragma unroll
         for (int k = 0; k < kBn / 16; ++k)
-          mma_ts(t_o, tmem + (gb & 1) * 128 + 8 * k + (k >= 4 ? 32 : 0),
+          mma_ts(tmem + 256 + ob * D, tmem + (g & 1) * 128 + 8 * k + (k >= 4 ? 32 : 0),
                  sdesc_from_lo(v_mn + mnmaj(k)), kIdO, (t > 0 || k > 0) ? 1u : 0u);
         mma_commit(bar_addr(c, BAR_O_DONE));
         mma_commit(bar_addr(c, BAR_V_EMPTY + vs));
-        if (t == nt - 1) mma_commit(bar_addr(c, BAR_O_LAST));
+        if (last) mma_commit(bar_addr(c, BAR_O_LAST));
+      }
+      if (!more) break;
+      if (!ahead && !(ok = issue_s(g + 1, i + 1, true, next_nt == 1))) break;
+      if (last) {
+        nt = next_nt;
+        t = 0;
+        ++i;
+      } else {
+        ++t;
       }
     }
-    g += nt;
   }
   if (__any_sync(0xffffffffu, !ok || *c.abort != 0)) {
     // completion of everything issued before tensor memory is released
@@ -901,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlot);
   if (*c.abort == 0) {
     if (warp < 4) {
-      if constexpr (D == 256) setmaxnreg_dec<kRegsCtl256>();
+      setmaxnreg_dec<kRegsCtl>();
       if (warp == 0)
         loader_role<D, false>(c, p, *part, smem, sbase, &tm_q, &tm_k);
       else if (warp == 1)
@@ -909,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else if (warp == 2)
         loader_role<D, true>(c, p, *part, smem, sbase, &tm_q, &tm_v);
     } else {
-      if constexpr (D == 256) setmaxnreg_inc<kRegsSoftmax256>();
+      setmaxnreg_inc<kRegsSoftmax>();
       softmax_role<T, D, SOFTCAP>(c, p, *part, smem, tmem);
     }
   }
@@ -924,60 +973,64 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of the tile that begins in part blockIdx.x and goes on behind
 // it: M = max m_i, L = sum l_i 2^(m_i - M), O = sum O_i 2^(m_i - M) / L, in the
 // order of the parts. One warp a row, D / 32 columns a lane.
-constexpr int kJoinWarps = 4, kJoinSplit = 8;
+constexpr int kJoinWarps = 8, kJoinSplit = 128 / kJoinWarps;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Params p) {
   grid_dependency_wait();
   const Shared s = reinterpret_cast<const Shared*>(p.workspace)[blockIdx.x];
-  if (s.parts == 0) return;
+  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  if (s.parts == 0 || r >= s.rows) return;
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const float* slots = reinterpret_cast<const float*>(p.workspace + kSharedBytes) +
                        2LL * blockIdx.x * slot_floats(D);
   // part i of the tile: slot 1 of the first CTA, slot 0 of the ones behind
   auto slot = [&](int i) { return slots + (i == 0 ? 1 : 2 * i) * slot_floats(D); };
-  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < s.rows;
-       r += kJoinWarps * kJoinSplit) {
-    float M = -INFINITY;
-    for (int i = lane; i < s.parts; i += 32) M = fmaxf(M, slot(i)[r]);
+  constexpr int kAhead = 4;  // parts whose O is on its way before the weights are known
+  float2 v[kAhead][E / 2];
+  auto load = [&](int i, float2 (&to)[E / 2]) {
+    const float* from = slot(i) + 256 + r * D + lane * E;
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float shift = M > -INFINITY ? M : 0.f;
-    float o[E], total = 0.f;
+    for (int e = 0; e < E / 2; ++e) to[e] = reinterpret_cast<const float2*>(from)[e];
+  };
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int i0 = 0; i0 < s.parts; i0 += 32) {
-      float f = 0.f, l = 0.f;
-      if (i0 + lane < s.parts) {
-        f = ex2_approx(slot(i0 + lane)[r] - shift);
-        l = slot(i0 + lane)[128 + r] * f;
-      }
-      const int n = min(32, s.parts - i0);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        total += __shfl_sync(0xffffffffu, l, i);
-        const float* from = slot(i0 + i) + 256 + r * D + lane * E;
-        if (fi > 0.f) {  // a part that saw nothing holds no numbers
+  for (int i = 0; i < kAhead; ++i)
+    if (i < s.parts) load(i, v[i]);
+  float M = -INFINITY;
+  for (int i = lane; i < s.parts; i += 32) M = fmaxf(M, slot(i)[r]);
 #pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const float2 v = *reinterpret_cast<const float2*>(from + e);
-            o[e] = fmaf(v.x, fi, o[e]);
-            o[e + 1] = fmaf(v.y, fi, o[e + 1]);
-          }
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float shift = M > -INFINITY ? M : 0.f;
+  float2 o[E / 2];
+  float total = 0.f;
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) o[e] = make_float2(0.f, 0.f);
+  for (int i0 = 0; i0 < s.parts; i0 += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u;
+      if (i >= s.parts) break;
+      const float f = ex2_approx(slot(i)[r] - shift);
+      if (f > 0.f) {  // a part that saw nothing holds no numbers
+        total = fmaf(slot(i)[128 + r], f, total);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          o[e].x = fmaf(v[u][e].x, f, o[e].x);
+          o[e].y = fmaf(v[u][e].y, f, o[e].y);
         }
       }
+      if (i + kAhead < s.parts) load(i + kAhead, v[u]);
     }
-    const float inv = total > 0.f ? 1.f / total : 0.f;
-    const int token = r / p.G, head = s.kvh * p.G + r - token * p.G;
-    const long long row = s.row0 + token;
-    T* out = static_cast<T*>(p.o) + row * p.o_token + head * p.o_head + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(out + e) = pack_pair<T>(o[e] * inv, o[e + 1] * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[row * p.H + head] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
   }
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const int token = r / p.G, head = s.kvh * p.G + r - token * p.G;
+  const long long row = s.row0 + token;
+  T* out = static_cast<T*>(p.o) + row * p.o_token + head * p.o_head + lane * E;
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e)
+    reinterpret_cast<uint32_t*>(out)[e] = pack_pair<T>(o[e].x * inv, o[e].y * inv);
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[row * p.H + head] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
 }
 
 // ------------------------------------------------------------------ host
