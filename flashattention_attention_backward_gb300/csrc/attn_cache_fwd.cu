@@ -33,6 +33,7 @@
 // CTA finds its part of the line itself, from two sums over the sequences.
 //   warp 0      Q of each tile; K in a ring of 2 stages (d <= 128) or 1
 //   warp 2      V in the same kind of ring
+//   warp 3      zeroes rows of V
 //   warp 1      MMA issuer: per tile S(0), then per block S(j + 1), P(j) V
 //   warps 4-11  softmax: warpgroup h takes keys 64 h .. 64 h + 63 of each block
 //               and columns h d/2 .. of O; then the tile's epilogue
@@ -57,6 +58,7 @@ constexpr int kBm = 128;  // rows of a tile (tensor-memory lanes)
 constexpr int kBn = 128;  // keys per block
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
+constexpr int kTileUnits = 2;  // what a tile costs besides its blocks, in blocks
 constexpr int kMaxCtas = 192;  // parts of the line at most (the workspace's size)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -64,29 +66,40 @@ constexpr float kRescale = 8.f;  // move the shift only when the maximum grows b
 constexpr long long kWaitLimitCycles = 2000000000LL;  // about one second
 
 // The softmax warps' state does not fit in the 168 registers that 384 threads are
-// launched with: setmaxnreg moves registers to them from the loaders and the MMA
-// warp.
-constexpr int kRegsSoftmax = 216, kRegsCtl = 72;
-static_assert(256 * kRegsSoftmax + 128 * kRegsCtl <= 384 * 168, "register pool");
+// launched with: setmaxnreg moves registers to them from the other four warps.
+template <int D>
+constexpr int kRegsSoftmax = D == 256 ? 200 : 216;
+template <int D>
+constexpr int kRegsCtl = D == 256 ? 96 : 72;
+static_assert(256 * kRegsSoftmax<256> + 128 * kRegsCtl<256> <= 384 * 168, "register pool");
+static_assert(256 * kRegsSoftmax<128> + 128 * kRegsCtl<128> <= 384 * 168, "register pool");
 
 template <int D>
 struct Layout {
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kStages = D <= 128 ? 2 : 1;   // of K, of V, of Q
-  static constexpr int kOBufs = D <= 128 ? 2 : 1;    // O accumulators in tensor memory
+  // K and V stages: an SM's share of the memory bandwidth wants some 100 KB in flight
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 2 : 1;
+  static constexpr int kQStages = D <= 128 ? 2 : 1;
+  static constexpr int kOBufs = D <= 128 ? 2 : 1;  // O accumulators in tensor memory
+  // rows of a narrow tile: the 4 copies' O in fp32 fill the warps' stages
+  static constexpr int kNarrow = D <= 128 ? 1024 / D : 0;
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + kStages * kTileBytes;
+  static constexpr int kK = kQ + kQStages * kTileBytes;
   static constexpr int kV = kK + kStages * kTileBytes;
-  // the softmax warpgroups' half-row maxima (two blocks in flight) and row sums:
-  // [2][2][128] + [2][128] fp32
-  static constexpr int kXchg = kV + kStages * kTileBytes;
+  // 2 KB for each softmax warp: rows of O on their way to coalesced stores
+  static constexpr int kStage = kV + kStages * kTileBytes;
+  // the softmax warpgroups' half-row maxima (two blocks in flight), the row sums
+  // of a finished tile: [2][2][128] + [2][128] fp32
+  static constexpr int kXchg = kStage + 8 * 2048;
   static constexpr int kBars = kXchg + 6 * 128 * 4;
-  static constexpr int kNumBars = 24;
+  static constexpr int kNumBars = 35;
   static constexpr int kSums = kBars + kNumBars * 8;   // [kWarps] long long
   static constexpr int kPart = kSums + kWarps * 8;     // Part
   static constexpr int kTmemSlot = kPart + 48;
   static constexpr int kAbort = kTmemSlot + 4;
-  static constexpr int kUsed = kAbort + 12;
+  // narrow tiles (d <= 128): the quadrants' shifts, [128] fp32
+  static constexpr int kShifts = kAbort + 12;
+  static constexpr int kUsed = kShifts + (D <= 128 ? 512 : 0);
   // more than half of the SM's shared memory, so that a second CTA never waits
   // on the first one's tensor memory
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
@@ -98,16 +111,16 @@ enum Bar {
   BAR_Q_FULL = 0,    // + Q stage
   BAR_Q_EMPTY = 2,   // + Q stage: the tile's last S GEMM has read it
   BAR_K_FULL = 4,    // + stage
-  BAR_K_EMPTY = 6,   // + stage
   BAR_V_FULL = 8,    // + stage
-  BAR_V_EMPTY = 10,  // + stage
-  BAR_S_FULL = 12,   // + S buffer (block parity): S of the block written
-  BAR_P_FULL = 14,   // + S buffer: P of the block written (and O rescaled if needed)
-  BAR_O_DONE = 16,   // P V of a block completed (one phase per key block)
-  BAR_O_LAST = 17,   // the tile's last P V completed (one phase per tile)
-  BAR_O_FREE = 18,   // + O buffer: the tile's epilogue has read O
-  BAR_V_EDGE = 20,   // + stage: copies of a V block some of whose rows are then zeroed
-  BAR_DRAIN = 22,    // abort path only: completion of everything issued
+  BAR_V_EDGE = 12,   // + stage: copies of a V block some of whose rows are then zeroed
+  BAR_S_DONE = 16,   // + block parity: S of the block written, its K read
+  BAR_P_FULL = 18,   // + block parity: P of the block written (and O rescaled if needed)
+  BAR_O_DONE = 20,   // + block parity: P V of the block completed, its V read
+  BAR_O_LAST = 22,   // + O buffer: the tile's last P V completed
+  BAR_O_FREE = 24,   // + O buffer: the tile's epilogue has read O
+  BAR_K_EMPTY = 26,  // + stage, where there are more than two: its K read
+  BAR_V_EMPTY = 30,  // + stage, where there are more than two: its V read
+  BAR_DRAIN = 34,    // abort path only: completion of everything issued
 };
 
 __device__ int g_status;
@@ -130,6 +143,7 @@ struct Params {
   long long o_token, o_head;
   char* workspace;
   int H, H_kv, G, tokens;  // tokens of a full tile: 128 / G
+  int narrow;              // rows of a narrow tile's copy of the queries, 0: none narrow
   int box;                 // slots of one TMA box: gcd(page_size, 128)
   int cap;                 // positions that the page table holds
   int whole;               // parts end at tiles' ends: no tile is shared, nothing to join
@@ -198,6 +212,7 @@ struct Tile {
   int pos0, count;  // position of its first token, its tokens
   int lo, hi, sinks;
   int j0, ns, nt;
+  __device__ __forceinline__ int units() const { return nt + kTileUnits; }
   __device__ __forceinline__ int block(int t) const { return t < ns ? t : j0 + t - ns; }
 };
 __device__ __forceinline__ Tile tile_of(const Params& p, const Seq& s, int tile) {
@@ -214,31 +229,49 @@ __device__ __forceinline__ Tile tile_of(const Params& p, const Seq& s, int tile)
   if (t.lo <= t.hi) {
     t.ns = min(t.j0, sink_blocks);
     t.nt = t.ns + t.hi / kBn - t.j0 + 1;
-  } else {
+  } else {  // no band: only sinks, if any
     t.ns = sink_blocks;
     t.nt = max(1, sink_blocks);
     t.j0 = 0;
+    t.lo = 1 << 30;  // above every key
   }
   return t;
 }
 
-// Blocks of one key/value head's tiles of a sequence, summed by a whole warp.
-__device__ __forceinline__ long long head_blocks(const Params& p, const Seq& s) {
+// A narrow tile (with a softcap; at most 8 rows at d = 128, 16 at d = 64) has four
+// copies of its queries, in rows 0, 32, 64 and 96 of the tile, and the warps of each
+// quadrant of tensor memory take a quarter of every block's keys. With its rows in
+// one quadrant the softmax of a block is two warps' work, the others idle: with the
+// softcap's tanh that takes longer than the block's loads (64 requests of up to 8192
+// keys, 32 heads over 8, d = 128: 253 us, 183 narrow). Without a softcap the loads
+// take longer either way (183 and 182 us), and short sequences pay for the joining
+// of the copies (256 requests of up to 300 keys 71 us, 74 narrow).
+template <int D, bool SOFTCAP>
+constexpr bool kHasNarrow = SOFTCAP && D <= 128;
+template <int D, bool SOFTCAP>
+__device__ __forceinline__ bool is_narrow(const Params& p, const Tile& t) {
+  return kHasNarrow<D, SOFTCAP> && t.count * p.G <= p.narrow;
+}
+
+// The line is measured in units: a block is one, and a tile has kTileUnits in
+// front of its first (its queries, its epilogue). Units of one key/value head's
+// tiles of a sequence, summed by a whole warp:
+__device__ __forceinline__ long long head_units(const Params& p, const Seq& s) {
   const int lane = threadIdx.x & 31;
   long long sum = 0;
-  for (int i = lane; i < s.tiles; i += 32) sum += tile_of(p, s, i).nt;
+  for (int i = lane; i < s.tiles; i += 32) sum += tile_of(p, s, i).units();
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   return sum;
 }
 
-// Blocks of one key/value head for sequence b0 + lane (0 past the end), a whole
-// warp together: sequences of one tile in parallel, longer ones one by one.
-__device__ __forceinline__ long long lane_blocks(const Params& p, int b0, int end) {
+// The same for sequence b0 + lane (0 past the end), a whole warp together:
+// sequences of one tile in parallel, longer ones one by one.
+__device__ __forceinline__ long long lane_units(const Params& p, int b0, int end) {
   const int lane = threadIdx.x & 31;
   Seq s{};
   if (b0 + lane < end) s = seq_of(p, b0 + lane);
-  long long blocks = s.tiles == 1 ? tile_of(p, s, 0).nt : 0;
+  long long units = s.tiles == 1 ? tile_of(p, s, 0).units() : 0;
   uint32_t more = __ballot_sync(0xffffffffu, s.tiles > 1);
   while (more != 0) {
     const int src = __ffs(more) - 1;
@@ -249,22 +282,22 @@ __device__ __forceinline__ long long lane_blocks(const Params& p, int b0, int en
     o.length = __shfl_sync(0xffffffffu, s.length, src);
     o.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
     o.tiles = __shfl_sync(0xffffffffu, s.tiles, src);
-    const long long sum = head_blocks(p, o);
-    if (lane == src) blocks = sum;
+    const long long sum = head_units(p, o);
+    if (lane == src) units = sum;
   }
-  return blocks;
+  return units;
 }
 
-// A CTA's part of the line: where it begins, how many blocks it has, and how many
-// a full part has.
+// A CTA's part of the line: the tile and the unit of it where it begins, how many
+// units it has, how many a full part has, and the units before it.
 struct Part {
-  int b, kvh, tile, blk;
+  int b, kvh, tile, at;
   long long count, share, first;
 };
 
 // Finds the CTA's part (every thread of the CTA calls; `sums` and `part` in
-// shared memory). Warp w sums the blocks of its chunk of the sequences, 32 at a
-// time; the warp whose chunk holds the part's first block then looks for it there
+// shared memory). Warp w sums the units of its chunk of the sequences, 32 at a
+// time; the warp whose chunk holds the part's first unit then looks for it there
 // (a chunk of up to 32 sequences, so up to 384 in all, is not summed again).
 __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part* part) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -272,7 +305,7 @@ __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part
   const int chunk = (B + kWarps - 1) / kWarps;
   const int first = min(B, warp * chunk), end = min(B, first + chunk);
   long long sum = 0, mine = 0;
-  for (int b = first; b < end; b += 32) sum += mine = lane_blocks(p, b, end);
+  for (int b = first; b < end; b += 32) sum += mine = lane_units(p, b, end);
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (lane == 0) sums[warp] = sum * p.H_kv;
@@ -288,8 +321,8 @@ __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part
   if (u0 < total && u0 >= before && u0 < before + sums[warp]) {
     long long at = u0 - before;  // within this warp's chunk
     for (int b = first; b < end; b += 32) {
-      const long long blocks = (chunk <= 32 ? mine : lane_blocks(p, b, end)) * p.H_kv;
-      long long upto = blocks;  // inclusive sum over the lanes
+      const long long units = (chunk <= 32 ? mine : lane_units(p, b, end)) * p.H_kv;
+      long long upto = units;  // inclusive sum over the lanes
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, upto, off);
@@ -301,14 +334,14 @@ __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part
         continue;
       }
       const int src = __ffs(past) - 1;
-      const long long per_head = __shfl_sync(0xffffffffu, blocks, src) / p.H_kv;
-      at -= __shfl_sync(0xffffffffu, upto - blocks, src);
+      const long long per_head = __shfl_sync(0xffffffffu, units, src) / p.H_kv;
+      at -= __shfl_sync(0xffffffffu, upto - units, src);
       const int kvh = static_cast<int>(at / per_head);
       at -= kvh * per_head;
       const Seq s = seq_of(p, b + src);
       for (int i = 0; i < s.tiles; i += 32) {
-        const int nt = i + lane < s.tiles ? tile_of(p, s, i + lane).nt : 0;
-        int sum_to = nt;
+        const int here = i + lane < s.tiles ? tile_of(p, s, i + lane).units() : 0;
+        int sum_to = here;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
           const int v = __shfl_up_sync(0xffffffffu, sum_to, off);
@@ -320,12 +353,12 @@ __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part
           continue;
         }
         const int t = __ffs(in) - 1;
-        at -= __shfl_sync(0xffffffffu, sum_to - nt, t);
+        at -= __shfl_sync(0xffffffffu, sum_to - here, t);
         if (lane == 0) {
           part->b = b + src;
           part->kvh = kvh;
           part->tile = i + t;
-          part->blk = static_cast<int>(at);
+          part->at = static_cast<int>(at);
           part->share = share;
           part->first = u0;
           part->count = min(share, total - u0);
@@ -338,44 +371,44 @@ __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part
   __syncthreads();
 }
 
-// Walks the tiles of a part; every role has its own.
+// Walks the tiles of a part; every role has its own, and one call of step(): it is
+// inlined, and more copies of it move the code of the roles' blocks apart, which
+// then misses the instruction cache (a chunk of 2048 tokens over 18432 keys took
+// 463 us with three, TODO with one).
 struct Walk {
-  int b, kvh, tile, blk, take, left;
+  int b, kvh, next, at, left;  // what comes: a tile, from which unit of it on; units left
+  int tile, blk, take;         // the tile's blocks blk .. blk + take - 1 are the part's
   Seq s;
   Tile t;
-  __device__ __forceinline__ void begin(const Params& p, const Part& part) {
-    b = part.b;
-    kvh = part.kvh;
-    tile = part.tile;
-    blk = part.blk;
-    left = static_cast<int>(part.count);
-    if (left > 0) {
-      s = seq_of(p, b);
-      t = tile_of(p, s, tile);
-      take = min(t.nt - blk, left);
-      if (p.whole) {  // a tile belongs to the part that holds its first block
-        if (blk > 0)
-          next(p);
-        else
-          take = t.nt;
-      }
-    }
+  __device__ __forceinline__ Walk(const Params& p, const Part& part)
+      : b(part.b), kvh(part.kvh), next(part.tile), at(part.at),
+        left(static_cast<int>(part.count)) {
+    if (left > 0) s = seq_of(p, b);
   }
-  __device__ __forceinline__ void next(const Params& p) {
-    left -= take;
-    if (left <= 0) return;
-    blk = 0;
-    if (++tile == s.tiles) {
-      tile = 0;
-      if (++kvh == p.H_kv) {
-        kvh = 0;
-        do {  // left > 0: a sequence with tiles follows
-          s = seq_of(p, ++b);
-        } while (s.tiles == 0 && b + 1 < p.batch.B);
+  // The next tile; false behind the last. A part that ends in the units before a
+  // tile's first block leaves the tile to the next one.
+  __device__ __forceinline__ bool step(const Params& p) {
+    bool skip;
+    do {
+      if (left <= 0) return false;
+      if (next == s.tiles) {
+        next = 0;
+        if (++kvh == p.H_kv) {
+          kvh = 0;
+          do {  // left > 0: a sequence with tiles follows
+            s = seq_of(p, ++b);
+          } while (s.tiles == 0 && b + 1 < p.batch.B);
+        }
       }
-    }
-    t = tile_of(p, s, tile);
-    take = p.whole ? t.nt : min(t.nt, left);
+      tile = next++;
+      t = tile_of(p, s, tile);
+      blk = max(0, at - kTileUnits);
+      take = max(0, (p.whole ? t.nt : min(t.nt, at + left - kTileUnits)) - blk);
+      left -= t.units() - at;  // below 0: the tile goes on in the next part
+      skip = p.whole && at > 0;  // a whole tile belongs to the part that holds its first unit
+      at = 0;
+    } while (skip);
+    return take > 0;
   }
 };
 
@@ -425,66 +458,52 @@ __device__ __forceinline__ void load_pieces(const Ctx& c, const Params& p, const
   __syncwarp();
 }
 
-// A V block with rows that no row of its tile sees, on its way into stage st.
-struct Edge {
-  int st = -1, n0 = 0, lo = 0, hi = 0, sinks = 0;
-  bool copied = false;  // some of its pieces are loaded
-};
-// Zeroes those rows once the copies have landed and hands the stage over. Bit st of
-// `parity` is that of the stage's next copies.
-template <int D>
-__device__ __forceinline__ bool finish_edge(const Ctx& c, Edge& e, uint32_t& parity,
-                                            uint8_t* ring) {
-  if (e.st < 0) return true;
-  const int lane = threadIdx.x & 31;
-  if (e.copied) {
-    if (!wait_warp(c, BAR_V_EDGE + e.st, (parity >> e.st) & 1)) return false;
-    parity ^= 1u << e.st;
-  }
-  for (int r = lane >> 3; r < kBn; r += 4) {  // 8 lanes a row
-    const int key = e.n0 + r;
-    if (key <= e.hi && (key >= e.lo || key < e.sinks)) continue;
-#pragma unroll
-    for (int cb = 0; cb < D / 64; ++cb)
-      *reinterpret_cast<uint4*>(ring + e.st * Layout<D>::kTileBytes + cb * 16384 + r * 128 +
-                                (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar_addr(c, BAR_V_FULL + e.st));
-  e.st = -1;
-  return true;
+// Waits until stage g mod kS of K or of V has been read by block g - kS. With two
+// stages or one the barriers of the products serve: no block of that parity behind
+// g - kS can have completed, so that the phase is that block's.
+template <int D, bool IS_V>
+__device__ __forceinline__ bool wait_stage(const Ctx& c, int g) {
+  constexpr int kS = Layout<D>::kStages;
+  const int before = g - kS;
+  if (before < 0) return true;
+  if (kS > 2)
+    return wait_warp(c, (IS_V ? BAR_V_EMPTY : BAR_K_EMPTY) + g % kS, (before / kS) & 1);
+  return wait_warp(c, (IS_V ? BAR_O_DONE : BAR_S_DONE) + (before & 1), (before >> 1) & 1);
+}
+
+// Whether a block of a tile has keys that no row of the tile sees.
+__device__ __forceinline__ bool is_cut(const Tile& t, int n0) {
+  return n0 + kBn - 1 > t.hi || (n0 < t.lo && n0 + kBn > t.sinks);
 }
 
 // Warp 0: Q of each tile and its K blocks; warp 2: the V blocks. Each ring waits
-// for its own stages, in the order the tensor cores finish them. A V block whose
-// rows are to be zeroed is finished behind the next block's request, so that its
-// copies' latency does not leave the ring empty.
-template <int D, bool IS_V>
-__device__ void loader_role(const Ctx& c, const Params& p, const Part& part, uint8_t* smem,
-                            uint32_t sbase, const CUtensorMap* tq, const CUtensorMap* tkv) {
+// for its own stages, in the order the tensor cores finish them.
+template <int D, bool SOFTCAP, bool IS_V>
+__device__ void loader_role(const Ctx& c, const Params& p, const Part& part, uint32_t sbase,
+                            const CUtensorMap* tq, const CUtensorMap* tqn,
+                            const CUtensorMap* tkv) {
   using L = Layout<D>;
-  constexpr int kS = L::kStages;
+  constexpr int kS = L::kStages, kQS = L::kQStages;
   const int lane = threadIdx.x & 31;
   const int bar_full = IS_V ? BAR_V_FULL : BAR_K_FULL;
-  const int bar_empty = IS_V ? BAR_V_EMPTY : BAR_K_EMPTY;
   const int ring = IS_V ? L::kV : L::kK;
   int g = 0, i = 0;  // blocks and tiles issued
-  Edge edge;
-  uint32_t edge_parity = 0;
   bool ok = true;
-  Walk w;
-  for (w.begin(p, part); ok && w.left > 0; w.next(p), ++i) {
+  Walk w(p, part);
+  for (; ok && w.step(p); ++i) {
     if (!IS_V) {
-      const int qs = i % kS;
-      if (i >= kS && !(ok = wait_warp(c, BAR_Q_EMPTY + qs, ((i / kS) - 1) & 1))) break;
+      const int qs = i % kQS;
+      if (i >= kQS && !(ok = wait_warp(c, BAR_Q_EMPTY + qs, ((i / kQS) - 1) & 1))) break;
       if (lane == 0) {
         if (p.batch.lengths[w.b] > p.cap) record_status(ATTN_ERR_PAGE);
-        mbar_arrive_expect_tx(bar_addr(c, BAR_Q_FULL + qs), p.tokens * p.G * (D * 2));
-        for (int cb = 0; cb < D / 64; ++cb)
-          tma_load_4d(sbase + L::kQ + qs * L::kTileBytes + cb * 16384, tq,
-                      bar_addr(c, BAR_Q_FULL + qs), 64 * cb, 0, w.kvh,
-                      w.s.row0 + w.tile * p.tokens);
+        const bool narrow = is_narrow<D, SOFTCAP>(p, w.t);
+        const int rows = narrow ? 4 * p.narrow : p.tokens * p.G;
+        mbar_arrive_expect_tx(bar_addr(c, BAR_Q_FULL + qs), rows * (D * 2));
+        for (int copy = 0; copy < (narrow ? 4 : 1); ++copy)
+          for (int cb = 0; cb < D / 64; ++cb)
+            tma_load_4d(sbase + L::kQ + qs * L::kTileBytes + cb * 16384 + copy * 4096,
+                        narrow ? tqn : tq, bar_addr(c, BAR_Q_FULL + qs), 64 * cb, 0, w.kvh,
+                        w.s.row0 + w.tile * p.tokens);
       }
       __syncwarp();
     }
@@ -494,39 +513,63 @@ __device__ void loader_role(const Ctx& c, const Params& p, const Part& part, uin
     for (int t = 0; t < w.take; ++t, ++g) {
       const Pieces x = next;
       if (t + 1 < w.take) next = pieces_of(p, w, w.blk + t + 1);
+      if (!(ok = wait_stage<D, IS_V>(c, g))) break;
       const int st = g % kS;
-      // with one stage the block before has to be finished first
-      if (IS_V && kS == 1 && !(ok = finish_edge<D>(c, edge, edge_parity, smem + ring))) break;
-      if (g >= kS && !(ok = wait_warp(c, bar_empty + st, ((g / kS) - 1) & 1))) break;
-      const uint32_t dst = sbase + ring + st * L::kTileBytes;
-      const int n0 = w.t.block(w.blk + t) * kBn;
-      const bool cut = IS_V && (n0 + kBn - 1 > w.t.hi || (n0 < w.t.lo && n0 + kBn > w.t.sinks));
+      const bool cut = IS_V && is_cut(w.t, w.t.block(w.blk + t) * kBn);
+      // what zero_role finishes completes on a barrier of its own, if at all
       if (!cut || x.needed != 0)
-        load_pieces<D>(c, p, x, w.kvh, dst, tkv, cut ? BAR_V_EDGE + st : bar_full + st);
-      if (IS_V) {
-        if (!(ok = finish_edge<D>(c, edge, edge_parity, smem + ring))) break;
-        if (cut) {
-          edge.st = st;
-          edge.n0 = n0;
-          edge.lo = w.t.lo;
-          edge.hi = w.t.hi;
-          edge.sinks = w.t.sinks;
-          edge.copied = x.needed != 0;
-        }
-      }
+        load_pieces<D>(c, p, x, w.kvh, sbase + ring + st * L::kTileBytes, tkv,
+                       cut ? BAR_V_EDGE + st : bar_full + st);
     }
   }
-  if (IS_V && ok) ok = finish_edge<D>(c, edge, edge_parity, smem + ring);
   // When aborting, the copies in flight must land before the CTA exits (a phase
   // that was never begun ends the wait by its limit).
   if (!ok || *c.abort) {
-    for (int st = 0; st < kS; ++st) {
-      const int uses = (g + kS - st) / kS;  // blocks that went to this stage, or one more
-      wait_drain(c, bar_full + st, (uses > 0 ? uses - 1 : 0) & 1);
-      if (IS_V) wait_drain(c, BAR_V_EDGE + st, (edge_parity >> st) & 1);
-      if (!IS_V) wait_drain(c, BAR_Q_FULL + st, (i / kS) & 1);
+    for (int st = 0; st < kS; ++st)
+      wait_drain(c, bar_full + st, ((g + kS - st) / kS - 1) & 1);
+    if (!IS_V)
+      for (int st = 0; st < kQS; ++st) wait_drain(c, BAR_Q_FULL + st, (i / kQS) & 1);
+  }
+}
+
+// Warp 3: sets the rows of V that no row of the tile sees to zero, in the blocks
+// that have such rows, once their copies have landed, and hands the stage on.
+template <int D>
+__device__ void zero_role(const Ctx& c, const Params& p, const Part& part, uint8_t* smem) {
+  using L = Layout<D>;
+  constexpr int kS = L::kStages;
+  const int lane = threadIdx.x & 31;
+  uint32_t parity = 0;  // bit st: that of the stage's next copies
+  int g = 0;
+  bool ok = true;
+  Walk w(p, part);
+  while (ok && w.step(p)) {
+    for (int t = 0; t < w.take; ++t, ++g) {
+      const int n0 = w.t.block(w.blk + t) * kBn, st = g % kS;
+      if (!is_cut(w.t, n0)) continue;
+      const int key = n0 + 4 * lane;  // any of the block's keys visible: it has copies
+      const bool seen = (key <= w.t.hi && key + 3 >= w.t.lo) || key < w.t.sinks;
+      if (__any_sync(0xffffffffu, seen)) {
+        if (!(ok = wait_warp(c, BAR_V_EDGE + st, (parity >> st) & 1))) break;
+        parity ^= 1u << st;
+      } else if (!(ok = wait_stage<D, true>(c, g))) {
+        break;
+      }
+      for (int r = lane >> 3; r < kBn; r += 4) {  // 8 lanes a row
+        const int k = n0 + r;
+        if (k <= w.t.hi && (k >= w.t.lo || k < w.t.sinks)) continue;
+#pragma unroll
+        for (int cb = 0; cb < D / 64; ++cb)
+          *reinterpret_cast<uint4*>(smem + L::kV + st * L::kTileBytes + cb * 16384 + r * 128 +
+                                    (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_addr(c, BAR_V_FULL + st));
     }
   }
+  if (!ok || *c.abort)
+    for (int st = 0; st < kS; ++st) wait_drain(c, BAR_V_EDGE + st, (parity >> st) & 1);
 }
 
 // ------------------------------------------------------------------ MMA issuer
@@ -541,89 +584,83 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn_major) {
 // 1) was read by P(g - 1) V, issued before), also where block g + 1 begins the next
 // tile and two Q stages hold both tiles' queries, so that the softmax finds its
 // scores behind the epilogue; then P(g) V into the tile's O buffer once the
-// softmax has written P(g).
+// softmax has written P(g). One thread does all of it: few MMAs can be queued, so
+// what it spends between the last MMA of one product and the first of the next is
+// time of the tensor cores (with the whole warp in the loop, votes behind every
+// wait and a commit for each of the loaders, a chunk of 2048 tokens over 18432 keys
+// took 468 us, TODO so).
 template <typename T, int D>
-__device__ void mma_role(const Ctx& c, const Params& p, const Part& part, uint32_t sbase,
-                         uint32_t tmem) {
+__device__ __forceinline__ void issue_mmas(const Ctx& c, const Params& p, const Part& part,
+                                           uint32_t sbase, uint32_t tmem) {
   using L = Layout<D>;
-  constexpr int kS = L::kStages, kOB = L::kOBufs;
-  const bool leader = elect_one_sync() != 0;
+  constexpr int kS = L::kStages, kQS = L::kQStages, kOB = L::kOBufs;
   constexpr uint32_t kIdS = idesc<T>(kBm, kBn, false);  // S = Q K^T
   constexpr uint32_t kIdO = idesc<T>(kBm, D, true);     // O += P V
   auto kmaj = [](int k) { return static_cast<uint32_t>(((k >> 2) * 16384 + (k & 3) * 32) >> 4); };
   auto mnmaj = [](int k) { return static_cast<uint32_t>((2048 * k) >> 4); };
+  const uint32_t q_0 = sdesc_lo(sbase + L::kQ, 16), k_0 = sdesc_lo(sbase + L::kK, 16);
+  const uint32_t v_0 = sdesc_lo(sbase + L::kV, 16384);
+  constexpr uint32_t kStep = L::kTileBytes >> 4;  // from one stage's descriptor to the next
   // S of block g of tile i; `first`, `last` of the tile's blocks
   auto issue_s = [&](int g, int i, bool first, bool last) -> bool {
-    const int st = g % kS, qs = i % kS;
-    if (first && !wait_warp(c, BAR_Q_FULL + qs, (i / kS) & 1)) return false;
-    if (!wait_warp(c, BAR_K_FULL + st, (g / kS) & 1)) return false;
-    tc_fence_after();
-    if (leader) {
-      const uint32_t q_lo = sdesc_lo(sbase + L::kQ + qs * L::kTileBytes, 16);
-      const uint32_t k_lo = sdesc_lo(sbase + L::kK + st * L::kTileBytes, 16);
+    const int st = g % kS, qs = i % kQS;
+    if (first && !wait(c, BAR_Q_FULL + qs, (i / kQS) & 1)) return false;
+    if (!wait(c, BAR_K_FULL + st, (g / kS) & 1)) return false;
+    const uint32_t q_lo = q_0 + qs * kStep, k_lo = k_0 + st * kStep, s_to = tmem + (g & 1) * 128;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_ss(tmem + (g & 1) * 128, sdesc_from_lo(q_lo + kmaj(k)), sdesc_from_lo(k_lo + kmaj(k)),
-               kIdS, k > 0);
-      mma_commit(bar_addr(c, BAR_S_FULL + (g & 1)));
-      mma_commit(bar_addr(c, BAR_K_EMPTY + st));
-      if (last) mma_commit(bar_addr(c, BAR_Q_EMPTY + qs));
-    }
+    for (int k = 0; k < D / 16; ++k)
+      mma_ss(s_to, sdesc_from_lo(q_lo + kmaj(k)), sdesc_from_lo(k_lo + kmaj(k)), kIdS, k > 0);
+    mma_commit(bar_addr(c, BAR_S_DONE + (g & 1)));
+    if (kS > 2) mma_commit(bar_addr(c, BAR_K_EMPTY + st));
+    if (last) mma_commit(bar_addr(c, BAR_Q_EMPTY + qs));
     return true;
   };
   bool ok = true;
-  Walk w;
-  w.begin(p, part);
-  if (w.left > 0) {
-    int nt = w.take, next_nt = 0;
-    ok = issue_s(0, 0, true, nt == 1);
-    for (int g = 0, i = 0, t = 0; ok; ++g) {
-      const bool last = t + 1 == nt;
-      bool more = !last;
-      if (last) {
-        w.next(p);
-        more = w.left > 0;
-        next_nt = w.take;
-      }
-      const bool ahead = kS >= 2 || !last;
-      if (more && ahead &&
-          !(ok = issue_s(g + 1, last ? i + 1 : i, last, last ? next_nt == 1 : t + 2 == nt)))
-        break;
-      if (!(ok = wait_warp(c, BAR_P_FULL + (g & 1), (g >> 1) & 1))) break;
+  Walk w(p, part);
+  // block g, number t of the nt of tile i, is the next P V; none yet at -1
+  int g = -1, i = -1, t = 0, nt = 0;
+  for (;;) {
+    const bool last = t + 1 >= nt;
+    const bool more = last ? w.step(p) : true;
+    const int next_nt = w.take;
+    const bool ahead = kQS >= 2 || !last || g < 0;
+    if (more && ahead &&
+        !(ok = issue_s(g + 1, last ? i + 1 : i, last, last ? next_nt == 1 : t + 2 == nt)))
+      break;
+    if (g >= 0) {
       const int vs = g % kS, ob = i % kOB;
-      if (!(ok = wait_warp(c, BAR_V_FULL + vs, (g / kS) & 1))) break;
-      if (t == 0 && i >= kOB && !(ok = wait_warp(c, BAR_O_FREE + ob, ((i / kOB) - 1) & 1)))
-        break;
+      const uint32_t v_lo = v_0 + vs * kStep, p_at = tmem + (g & 1) * 128;
+      const uint32_t o_to = tmem + 256 + ob * D;
+      if (!(ok = wait(c, BAR_V_FULL + vs, (g / kS) & 1))) break;
+      if (t == 0 && i >= kOB && !(ok = wait(c, BAR_O_FREE + ob, ((i / kOB) - 1) & 1))) break;
+      if (!(ok = wait(c, BAR_P_FULL + (g & 1), (g >> 1) & 1))) break;
       tc_fence_after();
-      if (leader) {
-        const uint32_t v_mn = sdesc_lo(sbase + L::kV + vs * L::kTileBytes, 16384);
-        // A = P (pairs in the S buffer of block g: keys 0-63 in columns 0-31,
-        // keys 64-127 in columns 64-95, one half per softmax warpgroup)
+      // A = P (pairs in the S buffer of block g: keys 0-63 in columns 0-31,
+      // keys 64-127 in columns 64-95, one half per softmax warpgroup)
 #pragma unroll
-        for (int k = 0; k < kBn / 16; ++k)
-          mma_ts(tmem + 256 + ob * D, tmem + (g & 1) * 128 + 8 * k + (k >= 4 ? 32 : 0),
-                 sdesc_from_lo(v_mn + mnmaj(k)), kIdO, (t > 0 || k > 0) ? 1u : 0u);
-        mma_commit(bar_addr(c, BAR_O_DONE));
-        mma_commit(bar_addr(c, BAR_V_EMPTY + vs));
-        if (last) mma_commit(bar_addr(c, BAR_O_LAST));
-      }
-      if (!more) break;
-      if (!ahead && !(ok = issue_s(g + 1, i + 1, true, next_nt == 1))) break;
-      if (last) {
-        nt = next_nt;
-        t = 0;
-        ++i;
-      } else {
-        ++t;
-      }
+      for (int k = 0; k < kBn / 16; ++k)
+        mma_ts(o_to, p_at + 8 * k + (k >= 4 ? 32 : 0), sdesc_from_lo(v_lo + mnmaj(k)), kIdO,
+               (t > 0 || k > 0) ? 1u : 0u);
+      mma_commit(bar_addr(c, BAR_O_DONE + (g & 1)));
+      if (kS > 2) mma_commit(bar_addr(c, BAR_V_EMPTY + vs));
+      if (last) mma_commit(bar_addr(c, BAR_O_LAST + ob));
     }
+    if (!more) break;
+    if (!ahead && !(ok = issue_s(g + 1, i + 1, true, next_nt == 1))) break;
+    if (last) {
+      nt = next_nt;
+      t = 0;
+      ++i;
+    } else {
+      ++t;
+    }
+    ++g;
   }
-  if (__any_sync(0xffffffffu, !ok || *c.abort != 0)) {
+  if (!ok || *c.abort != 0) {
     // completion of everything issued before tensor memory is released
-    if (leader) mma_commit(bar_addr(c, BAR_DRAIN));
+    mma_commit(bar_addr(c, BAR_DRAIN));
     wait_drain(c, BAR_DRAIN, 0);
   }
-  __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax
@@ -710,9 +747,252 @@ __device__ __forceinline__ float chunk_p(const Params& p, const uint32_t (&raw)[
 
 constexpr int kBarBoth = 3;  // named barrier of both softmax warpgroups
 
+// O (this warp's lanes, D / 2 columns from tO on) times f, 32 columns at a time.
+template <int D>
+__device__ __forceinline__ void scale_o(uint32_t tO, float f) {
+  const uint64_t f2 = f2_make(f, f);
+#pragma unroll
+  for (int c32 = 0; c32 < D / 64; ++c32) {
+    uint32_t o[32];
+    tmem_ld32(tO + c32 * 32, o);
+    uint32_t a[16], b[16];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint64_t v = f2_mul(f2_make(o[2 * u], o[2 * u + 1]), f2);
+      const uint64_t x = f2_mul(f2_make(o[16 + 2 * u], o[17 + 2 * u]), f2);
+      a[2 * u] = static_cast<uint32_t>(v);
+      a[2 * u + 1] = static_cast<uint32_t>(v >> 32);
+      b[2 * u] = static_cast<uint32_t>(x);
+      b[2 * u + 1] = static_cast<uint32_t>(x >> 32);
+    }
+    tmem_st16(tO + c32 * 32, a);
+    tmem_st16(tO + c32 * 32 + 16, b);
+  }
+}
+
+// One row's running shift (log2 units) and sum.
+struct Stats {
+  float m, l;
+};
+
+// Takes the block's row maximum of raw scores in: moves the shift when the maximum
+// outgrows it by more than kRescale, and then scales l and, once P V of block g - 1
+// has completed, O. Returns the shift to use.
+template <int D, bool SOFTCAP>
+__device__ __forceinline__ float take_max(const Ctx& c, Stats& x, float smax, float c_log2,
+                                          float cap_in, float cap_out, bool has_o, int g,
+                                          uint32_t tO, bool& ok) {
+  float m_tile = -INFINITY;  // row maximum of the logits (log2 units) over this block
+  if (smax > -INFINITY) {
+    if (SOFTCAP) {
+      const float ex = ex2_approx(smax * cap_in);
+      m_tile = (1.f - 2.f * rcp_approx(ex + 1.f)) * cap_out;
+    } else {
+      m_tile = smax * c_log2;
+    }
+  }
+  const bool need = m_tile > x.m + kRescale;
+  if (__any_sync(0xffffffffu, need)) {
+    const float m_new = need ? m_tile : x.m;
+    const float f = need ? ex2_approx(x.m - m_new) : 1.f;  // 0 while m = -inf
+    // a wait that gives up is voted on at the next barrier
+    if (__any_sync(0xffffffffu, need && x.m > -INFINITY) && has_o) {
+      if (!wait_warp(c, BAR_O_DONE + ((g - 1) & 1), ((g - 1) >> 1) & 1)) ok = false;
+      if (ok) {
+        tc_fence_after();
+        scale_o<D>(tO, f);
+      }
+    }
+    x.l *= f;
+    x.m = m_new;
+  }
+  return x.m > -INFINITY ? x.m : 0.f;
+}
+
+// Writes 64 bytes of each of the warp's 32 rows through `stage` (2 KB of the
+// warp's own), so that neighbouring lanes store neighbouring pieces of a row: lane
+// r comes with row r's pieces and its address, 0 for none.
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&v)[16],
+                                           unsigned long long address) {
+  const int lane = threadIdx.x & 31;
+  // piece j of row r at 4 r + (j ^ (r / 2 mod 4)): eight neighbouring lanes, on
+  // either side, are on all banks
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(stage + (lane * 4 + (j ^ ((lane >> 1) & 3))) * 16) =
+        make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  __syncwarp();
+  const int j = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 8 * i + (lane >> 2);
+    const unsigned long long to = __shfl_sync(0xffffffffu, address, row);
+    if (to != 0)
+      reinterpret_cast<uint4*>(to)[j] =
+          *reinterpret_cast<const uint4*>(stage + (row * 4 + (j ^ ((row >> 1) & 3))) * 16);
+  }
+  __syncwarp();
+}
+
+// What the epilogue of a tile needs: this row's statistics, the part's blocks of the
+// tile, its place in the batch.
+struct Done {
+  Stats x;
+  int take, blk, nt, left;
+  int row0, kvh, rows;
+  bool narrow;
+};
+
+// Writes out O and LSE of tile i of the part, or what the part has of them, once
+// the tile's last P V has completed. That has a barrier of its own for each O
+// buffer: by now the next tile's blocks may have completed too, which moves O_DONE
+// on, but the tile after that waits for this epilogue to free the buffer.
+template <typename T, int D, bool SOFTCAP>
+__device__ __forceinline__ bool epilogue(const Ctx& c, const Params& p, const Part& part,
+                                         const Done& d, bool ok, int i, int h, uint32_t lanes,
+                                         float* xsum, float* shifts, uint8_t* smem,
+                                         uint8_t* stage, int token) {
+  using L = Layout<D>;
+  const int lane = threadIdx.x & 31;
+  const int quadrant = (threadIdx.x >> 5) & 3;
+  const int r = (quadrant << 5) + lane;
+  const uint32_t tO = lanes + 256 + (i % L::kOBufs) * D + h * (D / 2);
+  const int row = d.narrow ? lane : r;
+  const bool idle = !d.narrow && (r & ~31) >= d.rows;
+  if (ok) ok = wait(c, BAR_O_LAST + i % L::kOBufs, (i / L::kOBufs) & 1);
+  xsum[h * 128 + r] = d.x.l;
+  if (kHasNarrow<D, SOFTCAP> && d.narrow && h == 0) shifts[r] = d.x.m;
+  if (!named_bar_and(kBarBoth, 256, ok)) return false;
+  tc_fence_after();
+  const bool whole = d.blk == 0 && d.take == d.nt;
+  const int head = d.kvh * p.G + row - token * p.G;
+  const long long out_row = static_cast<long long>(d.row0) + token;
+  float* partial = reinterpret_cast<float*>(p.workspace + kSharedBytes) +
+                   (2LL * blockIdx.x + (d.blk == 0 ? 1 : 0)) * slot_floats(D);
+  if (kHasNarrow<D, SOFTCAP> && d.narrow) {
+    // the quadrants' shifts and sums of a row
+    auto join = [&](int at, float& M, float& total) {
+      M = -INFINITY;
+      total = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) M = fmaxf(M, shifts[32 * k + at]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (shifts[32 * k + at] > -INFINITY)
+          total = fmaf(xsum[32 * k + at] + xsum[128 + 32 * k + at],
+                       ex2_approx(shifts[32 * k + at] - M), total);
+    };
+    float M, total;
+    join(lane, M, total);
+    const float f = d.x.m > -INFINITY ? ex2_approx(d.x.m - M) : 0.f;
+    if (quadrant == 0 && h == 0 && lane < d.rows) {
+      if (!whole) {
+        partial[lane] = M;
+        partial[128 + lane] = total;
+      } else if (p.lse != nullptr) {
+        p.lse[out_row * p.H + head] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
+      }
+    }
+    // [quadrant][row][column] fp32 over all of the warps' stages, then the quadrants
+    // added in order
+    float* sum = reinterpret_cast<float*>(smem + L::kStage);
+#pragma unroll
+    for (int c0 = 0; c0 < D / 2; c0 += 32) {
+      uint32_t o[32];
+      tmem_ld32(tO + c0, o);
+      if (lane < d.rows) {
+        float4* to = reinterpret_cast<float4*>(sum + (quadrant * p.narrow + lane) * D +
+                                               h * (D / 2) + c0);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          to[u] = f > 0.f ? make_float4(__uint_as_float(o[4 * u]) * f,
+                                        __uint_as_float(o[4 * u + 1]) * f,
+                                        __uint_as_float(o[4 * u + 2]) * f,
+                                        __uint_as_float(o[4 * u + 3]) * f)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    named_bar_sync(kBarBoth, 256);
+    const int k = static_cast<int>(threadIdx.x) - 128;  // rows * D / 4 <= 256
+    if (k < d.rows * (D / 4)) {
+      const int at = k / (D / 4), col = (k % (D / 4)) * 4;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 v = *reinterpret_cast<const float4*>(sum + (q * p.narrow + at) * D + col);
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+      if (!whole) {
+        *reinterpret_cast<float4*>(partial + 256 + at * D + col) = o;
+      } else {
+        join(at, M, total);
+        const float inv = total > 0.f ? 1.f / total : 0.f;
+        const int tok = at / p.G;
+        T* out = static_cast<T*>(p.o) + (static_cast<long long>(d.row0) + tok) * p.o_token +
+                 (d.kvh * p.G + at - tok * p.G) * p.o_head + col;
+        *reinterpret_cast<uint2*>(out) =
+            make_uint2(pack_pair<T>(o.x * inv, o.y * inv), pack_pair<T>(o.z * inv, o.w * inv));
+      }
+    }
+  } else if (!idle) {
+    const bool mine = r < d.rows;
+    const float total = xsum[r] + xsum[128 + r];
+    if (whole) {
+      T* out = static_cast<T*>(p.o) + out_row * p.o_token + head * p.o_head + h * (D / 2);
+      const float inv = total > 0.f ? 1.f / total : 0.f;
+      const uint64_t inv2 = f2_make(inv, inv);
+#pragma unroll
+      for (int c0 = 0; c0 < D / 2; c0 += 32) {
+        uint32_t raw[32], packed[16];
+        tmem_ld32(tO + c0, raw);
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const uint64_t v = f2_mul(f2_make(raw[2 * u], raw[2 * u + 1]), inv2);
+          // a row that sees nothing: its P V was 0 times what V held
+          packed[u] = total > 0.f ? pack_pair<T>(f2_lo(v), f2_hi(v)) : 0u;
+        }
+        store_rows(stage, packed, mine ? reinterpret_cast<unsigned long long>(out + c0) : 0ull);
+      }
+      if (mine && h == 0 && p.lse != nullptr)
+        p.lse[out_row * p.H + head] = total > 0.f ? (d.x.m + __log2f(total)) * kLn2 : -INFINITY;
+    } else {
+      if (mine && h == 0) {
+        partial[r] = d.x.m;
+        partial[128 + r] = total;
+      }
+      float* to = partial + 256 + r * D + h * (D / 2);
+#pragma unroll
+      for (int c0 = 0; c0 < D / 2; c0 += 16) {
+        uint32_t raw[16];
+        tmem_ld16(tO + c0, raw);
+        store_rows(stage, raw, mine ? reinterpret_cast<unsigned long long>(to + c0) : 0ull);
+      }
+    }
+  }
+  if (d.blk == 0 && d.take < d.nt && threadIdx.x == 128) {
+    // the tile goes on in the parts behind: the last of them holds its last unit
+    const long long end = part.first + part.count - d.left;
+    Shared s;
+    s.parts = static_cast<int>((end - 1) / part.share) - static_cast<int>(blockIdx.x) + 1;
+    s.row0 = d.row0;
+    s.kvh = d.kvh;
+    s.rows = d.rows;
+    reinterpret_cast<Shared*>(p.workspace)[blockIdx.x] = s;
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar_addr(c, BAR_O_FREE + i % L::kOBufs));
+  return true;
+}
+
 // Thread r of each warpgroup owns row r; the warpgroups exchange the half-row
 // maxima through shared memory once per block, so that both take the same shift.
-// Warps without a row of the tile only keep the barriers' count.
+// Warps without a row of the tile only keep the barriers' count. In a narrow tile
+// lane r of every quadrant owns row r and has sums of its own over the quadrant's
+// keys, joined at the end.
 template <typename T, int D, bool SOFTCAP>
 __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, uint8_t* smem,
                              uint32_t tmem) {
@@ -720,24 +1000,28 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int h = (warp - 4) >> 2;  // which half of the keys (and of O's columns)
-  const int r = ((warp & 3) << 5) + lane;
-  const int token = r / p.G;
+  const int quadrant = warp & 3;
+  const int r = (quadrant << 5) + lane;
   const uint32_t lane_base = static_cast<uint32_t>(r & ~31) << 16;
   float* xmax = reinterpret_cast<float*>(smem + L::kXchg);  // [block parity][half][row]
   float* xsum = xmax + 4 * 128;                              // [half][row]
+  float* shifts = reinterpret_cast<float*>(smem + L::kShifts);
+  uint8_t* stage = smem + L::kStage + (warp - 4) * 2048;
+  const int wide_token = r / p.G, narrow_token = lane / p.G;
   const float c_log2 = p.scale * kLog2e;
   const float cap_in = SOFTCAP ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
   const float cap_out = SOFTCAP ? p.softcap * kLog2e : 0.f;
   bool ok = true;
   int g = 0;  // blocks of all tiles before
   int i = 0;
-  Walk w;
-  for (w.begin(p, part); ok && w.left > 0; w.next(p), ++i) {
+  Walk w(p, part);
+  for (; ok && w.step(p); ++i) {
     const int nt = w.take;
-    const int ob = i % L::kOBufs;
-    const uint32_t tO = tmem + lane_base + 256 + ob * D + h * (D / 2);
     const int rows = w.t.count * p.G;
-    const bool idle = (r & ~31) >= rows;  // the warp has no row
+    const bool narrow = is_narrow<D, SOFTCAP>(p, w.t);
+    const int token = narrow ? narrow_token : wide_token;
+    const bool idle = !narrow && (r & ~31) >= rows;  // the warp has no row
+    const uint32_t tO = tmem + lane_base + 256 + (i % L::kOBufs) * D + h * (D / 2);
     // the keys that this row sees, and those that every row of the tile sees
     const int pos = w.t.pos0 + token;
     const int hi = p.causal ? min(pos, w.s.length - 1) : w.s.length - 1;
@@ -745,175 +1029,173 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
     const int all_hi = p.causal ? min(w.t.pos0, w.s.length - 1) : w.s.length - 1;
     const int all_lo = p.left < 0 ? 0 : w.t.pos0 + w.t.count - 1 - p.left;
     float m_used = -INFINITY, l = 0.f;
-    for (int t = 0; t < nt; ++t) {
-      const int gb = g + t;
-      const int n0 = w.t.block(w.blk + t) * kBn;
-      const int key0 = n0 + 64 * h;
-      const uint32_t tS = tmem + lane_base + (gb & 1) * 128;
-      const bool masked =
-          n0 + kBn - 1 > all_hi || (n0 < all_lo && n0 + kBn > p.sinks);
-      const bool got = wait(c, BAR_S_FULL + (gb & 1), (gb >> 1) & 1);
-      uint32_t raw[64];
-      uint2 visible = make_uint2(~0u, ~0u);
-      float hmax = -INFINITY;
-      if (got && !idle) {
-        tc_fence_after();
-        tmem_ld32x2(tS + 64 * h, tS + 64 * h + 32, raw);
-        float m0 = -INFINITY, m1 = -INFINITY;
-        if (masked) {
-          visible = visible_bits(key0, lo, hi, p.sinks);
-          // hidden scores become -inf; with a softcap 0, which keeps them out of
-          // the choice of tanh's form (chunk_p hides the logits)
+    if (kHasNarrow<D, SOFTCAP> && narrow) {
+      Stats x{-INFINITY, 0.f};
+      for (int t = 0; t < nt; ++t) {
+        const int gb = g + t;
+        const int n0 = w.t.block(w.blk + t) * kBn;
+        const uint32_t tS = tmem + lane_base + (gb & 1) * 128;
+        const bool masked = n0 + kBn - 1 > all_hi || (n0 < all_lo && n0 + kBn > p.sinks);
+        const bool got = wait(c, BAR_S_DONE + (gb & 1), (gb >> 1) & 1);
+        float* slot = xmax + (gb & 1) * 256;
+        // keys 32 quadrant + 16 h .. + 15 of the block
+        const int key0 = n0 + 32 * quadrant + 16 * h;
+        uint32_t raw[16];
+        uint32_t visible = 0xffffu;
+        float hmax = -INFINITY;
+        if (got) {
+          tc_fence_after();
+          tmem_ld16(tS + 32 * quadrant + 16 * h, raw);
+          if (masked) visible = visible_bits(key0, lo, hi, p.sinks).x;
+          if (lane >= rows) visible = 0;  // these lanes' scores are of no row
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            const bool seen = bit_of(visible, e);
-            if (SOFTCAP) {
-              if (seen) m0 = fmaxf(m0, __uint_as_float(raw[e]));
-              if (!seen) raw[e] = 0u;
-            } else if (!seen) {
-              raw[e] = 0xff800000u;
-            }
+          for (int e = 0; e < 16; ++e) {
+            const bool seen = (visible >> e) & 1u;
+            if (seen) hmax = fmaxf(hmax, __uint_as_float(raw[e]));
           }
         }
-        if (!SOFTCAP || !masked) {
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            m0 = fmaxf(m0, __uint_as_float(raw[e]));
-            m1 = fmaxf(m1, __uint_as_float(raw[e + 1]));
-          }
-        }
-        hmax = fmaxf(m0, m1);
-      }
-      float* slot = xmax + (gb & 1) * 256;
-      slot[h * 128 + r] = hmax;
-      ok = named_bar_and(kBarBoth, 256, ok && got);
-      if (!ok) break;
-      if (!idle) {
+        slot[h * 128 + r] = hmax;
+        ok = named_bar_and(kBarBoth, 256, ok && got);
+        if (!ok) break;
         const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
-        float m_tile = -INFINITY;  // row maximum of the logits (log2 units) over this block
-        if (smax > -INFINITY) {
-          if (SOFTCAP) {
-            const float ex = ex2_approx(smax * cap_in);
-            m_tile = (1.f - 2.f * rcp_approx(ex + 1.f)) * cap_out;
-          } else {
-            m_tile = smax * c_log2;
-          }
+        const float shift =
+            take_max<D, SOFTCAP>(c, x, smax, c_log2, cap_in, cap_out, t > 0, gb, tO, ok);
+        // P of the warp's 16 keys; 0 for the keys of the other quadrants: of the
+        // 64 pair columns (0 .. 31 and 64 .. 95), in groups of 8 (16 keys),
+        // warpgroup h writes groups h, 2 + h, 4 + h, 6 + h, its keys' one among them
+        uint32_t pairs[8], zeros[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          // tanh of what a hidden score holds is not used
+          const uint64_t th2 = softcap::tanh_mufu2(
+              f2_mul(f2_make(raw[2 * u], raw[2 * u + 1]), f2_make(cap_in, cap_in)));
+          const float y0 =
+              (visible >> (2 * u)) & 1u ? fmaf(f2_lo(th2), cap_out, -shift) : -INFINITY;
+          const float y1 =
+              (visible >> (2 * u + 1)) & 1u ? fmaf(f2_hi(th2), cap_out, -shift) : -INFINITY;
+          const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+          x.l += p0 + p1;
+          pairs[u] = pack_pair<T>(p0, p1);
+          zeros[u] = 0u;
         }
-        const bool need = m_tile > m_used + kRescale;
-        if (__any_sync(0xffffffffu, need)) {
-          const float m_new = need ? m_tile : m_used;
-          const float f = need ? ex2_approx(m_used - m_new) : 1.f;  // 0 while m_used = -inf
-          // this half of the O row, once P(t - 1) V has completed; a wait that
-          // gives up is voted on at the next barrier
-          if (__any_sync(0xffffffffu, need && m_used > -INFINITY) && t > 0) {
-            if (!wait_warp(c, BAR_O_DONE, (gb - 1) & 1)) ok = false;
-            if (ok) {
-              tc_fence_after();
-              const uint64_t f2 = f2_make(f, f);
 #pragma unroll
-              for (int c32 = 0; c32 < D / 64; ++c32) {
-                uint32_t o[32];
-                tmem_ld32(tO + c32 * 32, o);
-                uint32_t a[16], b[16];
+        for (int j = 0; j < 4; ++j) {
+          const int group = 2 * j + h;
+          const uint32_t dst = tS + 8 * group + (group >= 4 ? 32 : 0);
+          if (j == quadrant)
+            tmem_st8(dst, pairs);
+          else
+            tmem_st8(dst, zeros);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_addr(c, BAR_P_FULL + (gb & 1)));  // one arrival per warp
+      }
+      m_used = x.m;
+      l = x.l;
+    } else {
+      for (int t = 0; t < nt; ++t) {
+        const int gb = g + t;
+        const int n0 = w.t.block(w.blk + t) * kBn;
+        const int key0 = n0 + 64 * h;
+        const uint32_t tS = tmem + lane_base + (gb & 1) * 128;
+        const bool masked =
+            n0 + kBn - 1 > all_hi || (n0 < all_lo && n0 + kBn > p.sinks);
+        const bool got = wait(c, BAR_S_DONE + (gb & 1), (gb >> 1) & 1);
+        uint32_t raw[64];
+        uint2 visible = make_uint2(~0u, ~0u);
+        float hmax = -INFINITY;
+        if (got && !idle) {
+          tc_fence_after();
+          tmem_ld32x2(tS + 64 * h, tS + 64 * h + 32, raw);
+          float m0 = -INFINITY, m1 = -INFINITY;
+          if (masked) {
+            visible = visible_bits(key0, lo, hi, p.sinks);
+            // hidden scores become -inf; with a softcap 0, which keeps them out of
+            // the choice of tanh's form (chunk_p hides the logits)
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                  const uint64_t v = f2_mul(f2_make(o[2 * u], o[2 * u + 1]), f2);
-                  const uint64_t x = f2_mul(f2_make(o[16 + 2 * u], o[17 + 2 * u]), f2);
-                  a[2 * u] = static_cast<uint32_t>(v);
-                  a[2 * u + 1] = static_cast<uint32_t>(v >> 32);
-                  b[2 * u] = static_cast<uint32_t>(x);
-                  b[2 * u + 1] = static_cast<uint32_t>(x >> 32);
-                }
-                tmem_st16(tO + c32 * 32, a);
-                tmem_st16(tO + c32 * 32 + 16, b);
+            for (int e = 0; e < 64; ++e) {
+              const bool seen = bit_of(visible, e);
+              if (SOFTCAP) {
+                if (seen) m0 = fmaxf(m0, __uint_as_float(raw[e]));
+                if (!seen) raw[e] = 0u;
+              } else if (!seen) {
+                raw[e] = 0xff800000u;
               }
             }
           }
-          l *= f;
-          m_used = m_new;
-        }
-        const float shift = m_used > -INFINITY ? m_used : 0.f;
-        l += chunk_p<T, SOFTCAP>(p, raw, tS + 64 * h, masked, visible, c_log2, cap_in, cap_out,
-                                 shift);
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_addr(c, BAR_P_FULL + (gb & 1)));  // one arrival per warp
-    }
-    // ---- epilogue, once the tile's last P V has completed (on a barrier of its
-    // own, one phase per tile: both of the last phases of O_DONE may be behind)
-    if (ok) ok = wait(c, BAR_O_LAST, i & 1);
-    xsum[h * 128 + r] = l;
-    if (!named_bar_and(kBarBoth, 256, ok)) break;
-    tc_fence_after();
-    const float lt = xsum[r] + xsum[128 + r];
-    const bool whole = w.blk == 0 && nt == w.t.nt;
-    if (!idle) {
-      const bool mine = r < rows;
-      if (whole) {
-        const int head = w.kvh * p.G + r - token * p.G;
-        const long long row = w.s.row0 + w.tile * p.tokens + token;
-        T* out = static_cast<T*>(p.o) + row * p.o_token + head * p.o_head + h * (D / 2);
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
-        const uint64_t inv2 = f2_make(inv, inv);
+          if (!SOFTCAP || !masked) {
 #pragma unroll
-        for (int c16 = 0; c16 < D / 32; ++c16) {
-          uint32_t raw[16];
-          tmem_ld16(tO + c16 * 16, raw);
-          uint32_t packed[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const uint64_t v = f2_mul(f2_make(raw[2 * u], raw[2 * u + 1]), inv2);
-            packed[u] = pack_pair<T>(f2_lo(v), f2_hi(v));
+            for (int e = 0; e < 64; e += 2) {
+              m0 = fmaxf(m0, __uint_as_float(raw[e]));
+              m1 = fmaxf(m1, __uint_as_float(raw[e + 1]));
+            }
           }
-          // a row that sees nothing: its P V was 0 times what V held
-          if (!(lt > 0.f)) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u) packed[u] = 0u;
-          }
-          if (mine) {
-            uint4* to = reinterpret_cast<uint4*>(out + c16 * 16);
-            to[0] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-            to[1] = make_uint4(packed[4], packed[5], packed[6], packed[7]);
-          }
+          hmax = fmaxf(m0, m1);
         }
-        if (mine && h == 0 && p.lse != nullptr)
-          p.lse[row * p.H + head] = lt > 0.f ? (m_used + __log2f(lt)) * kLn2 : -INFINITY;
-      } else {
-        float* to = reinterpret_cast<float*>(p.workspace + kSharedBytes) +
-                    (2LL * blockIdx.x + (w.blk == 0 ? 1 : 0)) * slot_floats(D);
-        if (mine && h == 0) {
-          to[r] = m_used;
-          to[128 + r] = lt;
-        }
-        to += 256 + r * D + h * (D / 2);
-#pragma unroll
-        for (int c16 = 0; c16 < D / 32; ++c16) {
-          uint32_t raw[16];
-          tmem_ld16(tO + c16 * 16, raw);
-          if (mine) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              reinterpret_cast<uint4*>(to + c16 * 16)[u] =
-                  make_uint4(raw[4 * u], raw[4 * u + 1], raw[4 * u + 2], raw[4 * u + 3]);
+        float* slot = xmax + (gb & 1) * 256;
+        slot[h * 128 + r] = hmax;
+        ok = named_bar_and(kBarBoth, 256, ok && got);
+        if (!ok) break;
+        if (!idle) {
+          const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
+          float m_tile = -INFINITY;  // row maximum of the logits (log2 units) over this block
+          if (smax > -INFINITY) {
+            if (SOFTCAP) {
+              const float ex = ex2_approx(smax * cap_in);
+              m_tile = (1.f - 2.f * rcp_approx(ex + 1.f)) * cap_out;
+            } else {
+              m_tile = smax * c_log2;
+            }
           }
+          const bool need = m_tile > m_used + kRescale;
+          if (__any_sync(0xffffffffu, need)) {
+            const float m_new = need ? m_tile : m_used;
+            const float f = need ? ex2_approx(m_used - m_new) : 1.f;  // 0 while m_used = -inf
+            // this half of the O row, once P(t - 1) V has completed; a wait that
+            // gives up is voted on at the next barrier
+            if (__any_sync(0xffffffffu, need && m_used > -INFINITY) && t > 0) {
+              if (!wait_warp(c, BAR_O_DONE + ((gb - 1) & 1), ((gb - 1) >> 1) & 1)) ok = false;
+              if (ok) {
+                tc_fence_after();
+                const uint64_t f2 = f2_make(f, f);
+#pragma unroll
+                for (int c32 = 0; c32 < D / 64; ++c32) {
+                  uint32_t o[32];
+                  tmem_ld32(tO + c32 * 32, o);
+                  uint32_t a[16], b[16];
+#pragma unroll
+                  for (int u = 0; u < 8; ++u) {
+                    const uint64_t v = f2_mul(f2_make(o[2 * u], o[2 * u + 1]), f2);
+                    const uint64_t x = f2_mul(f2_make(o[16 + 2 * u], o[17 + 2 * u]), f2);
+                    a[2 * u] = static_cast<uint32_t>(v);
+                    a[2 * u + 1] = static_cast<uint32_t>(v >> 32);
+                    b[2 * u] = static_cast<uint32_t>(x);
+                    b[2 * u + 1] = static_cast<uint32_t>(x >> 32);
+                  }
+                  tmem_st16(tO + c32 * 32, a);
+                  tmem_st16(tO + c32 * 32 + 16, b);
+                }
+              }
+            }
+            l *= f;
+            m_used = m_new;
+          }
+          const float shift = m_used > -INFINITY ? m_used : 0.f;
+          l += chunk_p<T, SOFTCAP>(p, raw, tS + 64 * h, masked, visible, c_log2, cap_in, cap_out,
+                                   shift);
+          tmem_wait_st();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_addr(c, BAR_P_FULL + (gb & 1)));  // one arrival per warp
       }
     }
-    if (w.blk == 0 && nt < w.t.nt && threadIdx.x == 128) {
-      // the tile goes on in the parts behind: the last of them holds its last block
-      const long long end = part.first + part.count + (w.t.nt - nt);
-      Shared s;
-      s.parts = static_cast<int>((end - 1) / part.share) - static_cast<int>(blockIdx.x) + 1;
-      s.row0 = w.s.row0 + w.tile * p.tokens;
-      s.kvh = w.kvh;
-      s.rows = rows;
-      reinterpret_cast<Shared*>(p.workspace)[blockIdx.x] = s;
-    }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_addr(c, BAR_O_FREE + ob));
+    const Done done{{m_used, l}, nt, w.blk, w.t.nt, w.left, w.s.row0 + w.tile * p.tokens,
+                    w.kvh, rows, narrow};
+    ok = epilogue<T, D, SOFTCAP>(c, p, part, done, ok, i, h, tmem + lane_base, xsum, shifts, smem, stage,
+                        token);
     g += nt;
   }
 }
@@ -922,6 +1204,7 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
 template <typename T, int D, bool SOFTCAP>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ CUtensorMap tm_qn,
                      const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using L = Layout<D>;
@@ -947,13 +1230,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (warp == 2 && (threadIdx.x & 31) == 0) {
-    prefetch_tmap(&tm_q);
+    prefetch_tmap(p.narrow > 0 ? &tm_qn : &tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
   // rows that no tile's copy fills hold zeros, not what shared memory held before
   const int unused = kBm - p.tokens * p.G;
-  for (int i = threadIdx.x; i < L::kStages * (D / 64) * unused * 8; i += kThreads) {
+  for (int i = threadIdx.x; i < L::kQStages * (D / 64) * unused * 8; i += kThreads) {
     const int row = kBm - 1 - (i >> 3) % unused, box = (i >> 3) / unused;
     *reinterpret_cast<uint4*>(smem + L::kQ + box * 16384 + row * 128 + (i & 7) * 16) =
         make_uint4(0u, 0u, 0u, 0u);
@@ -968,15 +1251,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlot);
   if (*c.abort == 0) {
     if (warp < 4) {
-      setmaxnreg_dec<kRegsCtl>();
+      setmaxnreg_dec<kRegsCtl<D>>();
       if (warp == 0)
-        loader_role<D, false>(c, p, *part, smem, sbase, &tm_q, &tm_k);
-      else if (warp == 1)
-        mma_role<T, D>(c, p, *part, sbase, tmem);
-      else if (warp == 2)
-        loader_role<D, true>(c, p, *part, smem, sbase, &tm_q, &tm_v);
+        loader_role<D, SOFTCAP, false>(c, p, *part, sbase, &tm_q, &tm_qn, &tm_k);
+      if (warp == 1) {
+        if (elect_one_sync()) issue_mmas<T, D>(c, p, *part, sbase, tmem);
+        __syncwarp();
+      }
+      if (warp == 2)
+        loader_role<D, SOFTCAP, true>(c, p, *part, sbase, &tm_q, &tm_qn, &tm_v);
+      if (warp == 3) zero_role<D>(c, p, *part, smem);
     } else {
-      setmaxnreg_inc<kRegsSoftmax>();
+      setmaxnreg_inc<kRegsSoftmax<D>>();
       softmax_role<T, D, SOFTCAP>(c, p, *part, smem, tmem);
     }
   }
@@ -989,66 +1275,92 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the tile that begins in part blockIdx.x and goes on behind
-// it: M = max m_i, L = sum l_i 2^(m_i - M), O = sum O_i 2^(m_i - M) / L, in the
-// order of the parts. One warp a row, D / 32 columns a lane.
-constexpr int kJoinWarps = 8, kJoinSplit = 128 / kJoinWarps;
+// it: M = max m_i, L = sum l_i 2^(m_i - M), O = sum O_i 2^(m_i - M) / L. One warp a
+// row, D / 32 columns a lane, parts in order; where a tile has more than kJoinFew
+// parts the warps of a block share a row, warp k takes parts k, k + 8, ... and the
+// warps' sums are added in order (one token over 131072 keys, one key/value head:
+// 147 parts, TODO us with a warp a row).
+constexpr int kJoinWarps = 8, kJoinSplit = 128 / kJoinWarps, kJoinFew = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Params p) {
   grid_dependency_wait();
   const Shared s = reinterpret_cast<const Shared*>(p.workspace)[blockIdx.x];
-  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  if (s.parts == 0 || r >= s.rows) return;
+  if (s.parts == 0) return;
+  const bool few = s.parts <= kJoinFew;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = few ? 0 : warp, step = few ? 1 : kJoinWarps;
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+  __shared__ float2 sums[kJoinWarps][32][E / 2];
+  __shared__ float totals[kJoinWarps];
   const float* slots = reinterpret_cast<const float*>(p.workspace + kSharedBytes) +
                        2LL * blockIdx.x * slot_floats(D);
   // part i of the tile: slot 1 of the first CTA, slot 0 of the ones behind
   auto slot = [&](int i) { return slots + (i == 0 ? 1 : 2 * i) * slot_floats(D); };
   constexpr int kAhead = 4;  // parts whose O is on its way before the weights are known
-  float2 v[kAhead][E / 2];
-  auto load = [&](int i, float2 (&to)[E / 2]) {
-    const float* from = slot(i) + 256 + r * D + lane * E;
+  // every warp of a block that shares its rows goes through the same ones
+  for (int r = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y; r < s.rows;
+       r += few ? 128 : kJoinSplit) {
+    float2 v[kAhead][E / 2];
+    auto load = [&](int i, float2 (&to)[E / 2]) {
+      const float* from = slot(i) + 256 + r * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) to[e] = reinterpret_cast<const float2*>(from)[e];
-  };
+      for (int e = 0; e < E / 2; ++e) to[e] = reinterpret_cast<const float2*>(from)[e];
+    };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (i < s.parts) load(i, v[i]);
-  float M = -INFINITY;
-  for (int i = lane; i < s.parts; i += 32) M = fmaxf(M, slot(i)[r]);
+    for (int u = 0; u < kAhead; ++u)
+      if (first + u * step < s.parts) load(first + u * step, v[u]);
+    float M = -INFINITY;
+    for (int i = lane; i < s.parts; i += 32) M = fmaxf(M, slot(i)[r]);
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float shift = M > -INFINITY ? M : 0.f;
-  float2 o[E / 2];
-  float total = 0.f;
+    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const float shift = M > -INFINITY ? M : 0.f;
+    float2 o[E / 2];
+    float total = 0.f;
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) o[e] = make_float2(0.f, 0.f);
-  for (int i0 = 0; i0 < s.parts; i0 += kAhead) {
+    for (int e = 0; e < E / 2; ++e) o[e] = make_float2(0.f, 0.f);
+    for (int i0 = first; i0 < s.parts; i0 += kAhead * step) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u;
-      if (i >= s.parts) break;
-      const float f = ex2_approx(slot(i)[r] - shift);
-      if (f > 0.f) {  // a part that saw nothing holds no numbers
-        total = fmaf(slot(i)[128 + r], f, total);
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * step;
+        if (i >= s.parts) break;
+        const float f = ex2_approx(slot(i)[r] - shift);
+        if (f > 0.f) {  // a part that saw nothing holds no numbers
+          total = fmaf(slot(i)[128 + r], f, total);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            o[e].x = fmaf(v[u][e].x, f, o[e].x);
+            o[e].y = fmaf(v[u][e].y, f, o[e].y);
+          }
+        }
+        if (i + kAhead * step < s.parts) load(i + kAhead * step, v[u]);
+      }
+    }
+    if (!few) {
+      __syncthreads();  // the row before has been read
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) sums[warp][lane][e] = o[e];
+      if (lane == 0) totals[warp] = total;
+      __syncthreads();
+      if (warp != 0) continue;
+      for (int k = 1; k < kJoinWarps; ++k) {
+        total += totals[k];
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
-          o[e].x = fmaf(v[u][e].x, f, o[e].x);
-          o[e].y = fmaf(v[u][e].y, f, o[e].y);
+          o[e].x += sums[k][lane][e].x;
+          o[e].y += sums[k][lane][e].y;
         }
       }
-      if (i + kAhead < s.parts) load(i + kAhead, v[u]);
     }
-  }
-  const float inv = total > 0.f ? 1.f / total : 0.f;
-  const int token = r / p.G, head = s.kvh * p.G + r - token * p.G;
-  const long long row = s.row0 + token;
-  T* out = static_cast<T*>(p.o) + row * p.o_token + head * p.o_head + lane * E;
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+    const int token = r / p.G, head = s.kvh * p.G + r - token * p.G;
+    const long long row = static_cast<long long>(s.row0) + token;
+    T* out = static_cast<T*>(p.o) + row * p.o_token + head * p.o_head + lane * E;
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e)
-    reinterpret_cast<uint32_t*>(out)[e] = pack_pair<T>(o[e].x * inv, o[e].y * inv);
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[row * p.H + head] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
+    for (int e = 0; e < E / 2; ++e)
+      reinterpret_cast<uint32_t*>(out)[e] = pack_pair<T>(o[e].x * inv, o[e].y * inv);
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[row * p.H + head] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -1071,7 +1383,8 @@ bool encode_4d(CUtensorMap* map, const void* base, int d, const long long (&exte
       map, std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
       4, const_cast<void*>(base), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_SWIZZLE_128B,
+      d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -1082,13 +1395,14 @@ struct Tensors {
 };
 
 template <typename T, int D, bool SOFTCAP>
-int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p,
-           int ctas, bool join, cudaStream_t stream) {
+int launch(const CUtensorMap (&maps)[4], const Params& p, int ctas, bool join,
+           cudaStream_t stream) {
   auto kern = cache_fwd_kernel<T, D, SOFTCAP>;
   static std::atomic<bool> configured[kMaxTrackedDevices];
   if (!set_smem_limit_once(kern, Layout<D>::kBytes, configured)) return ATTN_ERR_LAUNCH;
   const int rc = launch_overlapped(kern, dim3(static_cast<unsigned>(ctas)), kThreads,
-                                   Layout<D>::kBytes, 0, stream, tq, tk, tv, p);
+                                   Layout<D>::kBytes, 0, stream, maps[0], maps[1], maps[2],
+                                   maps[3], p);
   if (rc != ATTN_OK || !join) return rc;
   return launch_overlapped(cache_join_kernel<T, D>,
                            dim3(static_cast<unsigned>(ctas), kJoinSplit), 32 * kJoinWarps, 0, 0,
@@ -1099,16 +1413,18 @@ template <typename T>
 int run(const Tensors& x, const Params& given, int d, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_LAUNCH;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap maps[4];  // Q, Q of narrow tiles, K, V
   const Batch& c = given.batch;
   const long long q_extent[3] = {given.G, given.H_kv, c.T};
   const long long q_stride[3] = {x.q_in[1], x.q_in[1] * given.G, x.q_in[0]};
   const long long extent[3] = {given.H_kv, c.page_size, c.n_pages};
   const long long k_stride[3] = {x.k_in[2], x.k_in[1], x.k_in[0]};
   const long long v_stride[3] = {x.v_in[2], x.v_in[1], x.v_in[0]};
-  if (!encode_4d<T>(&tq, x.q, d, q_extent, q_stride, {given.G, 1, given.tokens}) ||
-      !encode_4d<T>(&tk, x.k, d, extent, k_stride, {1, given.box, 1}) ||
-      !encode_4d<T>(&tv, x.v, d, extent, v_stride, {1, given.box, 1}))
+  const int narrow_tokens = given.narrow > 0 ? given.narrow / given.G : 1;
+  if (!encode_4d<T>(&maps[0], x.q, d, q_extent, q_stride, {given.G, 1, given.tokens}) ||
+      !encode_4d<T>(&maps[1], x.q, d, q_extent, q_stride, {given.G, 1, narrow_tokens}) ||
+      !encode_4d<T>(&maps[2], x.k, d, extent, k_stride, {1, given.box, 1}) ||
+      !encode_4d<T>(&maps[3], x.v, d, extent, v_stride, {1, given.box, 1}))
     return ATTN_ERR_LAUNCH;
   // as many parts as there can be blocks, one an SM at most
   const long long tiles = (c.T / given.tokens + static_cast<long long>(c.B)) * given.H_kv;
@@ -1127,13 +1443,13 @@ int run(const Tensors& x, const Params& given, int d, cudaStream_t stream) {
   const bool join = !p.whole;
   const bool cap = p.softcap > 0.f;
   if (d == 64)
-    return cap ? launch<T, 64, true>(tq, tk, tv, p, ctas, join, stream)
-               : launch<T, 64, false>(tq, tk, tv, p, ctas, join, stream);
+    return cap ? launch<T, 64, true>(maps, p, ctas, join, stream)
+               : launch<T, 64, false>(maps, p, ctas, join, stream);
   if (d == 128)
-    return cap ? launch<T, 128, true>(tq, tk, tv, p, ctas, join, stream)
-               : launch<T, 128, false>(tq, tk, tv, p, ctas, join, stream);
-  return cap ? launch<T, 256, true>(tq, tk, tv, p, ctas, join, stream)
-             : launch<T, 256, false>(tq, tk, tv, p, ctas, join, stream);
+    return cap ? launch<T, 128, true>(maps, p, ctas, join, stream)
+               : launch<T, 128, false>(maps, p, ctas, join, stream);
+  return cap ? launch<T, 256, true>(maps, p, ctas, join, stream)
+             : launch<T, 256, false>(maps, p, ctas, join, stream);
 }
 
 // Sizes that both entry points check.
@@ -1222,6 +1538,11 @@ extern "C" int attn_cache_fwd(const void* q, const void* k_cache, const void* v_
   p.cap = cap < (1LL << 30) ? static_cast<int>(cap) : 1 << 30;
   p.scale = scale;
   p.softcap = softcap > 0.f ? softcap : 0.f;
+  p.narrow = (!(softcap > 0.f) ? 0
+              : d == 64        ? cachefwd::Layout<64>::kNarrow
+              : d == 128       ? cachefwd::Layout<128>::kNarrow
+                               : 0) /
+             p.G * p.G;  // whole tokens
   p.causal = causal != 0;
   p.left = window_left > (1 << 30) ? 1 << 30 : window_left;
   p.sinks = sinks;
