@@ -1,0 +1,103 @@
+// attn_bwd_sinks at d = 64 and 128: the kernels of attn_bwd_kernel.cuh with sinks, and
+// how their units are shared out. A source file of its own: the forms without sinks
+// keep their code (sinks as a run-time matter cost the dropout form 2 % in spills).
+#include <algorithm>
+
+#include "attn_bwd_kernel.cuh"
+
+namespace attn {
+namespace bwd {
+
+template <int D, bool SOFTCAP>
+int launch_units(const Maps& m, const SinkParams& p, int grid, cudaStream_t stream) {
+  auto kern = attn_bwd_kernel<D, false, SOFTCAP, false, false, true, false>;
+  static std::atomic<bool> configured[kMaxTrackedDevices];
+  if (!set_smem_limit_once(kern, Layout<D>::kBytes, configured)) return ATTN_ERR_LAUNCH;
+  kern<<<grid, kThreads, Layout<D>::kBytes, stream>>>(m.q, m.k, m.v, m.dO, m.dq, m.dk, m.dv, p);
+  return launch_status();
+}
+
+// The units 0 .. p.n_units - 1, each by a cluster of p.split CTAs.
+template <int D, bool SOFTCAP>
+int launch_split(const Maps& m, const SinkParams& p, cudaStream_t stream) {
+  auto kern = attn_bwd_kernel<D, false, SOFTCAP, false, false, true, true>;
+  static std::atomic<bool> configured[kMaxTrackedDevices];
+  if (!set_smem_limit_once(kern, Layout<D>::kBytes, configured)) return ATTN_ERR_LAUNCH;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(static_cast<unsigned>(p.n_units) * static_cast<unsigned>(p.split));
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = Layout<D>::kBytes;
+  config.stream = stream;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  if (cudaLaunchKernelEx(&config, kern, m.q, m.k, m.v, m.dO, m.dq, m.dk, m.dv, p) != cudaSuccess) {
+    cudaGetLastError();  // reported here, not by a later call
+    return ATTN_ERR_LAUNCH;
+  }
+  return ATTN_OK;
+}
+
+template <int D, bool SOFTCAP>
+int launch_both(const Maps& m, SinkParams p, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return ATTN_ERR_LAUNCH;
+  const int with_sinks = (p.sinks + kBc - 1) / kBc * p.H_kv * p.B;  // units, the first ones
+  // query tiles of a unit of a band, of one with sinks (all tiles but those before
+  // the unit's block), and of all units
+  const long long group = p.H / p.H_kv, most = group * p.m_blocks;
+  const long long band_tiles = std::min<long long>(
+      p.m_blocks, (static_cast<long long>(p.win_left) + p.win_right + kBc - 1) / kBr + 1);
+  const long long all = with_sinks * most + (p.n_units - with_sinks) * group * band_tiles;
+  // A unit with sinks that outlasts what an SM has on average is shared by a
+  // cluster of CTAs, in a launch of its own (1 x 8 heads over 1 x 16384 x 128, window
+  // 1024: the step takes 532 us, not 2361; 1 x 4 x 8192 x 64, window 512: 67, not 149).
+  // The last such unit has the fewest tiles: one for each CTA at least.
+  const long long least = group * (p.m_blocks - (p.sinks - 1) / kBc);
+  while (p.split < 8 && most * sms > all * 5 / 4 * p.split && 2 * p.split <= least) p.split *= 2;
+  if (p.split > 1) {
+    SinkParams shared = p;
+    shared.n_units = with_sinks;
+    const int rc = launch_split<D, SOFTCAP>(m, shared, stream);
+    if (rc != ATTN_OK || with_sinks == p.n_units) return rc;
+    p.first_unit = with_sinks;
+    p.n_units -= with_sinks;
+  }
+  const int grid = p.n_units < sms ? p.n_units : sms;
+  if (p.split == 1) {
+    p.heavy_passes = with_sinks / grid;
+    p.heavy = with_sinks % grid;
+    p.ahead = p.heavy > 0 ? static_cast<int>((p.m_blocks + band_tiles / 2) / band_tiles) : 0;
+  }
+  return launch_units<D, SOFTCAP>(m, p, grid, stream);
+}
+
+int launch_sinks(const Maps& m, const Params& base, int sinks, void* dk, void* dv, int d,
+                 cudaStream_t stream) {
+  SinkParams p{};
+  static_cast<Params&>(p) = base;
+  p.sinks = sinks;
+  p.split = 1;
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  const bool cap = p.softcap > 0.f;
+  if (d == 128)
+    return cap ? launch_both<128, true>(m, p, stream) : launch_both<128, false>(m, p, stream);
+  return cap ? launch_both<64, true>(m, p, stream) : launch_both<64, false>(m, p, stream);
+}
+
+int sinks_status(int* status, bool clear) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  *status = v;
+  const int zero = 0;
+  if (clear && v != 0 && cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess)
+    return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
+}  // namespace bwd
+}  // namespace attn

@@ -128,7 +128,8 @@ inline bool encode_f32_3d(CUtensorMap* map, const void* base, int d, int rows, l
 // Bounds of the visibility mask as the kernels take them: key j is visible to
 // query i iff j <= i + right and (j >= i - left or j < sinks). A negative or
 // wider-than-N side of the window is unbounded (N); the causal mask bounds the
-// right side at 0; without a left bound the first keys need no exception.
+// right side at 0; where the left bound hides nothing (N - 1 or more) the first keys
+// need no exception.
 struct Band {
   int left, right, sinks;
 };
@@ -136,7 +137,7 @@ inline Band band_of(int N, int causal, int window_left, int window_right, int si
   Band b;
   b.left = (window_left < 0 || window_left > N) ? N : window_left;
   b.right = causal ? 0 : ((window_right < 0 || window_right > N) ? N : window_right);
-  b.sinks = b.left >= N ? 0 : (sinks < N ? sinks : N);
+  b.sinks = b.left >= N - 1 ? 0 : (sinks < N ? sinks : N);
   return b;
 }
 
