@@ -46,10 +46,14 @@
 // Every mbarrier wait is bounded; on timeout the kernel records
 // ATTN_ERR_DEVICE_TIMEOUT in its device status word (attn_device_status
 // reads it) and returns.
+#include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "attn_common.cuh"
+#include "grid_ptx.cuh"
 #include "philox.cuh"
 #include "sm103_ptx.cuh"
 
@@ -141,16 +145,32 @@ struct Params {
   int pairs;
   int causal;
   Dropout drop;  // DROP: keep mask of philox.cuh
+  int first;     // the launch's first unit
+};
+
+// What the kernel whose units a cluster's CTAs share needs besides: how many CTAs,
+// and where the sums go.
+struct SplitParams : Params {
+  int split;
+  __nv_bfloat16 *dk, *dv;
 };
 
 struct Work {
   int b, g, n_block, half, G, m_start, per_head, T;
+  int rank, step;  // the CTA's tiles of the unit: rank, rank + step, ... (0, 1: all)
 };
 
 // Units heaviest first for a causal mask: u = 2 (n_block (H_kv B) + b H_kv + g) + half.
+template <bool SPLIT>
 __device__ __forceinline__ Work work_of(const Params& p) {
   Work w;
-  const int u = static_cast<int>(blockIdx.x);
+  w.rank = 0;
+  w.step = 1;
+  if constexpr (SPLIT) {
+    w.step = static_cast<const SplitParams&>(p).split;
+    w.rank = static_cast<int>(blockIdx.x) % w.step;
+  }
+  const int u = static_cast<int>(blockIdx.x) / w.step + p.first;
   w.half = u & 1;
   const int rest = u >> 1;
   const int per_nb = p.H_kv * p.B;
@@ -165,11 +185,13 @@ __device__ __forceinline__ Work work_of(const Params& p) {
       n0 < p.sinks ? p.m_blocks - 1 : min(p.m_blocks - 1, (n0 + kBc - 1 + p.win_left) / kBr);
   w.per_head = m_end - w.m_start + 1;  // >= 1: the band holds the diagonal
   w.T = w.G * w.per_head;
+  if (SPLIT) w.T = (w.T - w.rank + w.step - 1) / w.step;  // split <= T: every CTA has a tile
   return w;
 }
 
 // Tile t: query blocks from the last one down, the G heads of the group inner.
 __device__ __forceinline__ void tile_coord(const Work& w, int t, int& h, int& m_block) {
+  t = t * w.step + w.rank;
   const int mi = t / w.G;
   h = w.g * w.G + (t - mi * w.G);
   m_block = w.m_start + w.per_head - 1 - mi;
@@ -614,9 +636,52 @@ __device__ void mask_role(const Ctx& c, const Params& p, const Work& w, uint8_t*
 // dO buffers and TMA stores.
 constexpr int kBarDrain = 1;  // named barrier of the drain warpgroup
 
-template <bool DET>
-__device__ void drain_role(const Ctx& c, const Params& p, const Work& w, uint32_t sbase,
-                           uint32_t tmem, const CUtensorMap* tm_dq, const CUtensorMap* tm_dk,
+// dV and dK of a unit whose tiles a cluster's CTAs share: each leaves its sums in
+// its own shared memory (fp32 [128 keys][128], over K and V, which no GEMM reads any
+// more), and CTA k adds rows k 128 / split .. of all of them, in the order of the
+// CTAs, through distributed shared memory. 16-byte piece c of row r sits at piece
+// c ^ (r mod 32).
+constexpr int kPieces = kDh / 4;
+constexpr uint32_t kSums = 128 * kDh * 4;
+static_assert(2 * kSums <= Layout::kQ, "dV and dK over K and V");
+__device__ __forceinline__ void leave_sums(uint8_t* smem, uint32_t from, int r) {
+#pragma unroll
+  for (int c32 = 0; c32 < 8; ++c32) {  // dV's 128 columns, then dK's
+    uint32_t v[32];
+    tmem_ld32(from + c32 * 32, v);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      *reinterpret_cast<uint4*>(smem + (c32 >> 2) * kSums +
+                                (r * kPieces + (((c32 & 3) * 8 + u) ^ (r & 31))) * 16) =
+          make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+  }
+}
+__device__ __forceinline__ void join_sums(const SplitParams& p, const Work& w, uint32_t sbase) {
+  const int rows = 128 / p.split, row0 = w.n_block * kBc;
+  const long long head = static_cast<long long>(w.b * p.H_kv + w.g) * p.N;
+  for (int i = threadIdx.x; i < 2 * rows * kPieces; i += kThreads) {
+    const int m = i / (rows * kPieces), at = i - m * rows * kPieces;
+    const int row = w.rank * rows + at / kPieces, piece = at % kPieces;
+    const uint32_t addr = sbase + m * kSums + (row * kPieces + (piece ^ (row & 31))) * 16;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < p.split; ++k) {
+      const float4 v = ld_cluster_v4(addr, k);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    if (row0 + row >= p.N) continue;
+    const float mul = m == 0 ? 1.f : p.scale;
+    *reinterpret_cast<uint2*>((m == 0 ? p.dv : p.dk) + (head + row0 + row) * kD + kDh * w.half +
+                              piece * 4) =
+        make_uint2(pack_bf16x2(sum.x * mul, sum.y * mul), pack_bf16x2(sum.z * mul, sum.w * mul));
+  }
+}
+
+template <bool DET, bool SPLIT>
+__device__ void drain_role(const Ctx& c, const Params& p, const Work& w, uint8_t* smem,
+                           uint32_t sbase, uint32_t tmem, const CUtensorMap* tm_dq, const CUtensorMap* tm_dk,
                            const CUtensorMap* tm_dv) {
   using L = Layout;
   const int warp = threadIdx.x >> 5;
@@ -665,7 +730,12 @@ __device__ void drain_role(const Ctx& c, const Params& p, const Work& w, uint32_
   }
   // epilogue: every GEMM of the unit is done, so the Q and dO buffers are free
   if (ok) ok = wait(c, BAR_UNIT_DONE, 0);
-  if (named_bar_and(kBarDrain, 128, ok)) {
+  if (SPLIT) {
+    if (named_bar_and(kBarDrain, 128, ok)) {
+      tc_fence_after();
+      leave_sums(smem, tmem + lane_base + 256, r);
+    }
+  } else if (named_bar_and(kBarDrain, 128, ok)) {
     tc_fence_after();
     const int kvh = w.b * p.H_kv + w.g;
     const int n0 = w.n_block * kBc;
@@ -707,7 +777,7 @@ __device__ void drain_role(const Ctx& c, const Params& p, const Work& w, uint32_
 }
 
 // ------------------------------------------------------------------ kernel
-template <bool SOFTCAP, bool DET, bool DROP>
+template <bool SOFTCAP, bool DET, bool DROP, bool SPLIT>
 __global__ void __launch_bounds__(kThreadsFor<DROP>, 1)
     attn_bwd256_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
@@ -715,7 +785,8 @@ __global__ void __launch_bounds__(kThreadsFor<DROP>, 1)
                        const __grid_constant__ CUtensorMap tm_do,
                        const __grid_constant__ CUtensorMap tm_dq,
                        const __grid_constant__ CUtensorMap tm_dk,
-                       const __grid_constant__ CUtensorMap tm_dv, const Params p) {
+                       const __grid_constant__ CUtensorMap tm_dv,
+                       const std::conditional_t<SPLIT, SplitParams, Params> p) {
   using L = Layout;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -751,7 +822,7 @@ __global__ void __launch_bounds__(kThreadsFor<DROP>, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlot);
-  const Work w = work_of(p);
+  const Work w = work_of<SPLIT>(p);
   if (warp < 4) {
     if constexpr (DROP) setmaxnreg_dec<kRegsNarrowDrop>();
     if (warp == 0)
@@ -763,7 +834,7 @@ __global__ void __launch_bounds__(kThreadsFor<DROP>, 1)
     softmax_role<SOFTCAP, DROP>(c, p, w, smem, sbase, tmem);
   } else if (warp < 12) {
     if constexpr (DROP) setmaxnreg_inc<kRegsWideDrop>();
-    drain_role<DET>(c, p, w, sbase, tmem, &tm_dq, &tm_dk, &tm_dv);
+    drain_role<DET, SPLIT>(c, p, w, smem, sbase, tmem, &tm_dq, &tm_dk, &tm_dv);
   } else {
     if constexpr (DROP) {
       setmaxnreg_dec<kRegsNarrowDrop>();
@@ -772,6 +843,11 @@ __global__ void __launch_bounds__(kThreadsFor<DROP>, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (SPLIT) {
+    cluster_barrier();  // the sums of every CTA are there
+    join_sums(p, w, sbase);
+    cluster_barrier();  // and have been read
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -780,12 +856,38 @@ __global__ void __launch_bounds__(kThreadsFor<DROP>, 1)
 
 template <bool SOFTCAP, bool DET, bool DROP>
 int launch(const CUtensorMap (&m)[7], const Params& p, long long grid, cudaStream_t s) {
-  auto kern = attn_bwd256_kernel<SOFTCAP, DET, DROP>;
+  auto kern = attn_bwd256_kernel<SOFTCAP, DET, DROP, false>;
   static std::atomic<bool> configured[kMaxTrackedDevices];
   if (!set_smem_limit_once(kern, Layout::kBytes, configured)) return ATTN_ERR_LAUNCH;
   kern<<<static_cast<unsigned>(grid), kThreadsFor<DROP>, Layout::kBytes, s>>>(
       m[0], m[1], m[2], m[3], m[4], m[5], m[6], p);
   return launch_status();
+}
+
+// `units` units from the first on, each by a cluster of p.split CTAs.
+template <bool SOFTCAP>
+int launch_split(const CUtensorMap (&m)[7], const SplitParams& p, long long units,
+                 cudaStream_t s) {
+  auto kern = attn_bwd256_kernel<SOFTCAP, false, false, true>;
+  static std::atomic<bool> configured[kMaxTrackedDevices];
+  if (!set_smem_limit_once(kern, Layout::kBytes, configured)) return ATTN_ERR_LAUNCH;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(static_cast<unsigned>(units * p.split));
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = Layout::kBytes;
+  config.stream = s;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  if (cudaLaunchKernelEx(&config, kern, m[0], m[1], m[2], m[3], m[4], m[5], m[6], p) !=
+      cudaSuccess) {
+    cudaGetLastError();  // reported here, not by a later call
+    return ATTN_ERR_LAUNCH;
+  }
+  return ATTN_OK;
 }
 
 }  // namespace bwd256
@@ -837,7 +939,8 @@ int bwd256_run(const void* q, const void* k, const void* v, const void* dO, cons
   p.drop.keep = 1.f - p_drop;
   p.drop.log2_inv_keep =
       static_cast<float>(-std::log2(1.0 - static_cast<double>(p_drop)));
-  const long long grid = 2LL * p.n_blocks * H_kv * B;
+  p.first = 0;
+  long long grid = 2LL * p.n_blocks * H_kv * B;
   if (grid > 0x7fffffffLL) return ATTN_ERR_TOO_LARGE;
   CUtensorMap m[7];  // q, k, v, dO, dq (reduce), dk, dv (store)
   const long long hq = static_cast<long long>(B) * H, hk = static_cast<long long>(B) * H_kv;
@@ -847,6 +950,32 @@ int bwd256_run(const void* q, const void* k, const void* v, const void* dO, cons
             : encode_f32_3d(&m[4], dq_target, kD, N, hq, 32, kDh)) ||
       !encode_bf16_3d(&m[5], dk, kD, N, hk, kBc) || !encode_bf16_3d(&m[6], dv, kD, N, hk, kBc))
     return ATTN_ERR_LAUNCH;
+  if (p.sinks > 0) {  // neither dropout nor det
+    // As at d <= 128: units with sinks that outlast what an SM has on average are
+    // shared by clusters, in a launch of their own (1 x 8 heads over 2 x 4096, window
+    // 512: the step takes 211 us, not 700).
+    const int sms = sm_count();
+    if (sms <= 0) return ATTN_ERR_LAUNCH;
+    const long long heavy = 2LL * ((p.sinks + kBc - 1) / kBc) * H_kv * B;
+    const long long group = H / H_kv, most = group * p.m_blocks;
+    const long long band = std::min<long long>(
+        p.m_blocks, (static_cast<long long>(p.win_left) + p.win_right + kBc - 1) / kBr + 1);
+    const long long all = heavy * most + (grid - heavy) * group * band;
+    // the last such unit has the fewest tiles: one for each CTA at least
+    const long long least = group * (p.m_blocks - (p.sinks - 1) / kBc * (kBc / kBr));
+    SplitParams q{};
+    q.split = 1;
+    while (q.split < 8 && most * sms > all * 5 / 4 * q.split && 2 * q.split <= least) q.split *= 2;
+    if (q.split > 1) {
+      static_cast<Params&>(q) = p;
+      q.dk = static_cast<__nv_bfloat16*>(dk);
+      q.dv = static_cast<__nv_bfloat16*>(dv);
+      const int rc = cap ? launch_split<true>(m, q, heavy, s) : launch_split<false>(m, q, heavy, s);
+      if (rc != ATTN_OK || heavy == grid) return rc;
+      p.first = static_cast<int>(heavy);
+      grid -= heavy;
+    }
+  }
   if (p_drop > 0.f)  // not combined with det
     return cap ? launch<true, false, true>(m, p, grid, s)
                : launch<false, false, true>(m, p, grid, s);
