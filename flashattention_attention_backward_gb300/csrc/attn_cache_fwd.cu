@@ -58,7 +58,11 @@ constexpr int kBm = 128;  // rows of a tile (tensor-memory lanes)
 constexpr int kBn = 128;  // keys per block
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTileUnits = 2;  // what a tile costs besides its blocks, in blocks
+// What a tile costs besides its blocks, in blocks: about 2 us, against 0.9 us a block.
+// A prompt of 4096 tokens (32 heads over 8, d = 128, 1024 tiles of 1 to 32 blocks)
+// takes 137 us so, 159 with one and 189 with none; 256 requests of up to 300 keys 72,
+// 79 and 78.
+constexpr int kTileUnits = 2;
 constexpr int kMaxCtas = 192;  // parts of the line at most (the workspace's size)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -371,10 +375,8 @@ __device__ __forceinline__ void find_part(const Params& p, long long* sums, Part
   __syncthreads();
 }
 
-// Walks the tiles of a part; every role has its own, and one call of step(): it is
-// inlined, and more copies of it move the code of the roles' blocks apart, which
-// then misses the instruction cache (a chunk of 2048 tokens over 18432 keys took
-// 463 us with three, TODO with one).
+// Walks the tiles of a part; every role has its own and one call of step(), whose
+// code is long and inlined.
 struct Walk {
   int b, kvh, next, at, left;  // what comes: a tile, from which unit of it on; units left
   int tile, blk, take;         // the tile's blocks blk .. blk + take - 1 are the part's
@@ -588,7 +590,7 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn_major) {
 // what it spends between the last MMA of one product and the first of the next is
 // time of the tensor cores (with the whole warp in the loop, votes behind every
 // wait and a commit for each of the loaders, a chunk of 2048 tokens over 18432 keys
-// took 468 us, TODO so).
+// took 468 us, 419 so).
 template <typename T, int D>
 __device__ __forceinline__ void issue_mmas(const Ctx& c, const Params& p, const Part& part,
                                            uint32_t sbase, uint32_t tmem) {
@@ -700,18 +702,28 @@ __device__ __forceinline__ float chunk_p(const Params& p, const uint32_t (&raw)[
   const uint64_t out2 = f2_make(cap_out, cap_out);
   const float cap_u = SOFTCAP ? p.scale / p.softcap : 0.f;  // u = tau s / c
   const uint64_t cu2 = f2_make(cap_u, cap_u);
-  const uint64_t nsh2 = f2_make(-shift, -shift);
+  const uint64_t nsh2 = f2_make(-shift, -shift), plain2 = f2_make(c_log2, c_log2);
   uint64_t sum2 = f2_make(0.f, 0.f);
   uint32_t packed[32];
-  auto p_group = [&](auto fast_tag) {
-    constexpr bool FAST = decltype(fast_tag)::value;
+  // tanh's form: 0 through exp2, 1 the polynomial for |u| <= 1, 2 its Taylor sum up
+  // to u^7, for |u| <= 1/4, multiplied into the logit at once (the first term left
+  // out is below 8.3e-8, as the polynomial's error)
+  auto p_group = [&](auto form) {
+    constexpr int FORM = decltype(form)::value;
 #pragma unroll
     for (int u = 0; u < 32; ++u) {
       const uint64_t s2 = f2_make(raw[2 * u], raw[2 * u + 1]);
       uint64_t y2;
-      if (SOFTCAP) {
-        const uint64_t th2 = FAST ? softcap::tanh_poly2(f2_mul(s2, cu2))
-                                  : softcap::tanh_mufu2(f2_mul(s2, c2v));
+      if (SOFTCAP && FORM == 2) {
+        const uint64_t u2 = f2_mul(s2, cu2), x2 = f2_mul(u2, u2);
+        uint64_t w2 = f2_fma(x2, f2_make(-5.3968254e-2f, -5.3968254e-2f),
+                             f2_make(1.3333333e-1f, 1.3333333e-1f));
+        w2 = f2_fma(w2, x2, f2_make(-3.3333333e-1f, -3.3333333e-1f));
+        w2 = f2_fma(w2, x2, f2_make(1.f, 1.f));
+        y2 = f2_fma(f2_mul(s2, plain2), w2, nsh2);
+      } else if (SOFTCAP) {
+        const uint64_t th2 = FORM == 1 ? softcap::tanh_poly2(f2_mul(s2, cu2))
+                                       : softcap::tanh_mufu2(f2_mul(s2, c2v));
         y2 = f2_fma(th2, out2, nsh2);
       } else {
         y2 = f2_fma(s2, c2v, nsh2);
@@ -727,12 +739,15 @@ __device__ __forceinline__ float chunk_p(const Params& p, const uint32_t (&raw)[
     }
   };
   if constexpr (SOFTCAP) {
-    if (__all_sync(0xffffffffu, softcap::max_abs(raw) * cap_u <= softcap::kPolyMax))
-      p_group(std::true_type{});
+    const float most = softcap::max_abs(raw) * cap_u;
+    if (__all_sync(0xffffffffu, most <= 0.25f))
+      p_group(std::integral_constant<int, 2>{});
+    else if (__all_sync(0xffffffffu, most <= softcap::kPolyMax))
+      p_group(std::integral_constant<int, 1>{});
     else
-      p_group(std::false_type{});
+      p_group(std::integral_constant<int, 0>{});
   } else {
-    p_group(std::false_type{});
+    p_group(std::integral_constant<int, 0>{});
   }
   uint32_t lo[16], hi[16];
 #pragma unroll
@@ -1279,7 +1294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // row, D / 32 columns a lane, parts in order; where a tile has more than kJoinFew
 // parts the warps of a block share a row, warp k takes parts k, k + 8, ... and the
 // warps' sums are added in order (one token over 131072 keys, one key/value head:
-// 147 parts, TODO us with a warp a row).
+// 147 parts, 86 us with a warp a row, 32 so).
 constexpr int kJoinWarps = 8, kJoinSplit = 128 / kJoinWarps, kJoinFew = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Params p) {

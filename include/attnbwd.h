@@ -514,13 +514,15 @@ int attn_cache_append(const void* q, const void* k, const void* v, void* q_out, 
  *     j >= p - window_left (a negative window_left: no bound) or j < sinks;
  *   O = softmax(logits) V, LSE = ln sum exp(logits), logits as in attn_fwd.
  * A row that sees no key gets O = 0, LSE = -infinity.
- * In:  q [T,H,d]. Out: o [T,H,d], lse [T,H] fp32 contiguous (may be NULL).
+ * In:  q [T,H,d]. Out: o [T,H,d], lse [T,H] fp32 contiguous (may be NULL); they
+ *      overlap neither q nor the cache. Positions stay below 2^30.
  * Values in slots that no query of a sequence's call sees are never used,
  * whatever they hold (NaN too). Pages behind the window and past the sinks may
  * have been given away: their table entries are not read.
  * strides: HOST array of 10 element strides: (token, head) of q and o, (page,
- *      slot, head) of k_cache and v_cache; NULL: all contiguous. Multiples of
- *      8 elements (ATTN_ERR_ALIGN).
+ *      slot, head) of k_cache and v_cache; NULL: all contiguous. Positive
+ *      multiples of 8 elements (ATTN_ERR_ALIGN; but for dimensions of one
+ *      element).
  * d = 64, 128 or 256, page_size a multiple of 8, H / H_kv at most 128
  * (ATTN_ERR_UNSUPPORTED otherwise); scale > 0, sinks >= 0.
  * workspace: attn_cache_fwd_workspace_bytes(T, B, H, H_kv, d) bytes of device

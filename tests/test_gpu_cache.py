@@ -239,6 +239,11 @@ ATTEND = [
     ([(90, 300), (1, 70)], 4, 2, 64, 16, BF, -1, 0, 0.0, False, "slot"),
     ([(90, 300), (1, 70)], 4, 2, 128, 16, BF, 30, 9, 0.0, False, "slot"),
     ([(33, 500)], 4, 2, 256, 16, BF, 60, 5, 15.0, True, "slot"),
+    # logits far below the cap and near it; tiles of few rows and of many
+    ([(60, 300), (1, 700), (2, 40)], 8, 2, 128, 16, BF, -1, 0, 50.0, True, "slot"),
+    ([(60, 300), (1, 700), (2, 40)], 6, 2, 64, 16, HF, 90, 3, 400.0, True, "head"),
+    ([(1, 3000), (3, 100)], 8, 2, 64, 64, BF, -1, 0, 3.0, True, "slot"),
+    ([(1, 2000), (1, 90), (2, 500)], 16, 1, 64, 32, BF, 700, 6, 30.0, True, "slot"),
 ]
 
 
@@ -306,6 +311,20 @@ def test_bad_pages_and_long_lengths():
     assert attn.attn_device_status(clear=True)[1] == attn.ATTN_ERR_PAGE
     assert torch.equal(o3[0], runner.cache_attention(c.q, *c.batch(), 0.125)[0][0])
     attn.attn_device_status(clear=True)
+
+
+def test_without_lse_and_strides():
+    """The C entry point with no place for LSE and contiguous tensors."""
+    c = Case([(3, 130), (1, 300)], 4, 2, 128, 16, BF)
+    q, o = c.q.contiguous(), torch.empty(c.T, 4, 128, dtype=BF, device="cuda")
+    ws = torch.empty(attn.attn_cache_fwd_workspace_bytes(c.T, 2, 4, 2, 128), dtype=torch.uint8,
+                     device="cuda")
+    attn.check(attn.attn_cache_fwd(q, *c.caches, o, None, c.starts_d, c.lengths_d, c.pages_d, ws,
+                                   c.T, 2, 4, 2, 128, 16, c.max_pages, c.n_pages, 0.1, True, 0.0,
+                                   -1, 0, attn.ATTN_BF16))
+    want, lse = c.attend(scale=0.1)
+    assert torch.equal(o, want)
+    c.check(o, lse, scale=0.1)
 
 
 def test_shared_pages():

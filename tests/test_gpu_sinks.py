@@ -37,6 +37,14 @@ CASES = [
     (_w(1, 2, 2, 333, 64, True), (5, -1), 5000),
     (_w(16, 8, 4, 300, 128, True), (20, -1), 3),
     (_w(1, 2, 2, 385, 128, False), (-1, 37), 64),
+    # key blocks with sinks that clusters of CTAs share, ragged ends, few and
+    # many heads a group, all sinks in one block and in several
+    (_w(1, 8, 1, 1500, 128, True), (100, -1), 4),
+    (_w(1, 3, 3, 2001, 64, True), (64, -1), 200),
+    (_w(1, 4, 2, 1300, 64, False, 3.0, 2.0), (70, 30), 257),
+    (_w(2, 5, 1, 1111, 256, True), (50, -1), 129),
+    (_w(1, 1, 1, 1030, 256, False, 4.0, 2.0), (50, 9), 1),
+    (_w(1, 2, 1, 1025, 128, True, 8.0, 2.0), (10, -1), 1025),
 ]
 
 
