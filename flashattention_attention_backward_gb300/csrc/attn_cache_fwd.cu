@@ -1437,10 +1437,12 @@ int run(const Tensors& x, const Params& given, int d, cudaStream_t stream) {
   const long long v_stride[3] = {x.v_in[2], x.v_in[1], x.v_in[0]};
   const int narrow_tokens = given.narrow > 0 ? given.narrow / given.G : 1;
   if (!encode_4d<T>(&maps[0], x.q, d, q_extent, q_stride, {given.G, 1, given.tokens}) ||
-      !encode_4d<T>(&maps[1], x.q, d, q_extent, q_stride, {given.G, 1, narrow_tokens}) ||
+      (given.narrow > 0 &&
+       !encode_4d<T>(&maps[1], x.q, d, q_extent, q_stride, {given.G, 1, narrow_tokens})) ||
       !encode_4d<T>(&maps[2], x.k, d, extent, k_stride, {1, given.box, 1}) ||
       !encode_4d<T>(&maps[3], x.v, d, extent, v_stride, {1, given.box, 1}))
     return ATTN_ERR_LAUNCH;
+  if (given.narrow == 0) maps[1] = maps[0];  // not used
   // as many parts as there can be blocks, one an SM at most
   const long long tiles = (c.T / given.tokens + static_cast<long long>(c.B)) * given.H_kv;
   const long long blocks = (given.cap + kBn - 1) / kBn;

@@ -269,6 +269,34 @@ def test_attention(seqs, H, H_kv, d, page, dtype, left, sinks, softcap, causal, 
     assert torch.equal(o2[rows], o[rows, :H]) and torch.equal(lse2[rows], lse[rows])
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn(seed):
+    """Batches drawn from all that the call takes: chunks and single tokens,
+    pages of any multiple of 8, groups of up to 128 heads, windows, sinks."""
+    r = np.random.default_rng(100 + seed)
+    d = int(r.choice([64, 128, 256]))
+    H_kv = int(r.choice([1, 2, 3, 5]))
+    G = int(r.choice([1, 2, 3, 4, 7, 8, 16, 33]))
+    longest = int(r.choice([40, 400, 3000]))
+    seqs = []
+    for _ in range(int(r.integers(1, 9))):
+        n = int(r.choice([0, 1, 1, r.integers(1, 9), r.integers(1, 150)]))
+        seqs.append((n, n + int(r.integers(0, longest))))
+    seqs.append((1, 1 + int(r.integers(0, longest))))
+    softcap = float(r.choice([0.0, 0.0, 2.0, 30.0, 300.0]))
+    c = Case(seqs, H_kv * G, H_kv, d, int(r.choice([8, 16, 24, 40, 64, 104, 128, 192])),
+             [BF, HF][seed % 2], int(r.choice([-1, -1, 0, 9, 127, 128, 500])),
+             int(r.choice([0, 0, 1, 5, 64, 128, 300])), bool(r.random() < 0.8),
+             str(r.choice(["slot", "head"])), seed, int(r.integers(0, 3)), int(r.integers(0, 3)),
+             float(r.choice([0.5, 1.0, 2.0])))
+    o, lse = c.attend(softcap=softcap)
+    c.check(o, lse, softcap=softcap)
+    rows = slice(int(c.starts[0]), int(c.starts[-1]))
+    c.hide()
+    o2, lse2 = c.attend(softcap=softcap)
+    assert torch.equal(o2[rows], o[rows]) and torch.equal(lse2[rows], lse[rows])
+
+
 def test_large_logits():
     """Logits far apart and far from 0: the running maximum moves often, and a
     scale of its own."""
