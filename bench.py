@@ -42,6 +42,7 @@ METRIC = "attention-backward TFLOPS and % of GB300 bf16 tensor peak; ms per bwd 
 UNIT = "TFLOPS"
 PEAK_FALLBACK = {"bf16_tflops": 1890.0, "hbm_gbs": 6800.0, "source": "fallback"}
 KERNEL_SOURCES = ["flashattention_attention_backward_gb300/csrc/attn_bwd.cu",
+                  "flashattention_attention_backward_gb300/csrc/attn_bwd_kernel.cuh",
                   "flashattention_attention_backward_gb300/csrc/sm103_ptx.cuh"]
 TRAFFIC_PROFILE = os.path.join(ROOT, "profiles", "attn_bwd_causal_gqa_traffic.json")
 
