@@ -31,7 +31,7 @@
 // CTAs share leaves its partial O, m and l in the workspace, and a second, small
 // kernel joins them in the order of the blocks: the same bits every time. Each
 // CTA finds its part of the line itself, from two sums over the sequences.
-//   warp 0      Q of each tile; K in a ring of 2 stages (d <= 128) or 1
+//   warp 0      Q of each tile; K in a ring of 4, 2 or 1 stages (d = 64, 128, 256)
 //   warp 2      V in the same kind of ring
 //   warp 3      zeroes rows of V
 //   warp 1      MMA issuer: per tile S(0), then per block S(j + 1), P(j) V

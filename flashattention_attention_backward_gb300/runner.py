@@ -120,7 +120,7 @@ def forward(q, k, v, scale, causal, softcap=0.0, stream=None, impl="tc", dropout
     B, H, H_kv, N, d = _dims(q, k, v)
     if v.shape != k.shape:
         raise ValueError("v must have the shape of k")
-    window = _check_sinks(sinks, window, dropout)
+    window, sinks = _check_sinks(sinks, window, dropout)
     args = (B, H, H_kv, N, d, scale, causal, softcap)
     if dropout is not None:
         fn = {"tc": attn_fwd_dropout, "ref": attn_fwd_ref_dropout}[impl]
@@ -142,12 +142,21 @@ def forward(q, k, v, scale, causal, softcap=0.0, stream=None, impl="tc", dropout
 
 
 def _check_sinks(sinks, window, dropout):
-    """The window of a call with sinks (unbounded if there is none)."""
+    """(window, sinks) of a call: with sinks and no window, one without bounds."""
     if sinks < 0:
         raise ValueError("sinks must not be negative")
     if sinks and dropout is not None:
         raise ValueError("sinks have no dropout variant")
-    return (-1, -1) if sinks and window is None else window
+    if sinks and window is None:
+        window = (-1, -1)
+    return window if window is None else tuple(_bound(n) for n in window), _bound(sinks)
+
+
+def _bound(n):
+    """A count of keys as the C calls take it: an int keeps its low 32 bits on
+    the way there, and every count from 2^30 on (past every position) hides
+    and shows the same keys. Negative ones all mean no bound."""
+    return max(-1, min(n, 1 << 30))
 
 
 class BackwardBuffers:
@@ -192,7 +201,7 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
         positions, pos_stride = _check_rotary(rotary, positions, B, N, d, q.device)
     elif positions is not None:
         raise ValueError("positions are those of a rotary")
-    window = _check_sinks(sinks, window, dropout)
+    window, sinks = _check_sinks(sinks, window, dropout)
     if dropout is None and window is not None and deterministic:
         raise ValueError("the local window has no deterministic variant")
     with _On(stream, q.device) as on:
@@ -355,6 +364,8 @@ def _check_cache(q, k_cache, v_cache, pages, starts, lengths, dtype):
         raise ValueError("expected rows [T, heads, %d]" % d)
     if q is not None and d > 1 and q.stride(2) != 1:
         raise ValueError("rows must be contiguous")
+    if max(n_pages, page_size, pages.shape[1], 0 if q is None else q.shape[0]) >= 1 << 31:
+        raise ValueError("sizes must stay below 2^31")
     _check_cuda(k_cache.device, k_cache=k_cache, v_cache=v_cache, pages=pages, starts=starts,
                 lengths=lengths, q=q)
     return pages.shape[0], H_kv, d, page_size, pages.shape[1], n_pages
@@ -376,6 +387,8 @@ def cache_append(q, k, v, k_cache, v_cache, pages, starts, lengths, plan, out=No
             raise ValueError("%s must be [T, %d, %d] of k's dtype" % (name, H_kv, d))
         if d > 1 and t.stride(2) != 1:
             raise ValueError("rows must be contiguous")
+    if k.shape[0] >= 1 << 31:
+        raise ValueError("sizes must stay below 2^31")
     if q is not None and (q.shape[0] != k.shape[0] or q.dtype != k.dtype):
         raise ValueError("q must have k's rows and dtype")
     if out is not None:
@@ -446,8 +459,8 @@ def cache_attention(q, k_cache, v_cache, pages, starts, lengths, scale, causal=T
             [n for t in (k_cache, v_cache) for n in t.stride()[:3]]
         check(attn_cache_fwd(q, k_cache, v_cache, out[0], out[1], starts, lengths, pages,
                              workspace, T, B, H, H_kv, d, page_size, max_pages, n_pages, scale,
-                             causal, softcap, window_left, sinks, _DTYPES[q.dtype], strides,
-                             on.stream))
+                             causal, softcap, _bound(window_left), _bound(sinks), _DTYPES[q.dtype],
+                             strides, on.stream))
     return out
 
 

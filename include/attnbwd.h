@@ -525,7 +525,8 @@ int attn_cache_append(const void* q, const void* k, const void* v, void* q_out, 
  *      element).
  * d = 64, 128 or 256, page_size a multiple of 8, H / H_kv at most 128
  * (ATTN_ERR_UNSUPPORTED otherwise); scale > 0, sinks >= 0.
- * workspace: attn_cache_fwd_workspace_bytes(T, B, H, H_kv, d) bytes of device
+ * workspace: attn_cache_fwd_workspace_bytes(T, B, H, H_kv, d) bytes (an
+ *      ATTN_ERR_* code, negative, for sizes that a call refuses) of device
  *      memory, whose contents need no preparation and mean nothing after.
  *      Calls that may run at the same time (two streams, two captured graphs)
  *      need one each, and a captured call's lives as long as its graph.
@@ -542,7 +543,8 @@ int attn_cache_fwd(const void* q, const void* k_cache, const void* v_cache, void
  * attn_device_status: waits for `stream`, then reads the library's device
  * status word into *status (0 = no fault; ATTN_ERR_DEVICE_TIMEOUT when a
  * kernel gave up waiting on a barrier; ATTN_ERR_DEVICE for an internal
- * check; ATTN_ERR_PAGE when a call over a paged cache met a slot outside it). clear != 0 resets it to 0. Returns ATTN_OK or a launch error.
+ * check; ATTN_ERR_PAGE when a call over a paged cache met a slot outside it).
+ * clear != 0 resets it to 0. Returns ATTN_OK or a launch error.
  */
 int attn_device_status(int* status, int clear, void* stream);
 

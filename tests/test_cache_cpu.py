@@ -137,6 +137,9 @@ def _tensors(**kw):
     (dict(pages=torch.zeros(2, 3)), "int32"),
     (dict(lengths=torch.zeros(2, dtype=torch.int64)), "int32"),
     (dict(starts=torch.zeros(2, dtype=torch.int32)), "starts"),
+    (dict(zip(("k_cache", "v_cache"),
+              [torch.zeros(1, 8, 2, 64, dtype=torch.bfloat16).expand(1 << 32, 8, 2, 64)] * 2)),
+     "2\\^31"),
     (dict(q=torch.zeros(5, 4, 32, dtype=torch.bfloat16)), "rows"),
     (dict(q=torch.zeros(5, 64, 4, dtype=torch.bfloat16).transpose(1, 2)), "contiguous"),
 ])
@@ -149,3 +152,9 @@ def test_runner_refusals(lib, kw, what):
         runner.cache_append(t["q"], t["k"], t["v"], *rest, plan)
     with pytest.raises(ValueError, match=what):
         runner.cache_attention(t["q"], *rest, 0.125)
+
+
+def test_runner_bounds_counts():
+    # what the C calls take is the low 32 bits of an int
+    assert [runner._bound(n) for n in (-(1 << 40), -1, 0, 7, 1 << 30, 1 << 32, (1 << 40) + 1)] == \
+        [-1, -1, 0, 7, 1 << 30, 1 << 30, 1 << 30]

@@ -341,6 +341,16 @@ def test_bad_pages_and_long_lengths():
     attn.attn_device_status(clear=True)
 
 
+def test_counts_past_32_bits():
+    """A window and sinks that an int32 cannot hold."""
+    c = Case([(3, 130), (1, 300)], 4, 2, 64, 16, BF)
+    want, lse = c.attend()
+    for left, sinks in ((1 << 32, 0), ((1 << 32) + 5, 0), (5, 1 << 32), (5, (1 << 31) + 1)):
+        c.left, c.sinks = left, sinks
+        o, lse2 = c.attend()
+        assert torch.equal(o, want) and torch.equal(lse, lse2), (left, sinks)
+
+
 def test_without_lse_and_strides():
     """The C entry point with no place for LSE and contiguous tensors."""
     c = Case([(3, 130), (1, 300)], 4, 2, 128, 16, BF)

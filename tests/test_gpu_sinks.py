@@ -105,6 +105,21 @@ def test_no_sinks_is_the_local_call():
         assert torch.equal(dk, dk2) and torch.equal(dv, dv2)
 
 
+def test_counts_past_32_bits():
+    """Every key a sink: the causal call's values, up to P's and O's roundings."""
+    w = _w(1, 4, 2, 300, 64, True)
+    x = make_inputs(w)
+    f64 = {n: x[n].double().numpy() for n in ("q", "k", "v")}
+    O, LSE = attention_forward(f64["q"], f64["k"], f64["v"], w.scale, True, 0.0)
+    q, k, v = (x[n].cuda() for n in ("q", "k", "v"))
+    for win, sinks in (((70, -1), 1 << 32), ((1 << 32, 1 << 33), 0), ((1 << 32, -1), 3)):
+        out = {}
+        for impl in ("tc", "ref"):
+            out["o_" + impl], out["lse_" + impl] = runner.forward(
+                q, k, v, w.scale, True, window=win, sinks=sinks, impl=impl)
+        _check_forward({n: t.cpu() for n, t in out.items()}, O, LSE)
+
+
 def test_captured_and_on_a_stream():
     """A captured step replayed on new inputs, and one on a side stream."""
     w = _w(2, 4, 2, 600, 64, True)

@@ -108,3 +108,9 @@ def _refuse_deterministic(kw):
         runner.backward(t, t, t, t, t, None, 0.125, True, **kw)
     finally:
         runner._dims, runner._check_lse = saved
+
+
+def test_counts_past_32_bits():
+    assert runner._check_sinks(1 << 32, None, None) == ((-1, -1), 1 << 30)
+    assert runner._check_sinks(0, (-1 << 33, 1 << 33), None) == ((-1, 1 << 30), 0)
+    assert runner._check_sinks(0, None, (0.1, 3)) == (None, 0)
