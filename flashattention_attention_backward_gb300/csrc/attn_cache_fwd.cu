@@ -785,6 +785,15 @@ __device__ __forceinline__ void scale_o(uint32_t tO, float f) {
   }
 }
 
+// The sum of a row that sees nothing is 0 (of one that does 1 or more, but for
+// roundings), and NaN where one of its logits is, and then O and LSE are NaN too.
+__device__ __forceinline__ float inverse_of(float total) {
+  return total == 0.f ? 0.f : 1.f / total;
+}
+__device__ __forceinline__ float lse_of(float m, float total) {
+  return total == 0.f ? -INFINITY : (m + __log2f(total)) * kLn2;
+}
+
 // One row's running shift (log2 units) and sum.
 struct Stats {
   float m, l;
@@ -893,9 +902,9 @@ __device__ __forceinline__ bool epilogue(const Ctx& c, const Params& p, const Pa
       for (int k = 0; k < 4; ++k) M = fmaxf(M, shifts[32 * k + at]);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (shifts[32 * k + at] > -INFINITY)
-          total = fmaf(xsum[32 * k + at] + xsum[128 + 32 * k + at],
-                       ex2_approx(shifts[32 * k + at] - M), total);
+        total = fmaf(xsum[32 * k + at] + xsum[128 + 32 * k + at],
+                     shifts[32 * k + at] > -INFINITY ? ex2_approx(shifts[32 * k + at] - M) : 1.f,
+                     total);  // without a maximum the sum is 0, or NaN
     };
     float M, total;
     join(lane, M, total);
@@ -905,7 +914,7 @@ __device__ __forceinline__ bool epilogue(const Ctx& c, const Params& p, const Pa
         partial[lane] = M;
         partial[128 + lane] = total;
       } else if (p.lse != nullptr) {
-        p.lse[out_row * p.H + head] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
+        p.lse[out_row * p.H + head] = lse_of(M, total);
       }
     }
     // [quadrant][row][column] fp32 over all of the warps' stages, then the quadrants
@@ -944,7 +953,7 @@ __device__ __forceinline__ bool epilogue(const Ctx& c, const Params& p, const Pa
         *reinterpret_cast<float4*>(partial + 256 + at * D + col) = o;
       } else {
         join(at, M, total);
-        const float inv = total > 0.f ? 1.f / total : 0.f;
+        const float inv = inverse_of(total);
         const int tok = at / p.G;
         T* out = static_cast<T*>(p.o) + (static_cast<long long>(d.row0) + tok) * p.o_token +
                  (d.kvh * p.G + at - tok * p.G) * p.o_head + col;
@@ -957,7 +966,7 @@ __device__ __forceinline__ bool epilogue(const Ctx& c, const Params& p, const Pa
     const float total = xsum[r] + xsum[128 + r];
     if (whole) {
       T* out = static_cast<T*>(p.o) + out_row * p.o_token + head * p.o_head + h * (D / 2);
-      const float inv = total > 0.f ? 1.f / total : 0.f;
+      const float inv = inverse_of(total);
       const uint64_t inv2 = f2_make(inv, inv);
 #pragma unroll
       for (int c0 = 0; c0 < D / 2; c0 += 32) {
@@ -967,12 +976,12 @@ __device__ __forceinline__ bool epilogue(const Ctx& c, const Params& p, const Pa
         for (int u = 0; u < 16; ++u) {
           const uint64_t v = f2_mul(f2_make(raw[2 * u], raw[2 * u + 1]), inv2);
           // a row that sees nothing: its P V was 0 times what V held
-          packed[u] = total > 0.f ? pack_pair<T>(f2_lo(v), f2_hi(v)) : 0u;
+          packed[u] = total != 0.f ? pack_pair<T>(f2_lo(v), f2_hi(v)) : 0u;
         }
         store_rows(stage, packed, mine ? reinterpret_cast<unsigned long long>(out + c0) : 0ull);
       }
       if (mine && h == 0 && p.lse != nullptr)
-        p.lse[out_row * p.H + head] = total > 0.f ? (d.x.m + __log2f(total)) * kLn2 : -INFINITY;
+        p.lse[out_row * p.H + head] = lse_of(d.x.m, total);
     } else {
       if (mine && h == 0) {
         partial[r] = d.x.m;
@@ -1209,8 +1218,8 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
     }
     const Done done{{m_used, l}, nt, w.blk, w.t.nt, w.left, w.s.row0 + w.tile * p.tokens,
                     w.kvh, rows, narrow};
-    ok = epilogue<T, D, SOFTCAP>(c, p, part, done, ok, i, h, tmem + lane_base, xsum, shifts, smem, stage,
-                        token);
+    ok = epilogue<T, D, SOFTCAP>(c, p, part, done, ok, i, h, tmem + lane_base, xsum, shifts,
+                                 smem, stage, token);
     g += nt;
   }
 }
@@ -1338,9 +1347,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Param
       for (int u = 0; u < kAhead; ++u) {
         const int i = i0 + u * step;
         if (i >= s.parts) break;
-        const float f = ex2_approx(slot(i)[r] - shift);
+        const float f = ex2_approx(slot(i)[r] - shift), l = slot(i)[128 + r];
+        total = fmaf(l, f, total);
         if (f > 0.f) {  // a part that saw nothing holds no numbers
-          total = fmaf(slot(i)[128 + r], f, total);
 #pragma unroll
           for (int e = 0; e < E / 2; ++e) {
             o[e].x = fmaf(v[u][e].x, f, o[e].x);
@@ -1366,7 +1375,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Param
         }
       }
     }
-    const float inv = total > 0.f ? 1.f / total : 0.f;
+    const float inv = inverse_of(total);
     const int token = r / p.G, head = s.kvh * p.G + r - token * p.G;
     const long long row = static_cast<long long>(s.row0) + token;
     T* out = static_cast<T*>(p.o) + row * p.o_token + head * p.o_head + lane * E;
@@ -1374,7 +1383,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Param
     for (int e = 0; e < E / 2; ++e)
       reinterpret_cast<uint32_t*>(out)[e] = pack_pair<T>(o[e].x * inv, o[e].y * inv);
     if (lane == 0 && p.lse != nullptr)
-      p.lse[row * p.H + head] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
+      p.lse[row * p.H + head] = lse_of(M, total);
   }
 }
 

@@ -513,7 +513,7 @@ int attn_cache_append(const void* q, const void* k, const void* v, void* q_out, 
  *     0 <= j < length, j <= p if causal != 0, and
  *     j >= p - window_left (a negative window_left: no bound) or j < sinks;
  *   O = softmax(logits) V, LSE = ln sum exp(logits), logits as in attn_fwd.
- * A row that sees no key gets O = 0, LSE = -infinity.
+ * A row that sees no key gets O = 0, LSE = -infinity; one with a NaN logit NaN.
  * In:  q [T,H,d]. Out: o [T,H,d], lse [T,H] fp32 contiguous (may be NULL); they
  *      overlap neither q nor the cache. Positions stay below 2^30.
  * Values in slots that no query of a sequence's call sees are never used,

@@ -318,6 +318,42 @@ def test_rows_that_see_nothing():
     assert (o == 0).all() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("length", [40, 3000])  # tiles of one CTA and of many
+def test_nan_stays_visible(length, d, softcap):
+    """NaN in a query, or in a key that a row sees: its O and LSE are NaN, and the
+    other rows what they were."""
+    c = Case([(1, length), (2, length + 7)], 4, 2, d, 16, BF)
+    o, lse = c.attend(softcap=softcap)
+
+    def same(rows, o2, lse2):
+        if softcap == 0:
+            assert torch.equal(o2[rows], o[rows]) and torch.equal(lse2[rows], lse[rows])
+            return
+        # rows of one warp share tanh's form, which a NaN among them may change:
+        # logits then differ by 20 * 2e-7, LSE by as much and its roundings; every P
+        # and O may round to the other side, each a step of 2^-7, and the mean of
+        # |v|, weighted, stays below 2
+        assert float((lse2[rows] - lse[rows]).abs().max()) <= 1e-5 + 8 * U * 10
+        assert float((o2[rows].double() - o[rows].double()).abs().max()) <= 2 * 2 * 2 ** -7
+
+    q = c.q.clone()
+    q[0, 1, 5] = float("nan")
+    o2, lse2 = c.attend(q=q, softcap=softcap)
+    bad = torch.zeros(3, 4, dtype=torch.bool, device="cuda")
+    bad[0, 1] = True
+    assert o2[bad].isnan().all() and lse2[bad].isnan().all()
+    same(~bad, o2, lse2)
+    # key/value head 0 of the second sequence at its first position
+    c.caches[0][int(c.table[1, 0]), 0, 0, 0] = float("nan")
+    o3, lse3 = c.attend(softcap=softcap)
+    bad.zero_()
+    bad[1:, :2] = True
+    assert o3[bad].isnan().all() and lse3[bad].isnan().all()
+    same(~bad, o3, lse3)
+
+
 def test_bad_pages_and_long_lengths():
     """A page outside the cache reads as zeros, keys past the table are hidden;
     both are reported."""
