@@ -53,6 +53,7 @@
 #include <type_traits>
 
 #include "attn_common.cuh"
+#include "element.cuh"
 #include "grid_ptx.cuh"
 #include "philox.cuh"
 #include "sm103_ptx.cuh"
@@ -822,6 +823,9 @@ __global__ void __launch_bounds__(kThreadsFor<DROP>, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlot);
+  // The launch of the other units, whose inputs are this one's, may begin once all
+  // CTAs of this one hold their tensor memory ...
+  if constexpr (SPLIT) grid_dependency_launch();
   const Work w = work_of<SPLIT>(p);
   if (warp < 4) {
     if constexpr (DROP) setmaxnreg_dec<kRegsNarrowDrop>();
@@ -852,6 +856,10 @@ __global__ void __launch_bounds__(kThreadsFor<DROP>, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // ... and ends, with its last CTA, behind this one: what follows in the stream
+  // waits for both.
+  if constexpr (!SPLIT && !DET && !DROP)
+    if (p.first > 0 && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
 
 template <bool SOFTCAP, bool DET, bool DROP>
@@ -859,6 +867,9 @@ int launch(const CUtensorMap (&m)[7], const Params& p, long long grid, cudaStrea
   auto kern = attn_bwd256_kernel<SOFTCAP, DET, DROP, false>;
   static std::atomic<bool> configured[kMaxTrackedDevices];
   if (!set_smem_limit_once(kern, Layout::kBytes, configured)) return ATTN_ERR_LAUNCH;
+  if (p.first > 0)  // behind launch_split: may begin beside it
+    return launch_overlapped(kern, dim3(static_cast<unsigned>(grid)), kThreadsFor<DROP>,
+                             Layout::kBytes, 0, s, m[0], m[1], m[2], m[3], m[4], m[5], m[6], p);
   kern<<<static_cast<unsigned>(grid), kThreadsFor<DROP>, Layout::kBytes, s>>>(
       m[0], m[1], m[2], m[3], m[4], m[5], m[6], p);
   return launch_status();
@@ -952,8 +963,9 @@ int bwd256_run(const void* q, const void* k, const void* v, const void* dO, cons
     return ATTN_ERR_LAUNCH;
   if (p.sinks > 0) {  // neither dropout nor det
     // As at d <= 128: units with sinks that outlast what an SM has on average are
-    // shared by clusters, in a launch of their own (1 x 8 heads over 2 x 4096, window
-    // 512: the step takes 211 us, not 700).
+    // shared by clusters, in a launch of their own that the others' runs beside (1 x 8
+    // heads over 2 x 4096, window 512: the step takes 122 us, 211 with one launch behind
+    // the other, 700 without clusters).
     const int sms = sm_count();
     if (sms <= 0) return ATTN_ERR_LAUNCH;
     const long long heavy = 2LL * ((p.sinks + kBc - 1) / kBc) * H_kv * B;

@@ -1149,6 +1149,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlot);
+  // The launch of the other units, whose inputs are this one's, may begin once all
+  // CTAs of this one hold their tensor memory ...
+  if constexpr (SPLIT) grid_dependency_launch();
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsCtl>();
@@ -1181,6 +1184,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // ... and ends, with its last CTA, behind this one: what follows in the stream
+  // waits for both.
+  if constexpr (SINKS && !SPLIT)
+    if (blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
 
 // Tensor maps of one call: loads of Q, K, V, dO; reductions into dq_accum;

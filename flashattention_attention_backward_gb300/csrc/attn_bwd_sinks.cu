@@ -4,15 +4,20 @@
 #include <algorithm>
 
 #include "attn_bwd_kernel.cuh"
+#include "element.cuh"
 
 namespace attn {
 namespace bwd {
 
+// The units from p.first_unit on; behind launch_split they may begin beside its.
 template <int D, bool SOFTCAP>
 int launch_units(const Maps& m, const SinkParams& p, int grid, cudaStream_t stream) {
   auto kern = attn_bwd_kernel<D, false, SOFTCAP, false, false, true, false>;
   static std::atomic<bool> configured[kMaxTrackedDevices];
   if (!set_smem_limit_once(kern, Layout<D>::kBytes, configured)) return ATTN_ERR_LAUNCH;
+  if (p.split > 1)
+    return launch_overlapped(kern, dim3(static_cast<unsigned>(grid)), kThreads, Layout<D>::kBytes,
+                             0, stream, m.q, m.k, m.v, m.dO, m.dq, m.dk, m.dv, p);
   kern<<<grid, kThreads, Layout<D>::kBytes, stream>>>(m.q, m.k, m.v, m.dO, m.dq, m.dk, m.dv, p);
   return launch_status();
 }
@@ -53,8 +58,9 @@ int launch_both(const Maps& m, SinkParams p, cudaStream_t stream) {
       p.m_blocks, (static_cast<long long>(p.win_left) + p.win_right + kBc - 1) / kBr + 1);
   const long long all = with_sinks * most + (p.n_units - with_sinks) * group * band_tiles;
   // A unit with sinks that outlasts what an SM has on average is shared by a
-  // cluster of CTAs, in a launch of its own (1 x 8 heads over 1 x 16384 x 128, window
-  // 1024: the step takes 532 us, not 2361; 1 x 4 x 8192 x 64, window 512: 67, not 149).
+  // cluster of CTAs, in a launch of its own that the other units' runs beside (1 x 8
+  // heads over 1 x 16384 x 128, window 1024: the step takes 357 us, 528 with one launch
+  // behind the other, 2361 without clusters; 1 x 4 x 8192 x 64, window 512: 51, 67, 149).
   // The last such unit has the fewest tiles: one for each CTA at least.
   const long long least = group * (p.m_blocks - (p.sinks - 1) / kBc);
   while (p.split < 8 && most * sms > all * 5 / 4 * p.split && 2 * p.split <= least) p.split *= 2;
