@@ -45,6 +45,8 @@ CASES = [
     (_w(2, 5, 1, 1111, 256, True), (50, -1), 129),
     (_w(1, 1, 1, 1030, 256, False, 4.0, 2.0), (50, 9), 1),
     (_w(1, 2, 1, 1025, 128, True, 8.0, 2.0), (10, -1), 1025),
+    # more clusters than run at once
+    (_w(1, 18, 18, 1000, 64, True), (60, -1), 4),
 ]
 
 
@@ -149,6 +151,33 @@ def test_captured_and_on_a_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("w,left,sinks", [(_w(1, 8, 1, 1500, 128, True), 100, 4),
+                                          (_w(2, 5, 1, 1111, 256, True), 50, 129)],
+                         ids=["128", "256"])
+def test_captured_with_clusters(w, left, sinks):
+    """Both launches of the backward have ended where what follows them begins: a
+    captured step, replayed over and over, gives the oracle's gradients."""
+    dev = torch.device("cuda:0")
+    x = make_inputs(w)
+    q, k, v, do = (x[n].to(dev) for n in ("q", "k", "v", "do"))
+    kw = dict(window=(left, -1), sinks=sinks)
+    o, lse = runner.forward(q, k, v, w.scale, True, **kw)
+    runner.backward(q, k, v, o, do, lse, w.scale, True, **kw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = [runner.backward(q, k, v, o, do, lse, w.scale, True, **kw) for _ in range(2)]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    f64 = {n: x[n].double().numpy() for n in ("q", "k", "v", "do")}
+    grads = attention_backward(f64["q"], f64["k"], f64["v"], f64["do"], w.scale, True, 0.0,
+                               window=(left, -1), sinks=sinks)
+    for got in out:
+        for name, t, g in zip(("dq", "dk", "dv"), got, grads):
+            check_grad(name, t.cpu(), g)
 
 
 def test_rotary_gradients():
