@@ -5,9 +5,10 @@
 // j <= p (or all of the sequence's) with j >= p - left or j < sinks:
 //   x_j = logit of q and key j (log2 units),  O = sum_j 2^(x_j - m) v_j / l,
 //   l = sum_j 2^(x_j - m),  LSE = (m + log2 l) ln 2
-// with a running maximum m and sum l, as in attn_fwd: S = Q K^T in fp32 tensor
-// memory, P as 16-bit pairs over it, O accumulated in tensor memory and rescaled
-// only when a row's maximum grows by more than 2^8.
+// with a running shift m, the row's maximum (less 9 with fp16, see kHead), and sum l,
+// as in attn_fwd: S = Q K^T in fp32 tensor memory, P as 16-bit pairs over it, O
+// accumulated in tensor memory and rescaled only when a row's maximum outgrows it (by
+// more than 2^8, with fp16 2^6).
 //
 // Tiles. The G = H / H_kv heads that share a key/value head sit in one tile with
 // the tokens: row r of a tile is token r / G and head r mod G, floor(128 / G)
@@ -66,7 +67,19 @@ constexpr int kTileUnits = 2;
 constexpr int kMaxCtas = 192;  // parts of the line at most (the workspace's size)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescale = 8.f;  // move the shift only when the maximum grows by more
+// A row's shift is its maximum less kHead, moved only when that outgrows it by more
+// than kRescale (log2 units), so that weights stay below 2^(kHead + kRescale) and the
+// largest is 2^kHead or more. bf16 has fp32's exponents. An fp16 operand has eleven
+// bits down to 2^-14 only and is 0 below 2^-25: with the shift at the maximum, keys
+// that weigh 2^-23 of one large key each lost a seventh of what they weigh together,
+// and at 2^-25 all of it, while l kept it. Weights up to 2^15 instead (fp16 ends at
+// 2^16) have eleven bits down to 2^-23 of the row's largest, and below an error of 2^-34
+// of it. A ragged batch under a window and a softcap takes 70.4 us in fp16 so and 69.9
+// in bf16; with 11 and 4 71.9, with 7 and 8 70.3.
+template <typename T>
+constexpr float kHead = std::is_same<T, __half>::value ? 9.f : 0.f;
+template <typename T>
+constexpr float kRescale = std::is_same<T, __half>::value ? 6.f : 8.f;
 constexpr long long kWaitLimitCycles = 2000000000LL;  // about one second
 
 // The softmax warps' state does not fit in the 168 registers that 384 threads are
@@ -785,7 +798,7 @@ __device__ __forceinline__ void scale_o(uint32_t tO, float f) {
   }
 }
 
-// The sum of a row that sees nothing is 0 (of one that does 1 or more, but for
+// The sum of a row that sees nothing is 0 (of one that does 2^kHead or more, but for
 // roundings), and NaN where one of its logits is, and then O and LSE are NaN too.
 __device__ __forceinline__ float inverse_of(float total) {
   return total == 0.f ? 0.f : 1.f / total;
@@ -794,7 +807,7 @@ __device__ __forceinline__ float lse_of(float m, float total) {
   return total == 0.f ? -INFINITY : (m + __log2f(total)) * kLn2;
 }
 
-// One row's running shift (log2 units) and sum.
+// One row's running shift (log2 units) and the sum of its weights above it.
 struct Stats {
   float m, l;
 };
@@ -802,11 +815,11 @@ struct Stats {
 // Takes the block's row maximum of raw scores in: moves the shift when the maximum
 // outgrows it by more than kRescale, and then scales l and, once P V of block g - 1
 // has completed, O. Returns the shift to use.
-template <int D, bool SOFTCAP>
+template <typename T, int D, bool SOFTCAP>
 __device__ __forceinline__ float take_max(const Ctx& c, Stats& x, float smax, float c_log2,
                                           float cap_in, float cap_out, bool has_o, int g,
                                           uint32_t tO, bool& ok) {
-  float m_tile = -INFINITY;  // row maximum of the logits (log2 units) over this block
+  float m_tile = -INFINITY;  // the shift of this block's row maximum (log2 units)
   if (smax > -INFINITY) {
     if (SOFTCAP) {
       const float ex = ex2_approx(smax * cap_in);
@@ -814,8 +827,9 @@ __device__ __forceinline__ float take_max(const Ctx& c, Stats& x, float smax, fl
     } else {
       m_tile = smax * c_log2;
     }
+    m_tile -= kHead<T>;
   }
-  const bool need = m_tile > x.m + kRescale;
+  const bool need = m_tile > x.m + kRescale<T>;
   if (__any_sync(0xffffffffu, need)) {
     const float m_new = need ? m_tile : x.m;
     const float f = need ? ex2_approx(x.m - m_new) : 1.f;  // 0 while m = -inf
@@ -1083,7 +1097,7 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         if (!ok) break;
         const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
         const float shift =
-            take_max<D, SOFTCAP>(c, x, smax, c_log2, cap_in, cap_out, t > 0, gb, tO, ok);
+            take_max<T, D, SOFTCAP>(c, x, smax, c_log2, cap_in, cap_out, t > 0, gb, tO, ok);
         // P of the warp's 16 keys; 0 for the keys of the other quadrants: of the
         // 64 pair columns (0 .. 31 and 64 .. 95), in groups of 8 (16 keys),
         // warpgroup h writes groups h, 2 + h, 4 + h, 6 + h, its keys' one among them
@@ -1164,7 +1178,7 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         if (!ok) break;
         if (!idle) {
           const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
-          float m_tile = -INFINITY;  // row maximum of the logits (log2 units) over this block
+          float m_tile = -INFINITY;  // the shift of this block's row maximum (log2 units)
           if (smax > -INFINITY) {
             if (SOFTCAP) {
               const float ex = ex2_approx(smax * cap_in);
@@ -1172,8 +1186,9 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
             } else {
               m_tile = smax * c_log2;
             }
+            m_tile -= kHead<T>;
           }
-          const bool need = m_tile > m_used + kRescale;
+          const bool need = m_tile > m_used + kRescale<T>;
           if (__any_sync(0xffffffffu, need)) {
             const float m_new = need ? m_tile : m_used;
             const float f = need ? ex2_approx(m_used - m_new) : 1.f;  // 0 while m_used = -inf

@@ -1,0 +1,51 @@
+"""Where the attention over a paged cache can lose digits: small weights beside one
+large one in fp16.
+
+An error e of every logit moves a weight by at most 2 e of itself and LSE by e. In
+fp16 a weight's operand is rounded to half a step of 2^-24 below 2^-14, and a row's
+largest operand is 2^9 or more: 2^-34 of the row's largest weight besides half a
+step h of each.
+"""
+import numpy as np
+import pytest
+import torch
+
+import flashattention_attention_backward_gb300 as attn
+from test_gpu_cache import HF, U, Case, _half_step
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("a", [8.0, 15.5, 17.25, 20.0, 23.0])
+@pytest.mark.parametrize("d,softcap,tokens", [(64, 0.0, 1), (128, 0.0, 1), (256, 0.0, 1),
+                                              (128, 0.0, 20), (64, 30.0, 1), (128, 30.0, 1),
+                                              (128, 500.0, 20)])
+def test_small_weights_beside_a_large_one(d, softcap, tokens, a):
+    """One key that every row sees with the logit a, thousands with logit 0: what
+    the many weigh together is not lost, though each is e^-a of the one. As many
+    key/value heads as keep a tile's keys with one CTA."""
+    heads, length = 160, 4096
+    c = Case([(tokens, length)], heads, heads, d, 64, HF)
+    first = int(c.table[0, 0])
+    c.q.zero_()
+    c.q[:, :, 0] = 1.0
+    k, v = c.caches
+    k.zero_()
+    k[first, 0, :, 0] = a
+    v.uniform_(0.5, 1.5)  # one sign
+    v[first, 0] = 0.0
+    o, lse = c.attend(scale=1.0, softcap=softcap)
+    assert attn.attn_device_status(clear=True) == (0, 0)
+    z = softcap * np.tanh(a / softcap) if softcap else a
+    dense = v[c.pages_d[0, :length // 64].long()].flatten(0, 1).double()  # [length, heads, d]
+    p = torch.arange(length - tokens, length, device="cuda")
+    total = (p + np.exp(z))[:, None]
+    O, LSE = dense.cumsum(0)[p] / total[..., None], total.log()
+    # the logits are one product each, off by a rounding, under the cap by 2^-20
+    # of themselves
+    e = (2 * U + (2.0 ** -20 if softcap else 0.0)) * a
+    assert float((lse.double() - LSE).abs().max()) <= e + 2.0 ** -18 + 4 * U * float(LSE.max())
+    h = _half_step(HF)
+    tol = (2 * h + 2.0 ** -16 + 2.0 ** -20 + 2 * e) * O + 2.0 ** -25 + length * 1.5 * 2.0 ** -34
+    err = (o.double() - O).abs()
+    assert bool((err <= tol).all()), "O %.3e" % float((err - tol).max())
