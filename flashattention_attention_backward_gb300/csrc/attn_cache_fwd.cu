@@ -1066,9 +1066,8 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
     const int lo = p.left < 0 ? 0 : pos - p.left;
     const int all_hi = p.causal ? min(w.t.pos0, w.s.length - 1) : w.s.length - 1;
     const int all_lo = p.left < 0 ? 0 : w.t.pos0 + w.t.count - 1 - p.left;
-    float m_used = -INFINITY, l = 0.f;
+    Stats x{-INFINITY, 0.f};
     if (kHasNarrow<D, SOFTCAP> && narrow) {
-      Stats x{-INFINITY, 0.f};
       for (int t = 0; t < nt; ++t) {
         const int gb = g + t;
         const int n0 = w.t.block(w.blk + t) * kBn;
@@ -1130,8 +1129,6 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_addr(c, BAR_P_FULL + (gb & 1)));  // one arrival per warp
       }
-      m_used = x.m;
-      l = x.l;
     } else {
       for (int t = 0; t < nt; ++t) {
         const int gb = g + t;
@@ -1178,52 +1175,10 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         if (!ok) break;
         if (!idle) {
           const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
-          float m_tile = -INFINITY;  // the shift of this block's row maximum (log2 units)
-          if (smax > -INFINITY) {
-            if (SOFTCAP) {
-              const float ex = ex2_approx(smax * cap_in);
-              m_tile = (1.f - 2.f * rcp_approx(ex + 1.f)) * cap_out;
-            } else {
-              m_tile = smax * c_log2;
-            }
-            m_tile -= kHead<T>;
-          }
-          const bool need = m_tile > m_used + kRescale<T>;
-          if (__any_sync(0xffffffffu, need)) {
-            const float m_new = need ? m_tile : m_used;
-            const float f = need ? ex2_approx(m_used - m_new) : 1.f;  // 0 while m_used = -inf
-            // this half of the O row, once P(t - 1) V has completed; a wait that
-            // gives up is voted on at the next barrier
-            if (__any_sync(0xffffffffu, need && m_used > -INFINITY) && t > 0) {
-              if (!wait_warp(c, BAR_O_DONE + ((gb - 1) & 1), ((gb - 1) >> 1) & 1)) ok = false;
-              if (ok) {
-                tc_fence_after();
-                const uint64_t f2 = f2_make(f, f);
-#pragma unroll
-                for (int c32 = 0; c32 < D / 64; ++c32) {
-                  uint32_t o[32];
-                  tmem_ld32(tO + c32 * 32, o);
-                  uint32_t a[16], b[16];
-#pragma unroll
-                  for (int u = 0; u < 8; ++u) {
-                    const uint64_t v = f2_mul(f2_make(o[2 * u], o[2 * u + 1]), f2);
-                    const uint64_t x = f2_mul(f2_make(o[16 + 2 * u], o[17 + 2 * u]), f2);
-                    a[2 * u] = static_cast<uint32_t>(v);
-                    a[2 * u + 1] = static_cast<uint32_t>(v >> 32);
-                    b[2 * u] = static_cast<uint32_t>(x);
-                    b[2 * u + 1] = static_cast<uint32_t>(x >> 32);
-                  }
-                  tmem_st16(tO + c32 * 32, a);
-                  tmem_st16(tO + c32 * 32 + 16, b);
-                }
-              }
-            }
-            l *= f;
-            m_used = m_new;
-          }
-          const float shift = m_used > -INFINITY ? m_used : 0.f;
-          l += chunk_p<T, SOFTCAP>(p, raw, tS + 64 * h, masked, visible, c_log2, cap_in, cap_out,
-                                   shift);
+          const float shift =
+              take_max<T, D, SOFTCAP>(c, x, smax, c_log2, cap_in, cap_out, t > 0, gb, tO, ok);
+          x.l += chunk_p<T, SOFTCAP>(p, raw, tS + 64 * h, masked, visible, c_log2, cap_in,
+                                     cap_out, shift);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -1231,7 +1186,7 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         if (lane == 0) mbar_arrive(bar_addr(c, BAR_P_FULL + (gb & 1)));  // one arrival per warp
       }
     }
-    const Done done{{m_used, l}, nt, w.blk, w.t.nt, w.left, w.s.row0 + w.tile * p.tokens,
+    const Done done{x, nt, w.blk, w.t.nt, w.left, w.s.row0 + w.tile * p.tokens,
                     w.kvh, rows, narrow};
     ok = epilogue<T, D, SOFTCAP>(c, p, part, done, ok, i, h, tmem + lane_base, xsum, shifts,
                                  smem, stage, token);
