@@ -705,42 +705,61 @@ __device__ __forceinline__ bool bit_of(uint2 bits, int e) {
   return ((e < 32 ? bits.x : bits.y) >> (e & 31)) & 1u;
 }
 
+// Factors on a raw score s: its logit without a softcap (tau log2e); with one, u =
+// tau s / c, 2 u log2e, and what tanh(u) is multiplied by (c log2e).
+struct Factors {
+  float plain, u, in, out;
+};
+
+// The capped logit c tanh(u), log2 units, less the shift, of two scores, by one of
+// three forms of tanh. Up to 1/4 its Taylor sum to u^7, multiplied into the logit at
+// once: the first term left out is 62/2835 u^9, 8.4e-8 or less, the polynomial's error;
+// both shrink with u, so that a logit far below the cap is off by 2^-20 of itself. The
+// form through exp2 is off by 1e-7 of the cap: only for scores beyond the others, where
+// the logit is three quarters of the cap or more.
+enum { kTanhMufu = 0, kTanhPoly = 1, kTanhTaylor = 2 };
+constexpr float kTaylorMax = 0.25f;
+template <int FORM>
+__device__ __forceinline__ uint64_t cap_pair(const Factors& f, uint64_t s2, uint64_t nsh2) {
+  if (FORM == kTanhTaylor) {
+    const uint64_t u2 = f2_mul(s2, f2_make(f.u, f.u)), x2 = f2_mul(u2, u2);
+    uint64_t w2 = f2_fma(x2, f2_make(-5.3968254e-2f, -5.3968254e-2f),
+                         f2_make(1.3333333e-1f, 1.3333333e-1f));
+    w2 = f2_fma(w2, x2, f2_make(-3.3333333e-1f, -3.3333333e-1f));
+    w2 = f2_fma(w2, x2, f2_make(1.f, 1.f));
+    return f2_fma(f2_mul(s2, f2_make(f.plain, f.plain)), w2, nsh2);
+  }
+  const uint64_t th2 = FORM == kTanhPoly ? softcap::tanh_poly2(f2_mul(s2, f2_make(f.u, f.u)))
+                                         : softcap::tanh_mufu2(f2_mul(s2, f2_make(f.in, f.in)));
+  return f2_fma(th2, f2_make(f.out, f.out), nsh2);
+}
+// Calls body with the form that serves every score of the warp, `most` the lane's
+// largest in size.
+template <typename F>
+__device__ __forceinline__ void with_form(const Factors& f, float most, F body) {
+  most *= f.u;
+  if (__all_sync(0xffffffffu, most <= kTaylorMax))
+    body(std::integral_constant<int, kTanhTaylor>{});
+  else if (__all_sync(0xffffffffu, most <= softcap::kPolyMax))
+    body(std::integral_constant<int, kTanhPoly>{});
+  else
+    body(std::integral_constant<int, kTanhMufu>{});
+}
+
 // P = 2^(x - shift) of 64 keys as 16-bit pairs into tensor-memory columns dst ..
 // dst + 31; returns their sum (fp32, before rounding).
 template <typename T, bool SOFTCAP>
-__device__ __forceinline__ float chunk_p(const Params& p, const uint32_t (&raw)[64], uint32_t dst,
-                                         bool masked, uint2 visible, float c_log2, float cap_in,
-                                         float cap_out, float shift) {
-  const uint64_t c2v = f2_make(SOFTCAP ? cap_in : c_log2, SOFTCAP ? cap_in : c_log2);
-  const uint64_t out2 = f2_make(cap_out, cap_out);
-  const float cap_u = SOFTCAP ? p.scale / p.softcap : 0.f;  // u = tau s / c
-  const uint64_t cu2 = f2_make(cap_u, cap_u);
-  const uint64_t nsh2 = f2_make(-shift, -shift), plain2 = f2_make(c_log2, c_log2);
+__device__ __forceinline__ float chunk_p(const Factors& f, const uint32_t (&raw)[64],
+                                         uint32_t dst, bool masked, uint2 visible, float shift) {
+  const uint64_t nsh2 = f2_make(-shift, -shift), plain2 = f2_make(f.plain, f.plain);
   uint64_t sum2 = f2_make(0.f, 0.f);
   uint32_t packed[32];
-  // tanh's form: 0 through exp2, 1 the polynomial for |u| <= 1, 2 its Taylor sum up
-  // to u^7, for |u| <= 1/4, multiplied into the logit at once (the first term left
-  // out is below 8.3e-8, as the polynomial's error)
   auto p_group = [&](auto form) {
-    constexpr int FORM = decltype(form)::value;
 #pragma unroll
     for (int u = 0; u < 32; ++u) {
       const uint64_t s2 = f2_make(raw[2 * u], raw[2 * u + 1]);
-      uint64_t y2;
-      if (SOFTCAP && FORM == 2) {
-        const uint64_t u2 = f2_mul(s2, cu2), x2 = f2_mul(u2, u2);
-        uint64_t w2 = f2_fma(x2, f2_make(-5.3968254e-2f, -5.3968254e-2f),
-                             f2_make(1.3333333e-1f, 1.3333333e-1f));
-        w2 = f2_fma(w2, x2, f2_make(-3.3333333e-1f, -3.3333333e-1f));
-        w2 = f2_fma(w2, x2, f2_make(1.f, 1.f));
-        y2 = f2_fma(f2_mul(s2, plain2), w2, nsh2);
-      } else if (SOFTCAP) {
-        const uint64_t th2 = FORM == 1 ? softcap::tanh_poly2(f2_mul(s2, cu2))
-                                       : softcap::tanh_mufu2(f2_mul(s2, c2v));
-        y2 = f2_fma(th2, out2, nsh2);
-      } else {
-        y2 = f2_fma(s2, c2v, nsh2);
-      }
+      const uint64_t y2 =
+          SOFTCAP ? cap_pair<decltype(form)::value>(f, s2, nsh2) : f2_fma(s2, plain2, nsh2);
       float y0 = f2_lo(y2), y1 = f2_hi(y2);
       if (SOFTCAP && masked) {
         if (!bit_of(visible, 2 * u)) y0 = -INFINITY;
@@ -751,17 +770,10 @@ __device__ __forceinline__ float chunk_p(const Params& p, const uint32_t (&raw)[
       packed[u] = pack_pair<T>(p0, p1);
     }
   };
-  if constexpr (SOFTCAP) {
-    const float most = softcap::max_abs(raw) * cap_u;
-    if (__all_sync(0xffffffffu, most <= 0.25f))
-      p_group(std::integral_constant<int, 2>{});
-    else if (__all_sync(0xffffffffu, most <= softcap::kPolyMax))
-      p_group(std::integral_constant<int, 1>{});
-    else
-      p_group(std::integral_constant<int, 0>{});
-  } else {
+  if constexpr (SOFTCAP)
+    with_form(f, softcap::max_abs(raw), p_group);
+  else
     p_group(std::integral_constant<int, 0>{});
-  }
   uint32_t lo[16], hi[16];
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
@@ -816,16 +828,17 @@ struct Stats {
 // outgrows it by more than kRescale, and then scales l and, once P V of block g - 1
 // has completed, O. Returns the shift to use.
 template <typename T, int D, bool SOFTCAP>
-__device__ __forceinline__ float take_max(const Ctx& c, Stats& x, float smax, float c_log2,
-                                          float cap_in, float cap_out, bool has_o, int g,
-                                          uint32_t tO, bool& ok) {
+__device__ __forceinline__ float take_max(const Ctx& c, Stats& x, float smax, const Factors& fac,
+                                          bool has_o, int g, uint32_t tO, bool& ok) {
   float m_tile = -INFINITY;  // the shift of this block's row maximum (log2 units)
   if (smax > -INFINITY) {
+    // the weights' forms but the polynomial: above 1/4 an error of 1e-7 of the cap is
+    // one of 2^-20 of the logit
+    m_tile = smax * fac.plain;
     if (SOFTCAP) {
-      const float ex = ex2_approx(smax * cap_in);
-      m_tile = (1.f - 2.f * rcp_approx(ex + 1.f)) * cap_out;
-    } else {
-      m_tile = smax * c_log2;
+      const uint64_t s2 = f2_make(smax, smax), zero2 = f2_make(0.f, 0.f);
+      m_tile = f2_lo(cap_pair<kTanhTaylor>(fac, s2, zero2));
+      if (fabsf(smax) * fac.u > kTaylorMax) m_tile = f2_lo(cap_pair<kTanhMufu>(fac, s2, zero2));
     }
     m_tile -= kHead<T>;
   }
@@ -1046,9 +1059,9 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
   float* shifts = reinterpret_cast<float*>(smem + L::kShifts);
   uint8_t* stage = smem + L::kStage + (warp - 4) * 2048;
   const int wide_token = r / p.G, narrow_token = lane / p.G;
-  const float c_log2 = p.scale * kLog2e;
-  const float cap_in = SOFTCAP ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
-  const float cap_out = SOFTCAP ? p.softcap * kLog2e : 0.f;
+  const Factors fac{p.scale * kLog2e, SOFTCAP ? p.scale / p.softcap : 0.f,
+                    SOFTCAP ? 2.f * kLog2e * p.scale / p.softcap : 0.f,
+                    SOFTCAP ? p.softcap * kLog2e : 0.f};
   bool ok = true;
   int g = 0;  // blocks of all tiles before
   int i = 0;
@@ -1079,7 +1092,7 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         const int key0 = n0 + 32 * quadrant + 16 * h;
         uint32_t raw[16];
         uint32_t visible = 0xffffu;
-        float hmax = -INFINITY;
+        float hmax = -INFINITY, most = 0.f;
         if (got) {
           tc_fence_after();
           tmem_ld16(tS + 32 * quadrant + 16 * h, raw);
@@ -1089,6 +1102,7 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
           for (int e = 0; e < 16; ++e) {
             const bool seen = (visible >> e) & 1u;
             if (seen) hmax = fmaxf(hmax, __uint_as_float(raw[e]));
+            if (seen) most = fmaxf(most, fabsf(__uint_as_float(raw[e])));
           }
         }
         slot[h * 128 + r] = hmax;
@@ -1096,25 +1110,24 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         if (!ok) break;
         const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
         const float shift =
-            take_max<T, D, SOFTCAP>(c, x, smax, c_log2, cap_in, cap_out, t > 0, gb, tO, ok);
+            take_max<T, D, SOFTCAP>(c, x, smax, fac, t > 0, gb, tO, ok);
         // P of the warp's 16 keys; 0 for the keys of the other quadrants: of the
         // 64 pair columns (0 .. 31 and 64 .. 95), in groups of 8 (16 keys),
         // warpgroup h writes groups h, 2 + h, 4 + h, 6 + h, its keys' one among them
         uint32_t pairs[8], zeros[8];
+        with_form(fac, most, [&](auto form) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          // tanh of what a hidden score holds is not used
-          const uint64_t th2 = softcap::tanh_mufu2(
-              f2_mul(f2_make(raw[2 * u], raw[2 * u + 1]), f2_make(cap_in, cap_in)));
-          const float y0 =
-              (visible >> (2 * u)) & 1u ? fmaf(f2_lo(th2), cap_out, -shift) : -INFINITY;
-          const float y1 =
-              (visible >> (2 * u + 1)) & 1u ? fmaf(f2_hi(th2), cap_out, -shift) : -INFINITY;
-          const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
-          x.l += p0 + p1;
-          pairs[u] = pack_pair<T>(p0, p1);
-          zeros[u] = 0u;
-        }
+          for (int u = 0; u < 8; ++u) {
+            // the logit of what a hidden score holds is not used
+            const uint64_t y2 = cap_pair<decltype(form)::value>(
+                fac, f2_make(raw[2 * u], raw[2 * u + 1]), f2_make(-shift, -shift));
+            const float p0 = ex2_approx((visible >> (2 * u)) & 1u ? f2_lo(y2) : -INFINITY);
+            const float p1 = ex2_approx((visible >> (2 * u + 1)) & 1u ? f2_hi(y2) : -INFINITY);
+            x.l += p0 + p1;
+            pairs[u] = pack_pair<T>(p0, p1);
+            zeros[u] = 0u;
+          }
+        });
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int group = 2 * j + h;
@@ -1176,9 +1189,8 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         if (!idle) {
           const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
           const float shift =
-              take_max<T, D, SOFTCAP>(c, x, smax, c_log2, cap_in, cap_out, t > 0, gb, tO, ok);
-          x.l += chunk_p<T, SOFTCAP>(p, raw, tS + 64 * h, masked, visible, c_log2, cap_in,
-                                     cap_out, shift);
+              take_max<T, D, SOFTCAP>(c, x, smax, fac, t > 0, gb, tO, ok);
+          x.l += chunk_p<T, SOFTCAP>(fac, raw, tS + 64 * h, masked, visible, shift);
           tmem_wait_st();
         }
         tc_fence_before();
