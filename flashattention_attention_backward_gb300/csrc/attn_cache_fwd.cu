@@ -734,13 +734,15 @@ __device__ __forceinline__ uint64_t cap_pair(const Factors& f, uint64_t s2, uint
   return f2_fma(th2, f2_make(f.out, f.out), nsh2);
 }
 // Calls body with the form that serves every score of the warp, `most` the lane's
-// largest in size.
+// largest in size. A lane whose row is none of the tile's (`mine` false: another
+// sequence's query, or one of no sequence) has no say, so that what it holds changes no
+// bit of the others.
 template <typename F>
-__device__ __forceinline__ void with_form(const Factors& f, float most, F body) {
+__device__ __forceinline__ void with_form(const Factors& f, float most, bool mine, F body) {
   most *= f.u;
-  if (__all_sync(0xffffffffu, most <= kTaylorMax))
+  if (!__any_sync(0xffffffffu, mine && most > kTaylorMax))
     body(std::integral_constant<int, kTanhTaylor>{});
-  else if (__all_sync(0xffffffffu, most <= softcap::kPolyMax))
+  else if (!__any_sync(0xffffffffu, mine && most > softcap::kPolyMax))
     body(std::integral_constant<int, kTanhPoly>{});
   else
     body(std::integral_constant<int, kTanhMufu>{});
@@ -750,7 +752,8 @@ __device__ __forceinline__ void with_form(const Factors& f, float most, F body) 
 // dst + 31; returns their sum (fp32, before rounding).
 template <typename T, bool SOFTCAP>
 __device__ __forceinline__ float chunk_p(const Factors& f, const uint32_t (&raw)[64],
-                                         uint32_t dst, bool masked, uint2 visible, float shift) {
+                                         uint32_t dst, bool masked, uint2 visible, float shift,
+                                         bool mine) {
   const uint64_t nsh2 = f2_make(-shift, -shift), plain2 = f2_make(f.plain, f.plain);
   uint64_t sum2 = f2_make(0.f, 0.f);
   uint32_t packed[32];
@@ -771,7 +774,7 @@ __device__ __forceinline__ float chunk_p(const Factors& f, const uint32_t (&raw)
     }
   };
   if constexpr (SOFTCAP)
-    with_form(f, softcap::max_abs(raw), p_group);
+    with_form(f, softcap::max_abs(raw), mine, p_group);
   else
     p_group(std::integral_constant<int, 0>{});
   uint32_t lo[16], hi[16];
@@ -1115,7 +1118,7 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         // 64 pair columns (0 .. 31 and 64 .. 95), in groups of 8 (16 keys),
         // warpgroup h writes groups h, 2 + h, 4 + h, 6 + h, its keys' one among them
         uint32_t pairs[8], zeros[8];
-        with_form(fac, most, [&](auto form) {
+        with_form(fac, most, true, [&](auto form) {
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             // the logit of what a hidden score holds is not used
@@ -1190,7 +1193,8 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
           const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
           const float shift =
               take_max<T, D, SOFTCAP>(c, x, smax, fac, t > 0, gb, tO, ok);
-          x.l += chunk_p<T, SOFTCAP>(fac, raw, tS + 64 * h, masked, visible, shift);
+          x.l += chunk_p<T, SOFTCAP>(fac, raw, tS + 64 * h, masked, visible, shift,
+                                     r < rows);
           tmem_wait_st();
         }
         tc_fence_before();

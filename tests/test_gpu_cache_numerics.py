@@ -1,5 +1,6 @@
 """Where the attention over a paged cache can lose digits: small weights beside one
-large one in fp16, and softcaps far above the logits.
+large one in fp16, softcaps far above the logits, and rows of a tile that belong to
+no query of its sequence.
 
 An error e of every logit moves a weight by at most 2 e of itself and LSE by e. In
 fp16 a weight's operand is rounded to half a step of 2^-24 below 2^-14, and a row's
@@ -83,3 +84,22 @@ def test_caps_far_above_the_logits(tokens, d, dtype, softcap):
     o, lse = c.attend(softcap=softcap)
     _check(c, o, lse, scale, softcap, lambda x: ((d + 8) * 2 * U + 2.0 ** -20) * x,
            small=900 * 4 * 2.0 ** -34)
+
+
+@pytest.mark.parametrize("fill", [0.0, 300.0, float("nan"), float("inf")])
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, HF), (256, BF)])
+def test_rows_behind_change_nothing(d, dtype, fill):
+    """Rows of q behind the last sequence, and the next sequence's, stand in a tile
+    with the last tokens of a chunk and change no bit of theirs."""
+    c = Case([(20, 300), (1, 40), (20, 260)], 2, 1, d, 16, dtype, behind=120)
+    for softcap in (0.0, 20.0, 5.0):
+        o, lse = c.attend(softcap=softcap)
+        q = c.q.clone()
+        q[41:] = fill
+        o2, lse2 = c.attend(q=q, softcap=softcap)
+        assert torch.equal(o2[:41], o[:41]) and torch.equal(lse2[:41], lse[:41]), softcap
+        q[20] = fill if fill == fill and abs(fill) < 1e4 else 100.0
+        o2, lse2 = c.attend(q=q, softcap=softcap)
+        for rows in (slice(0, 20), slice(21, 41)):
+            assert torch.equal(o2[rows], o[rows]) and torch.equal(lse2[rows], lse[rows]), softcap
+    assert attn.attn_device_status(clear=True) == (0, 0)
