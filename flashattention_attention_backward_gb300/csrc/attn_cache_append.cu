@@ -255,7 +255,7 @@ extern "C" int attn_cache_append(const void* q, const void* k, const void* v, vo
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
       !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(turns))
     return ATTN_ERR_ALIGN;
-  if (H > 16384 || H_kv > 16384 ||
+  if (H > 16384 || H_kv > 16384 || B > (1 << 29) ||
       static_cast<long long>(T) * (H + 2LL * H_kv) >= (1LL << 40) / d)
     return ATTN_ERR_TOO_LARGE;
   auto at = [&](int i) { return strides != nullptr ? strides + i : nullptr; };
