@@ -67,6 +67,7 @@
 #include "attn_common.cuh"
 #include "grid_ptx.cuh"
 #include "philox.cuh"
+#include "sink_units.cuh"
 #include "sm103_ptx.cuh"
 
 namespace attn {
@@ -178,40 +179,18 @@ struct Work {
 
 // Units in heaviest-first order are u = n_block * (H_kv * B) + b * H_kv + g
 // (for a causal mask, key block 0 sees every query block). A persistent CTA
-// takes one unit per pass in snake order (pass r visits CTAs 0..grid-1 when
-// r is even, grid-1..0 when odd), which balances the shrinking causal units.
-// With sinks the first units visit every query block, the others a band's: the
-// `heavy` CTAs that have taken one more of those than the rest sit out `ahead`
-// passes, about as many units of a band as it is worth (causal GQA under a
-// window of 1024 keys: 128 query tiles against 36; snake order alone gives those
-// CTAs 200 to 236 tiles where the average is 131, and the step took 0.535 ms, not
-// 0.394).
+// takes one unit per pass, in the order of sink_units.cuh.
 template <bool SINKS, bool SPLIT>
 __device__ __forceinline__ int unit_of(int r, const Params& p) {
   const int grid = static_cast<int>(gridDim.x);
   const int cta = static_cast<int>(blockIdx.x);
-  auto snake = [&](int pass) { return pass * grid + ((pass & 1) ? grid - 1 - cta : cta); };
   if constexpr (!SINKS) {
-    const int u = snake(r);
+    const int u = snake_unit(r, cta, grid);
     return u < p.n_units ? u : -1;
   } else {
     const SinkParams& q = with_sinks(p);
     if (SPLIT) return r == 0 ? cta / q.split : -1;
-    int u;
-    if (r < q.heavy_passes) {  // all CTAs take a unit with sinks
-      u = snake(r);
-    } else {
-      r -= q.heavy_passes;
-      const int first = q.heavy_passes * grid;
-      const int light = grid - q.heavy;
-      if (q.heavy > 0 && cta < q.heavy) {
-        u = r == 0 ? first + cta : first + q.heavy + q.ahead * light + snake(r - 1);
-      } else if (r < q.ahead) {
-        u = first + q.heavy + r * light + cta - q.heavy;
-      } else {
-        u = first + q.heavy + q.ahead * light + snake(r - q.ahead);
-      }
-    }
+    const int u = sinks_unit(r, cta, grid, q.heavy_passes, q.heavy, q.ahead);
     return u < p.n_units ? q.first_unit + u : -1;
   }
 }
