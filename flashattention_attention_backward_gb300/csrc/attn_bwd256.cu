@@ -53,9 +53,11 @@
 #include <type_traits>
 
 #include "attn_common.cuh"
+#include "cluster_launch.cuh"
 #include "element.cuh"
 #include "grid_ptx.cuh"
 #include "philox.cuh"
+#include "sink_units.cuh"
 #include "sm103_ptx.cuh"
 
 namespace attn {
@@ -875,30 +877,19 @@ int launch(const CUtensorMap (&m)[7], const Params& p, long long grid, cudaStrea
   return launch_status();
 }
 
-// `units` units from the first on, each by a cluster of p.split CTAs.
+// The first units, each by a cluster of p.split CTAs.
 template <bool SOFTCAP>
-int launch_split(const CUtensorMap (&m)[7], const SplitParams& p, long long units,
+struct Split {
+  static constexpr auto kern = attn_bwd256_kernel<SOFTCAP, false, false, true>;
+  static constexpr int kBlock = kThreads, kSmem = Layout::kBytes;
+};
+template <bool SOFTCAP>
+int launch_split(const CUtensorMap (&m)[7], SplitParams& p, const SinkUnits& units, int sms,
                  cudaStream_t s) {
-  auto kern = attn_bwd256_kernel<SOFTCAP, false, false, true>;
-  static std::atomic<bool> configured[kMaxTrackedDevices];
-  if (!set_smem_limit_once(kern, Layout::kBytes, configured)) return ATTN_ERR_LAUNCH;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(p.split);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t config{};
-  config.gridDim = dim3(static_cast<unsigned>(units * p.split));
-  config.blockDim = dim3(kThreads);
-  config.dynamicSmemBytes = Layout::kBytes;
-  config.stream = s;
-  config.attrs = &attr;
-  config.numAttrs = 1;
-  if (cudaLaunchKernelEx(&config, kern, m[0], m[1], m[2], m[3], m[4], m[5], m[6], p) !=
-      cudaSuccess) {
-    cudaGetLastError();  // reported here, not by a later call
-    return ATTN_ERR_LAUNCH;
-  }
-  return ATTN_OK;
+  using Shared = Clusters<Split<SOFTCAP>>;
+  p.split = sinks_cluster_waves(units, sms, Shared::at_once);
+  if (p.split == 1) return ATTN_OK;
+  return Shared::launch(units.with_sinks, p.split, s, m[0], m[1], m[2], m[3], m[4], m[5], m[6], p);
 }
 
 }  // namespace bwd256
@@ -962,30 +953,26 @@ int bwd256_run(const void* q, const void* k, const void* v, const void* dO, cons
       !encode_bf16_3d(&m[5], dk, kD, N, hk, kBc) || !encode_bf16_3d(&m[6], dv, kD, N, hk, kBc))
     return ATTN_ERR_LAUNCH;
   if (p.sinks > 0) {  // neither dropout nor det
-    // As at d <= 128: units with sinks that outlast what an SM has on average are
-    // shared by clusters, in a launch of their own that the others' runs beside (1 x 8
-    // heads over 2 x 4096, window 512: the step takes 122 us, 211 with one launch behind
-    // the other, 700 without clusters).
+    // As at d <= 128 (1 x 8 heads over 2 x 4096, window 512: the step takes 122 us, 211
+    // with the clusters' launch in front of the others', 700 without clusters).
     const int sms = sm_count();
     if (sms <= 0) return ATTN_ERR_LAUNCH;
-    const long long heavy = 2LL * ((p.sinks + kBc - 1) / kBc) * H_kv * B;
-    const long long group = H / H_kv, most = group * p.m_blocks;
-    const long long band = std::min<long long>(
+    const long long heavy = 2LL * ((p.sinks + kBc - 1) / kBc) * H_kv * B, group = H / H_kv;
+    const long long band_tiles = std::min<long long>(
         p.m_blocks, (static_cast<long long>(p.win_left) + p.win_right + kBc - 1) / kBr + 1);
-    const long long all = heavy * most + (grid - heavy) * group * band;
-    // the last such unit has the fewest tiles: one for each CTA at least
-    const long long least = group * (p.m_blocks - (p.sinks - 1) / kBc * (kBc / kBr));
+    const SinkUnits units{heavy, grid - heavy, group * p.m_blocks, group * band_tiles,
+                          group * (p.m_blocks - (p.sinks - 1) / kBc * (kBc / kBr))};
     SplitParams q{};
-    q.split = 1;
-    while (q.split < 8 && most * sms > all * 5 / 4 * q.split && 2 * q.split <= least) q.split *= 2;
+    static_cast<Params&>(q) = p;
+    q.dk = static_cast<__nv_bfloat16*>(dk);
+    q.dv = static_cast<__nv_bfloat16*>(dv);
+    const int rc = cap ? launch_split<true>(m, q, units, sms, s)
+                       : launch_split<false>(m, q, units, sms, s);
+    if (rc != ATTN_OK) return rc;
     if (q.split > 1) {
-      static_cast<Params&>(q) = p;
-      q.dk = static_cast<__nv_bfloat16*>(dk);
-      q.dv = static_cast<__nv_bfloat16*>(dv);
-      const int rc = cap ? launch_split<true>(m, q, heavy, s) : launch_split<false>(m, q, heavy, s);
-      if (rc != ATTN_OK || heavy == grid) return rc;
+      if (units.others == 0) return ATTN_OK;
       p.first = static_cast<int>(heavy);
-      grid -= heavy;
+      grid = units.others;
     }
   }
   if (p_drop > 0.f)  // not combined with det

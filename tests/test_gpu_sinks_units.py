@@ -1,5 +1,5 @@
 """The backward with sinks where its units are shared out in ways of their own: more
-units with sinks than SMs, and as many."""
+units with sinks than SMs, as many, and at d = 256 more clusters than run at once."""
 import pytest
 import torch
 
@@ -33,3 +33,12 @@ def test_as_many_units_with_sinks_as_sms():
     """Every CTA takes one, and the others' units then come in snake order."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     _check(_w(sms, 1, 1, 300, 64, True), (20, -1), 4)
+
+
+@pytest.mark.parametrize("w,win,sinks", [
+    (_w(1, 2, 2, 2500, 256, True), (40, -1), 600),
+    (_w(2, 4, 1, 1700, 256, True), (60, -1), 1100),
+    (_w(3, 2, 1, 900, 256, False, 6.0, 2.0), (30, 20), 400),
+], ids=["2500", "1700", "900"])
+def test_more_clusters_than_run_at_once(w, win, sinks):
+    _check(w, win, sinks)

@@ -1,5 +1,5 @@
 """How the backward with sinks shares its units out (csrc/sink_units.cuh, plain C++,
-compiled here): every unit is taken once."""
+compiled here): every unit is taken once, and clusters are of sizes that can run."""
 import ctypes
 import os
 import subprocess
@@ -14,6 +14,17 @@ extern "C" int unit(int r, int cta, int grid, int passes, int heavy, int ahead) 
   return attn::sinks_unit(r, cta, grid, passes, heavy, ahead);
 }
 extern "C" int snake(int r, int cta, int grid) { return attn::snake_unit(r, cta, grid); }
+// fit: clusters of 2, 4 and 8 that run at once; *asked counts the questions
+extern "C" int cluster(long long with_sinks, long long others, long long most, long long band,
+                       long long least, int sms, const int* fit, int* asked, int waves) {
+  const attn::SinkUnits units{with_sinks, others, most, band, least};
+  auto at_once = [&](int n) {
+    ++*asked;
+    return fit[n == 2 ? 0 : n == 4 ? 1 : 2];
+  };
+  return waves ? attn::sinks_cluster_waves(units, sms, at_once)
+               : attn::sinks_cluster(units, sms, at_once);
+}
 """
 
 
@@ -26,7 +37,10 @@ def units(tmp_path_factory):
     r = subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Wextra", "-Werror", "-shared",
                         "-fPIC", "-I", CSRC, src, "-o", lib], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
-    return ctypes.CDLL(lib)
+    u = ctypes.CDLL(lib)
+    u.cluster.argtypes = [ctypes.c_longlong] * 5 + [ctypes.c_int, ctypes.POINTER(ctypes.c_int),
+                                                    ctypes.POINTER(ctypes.c_int), ctypes.c_int]
+    return u
 
 
 def _taken(f, grid, n_units):
@@ -59,3 +73,38 @@ def test_every_unit_once(units, grid):
                     count = sum(u < with_sinks for u in mine)
                     assert all(u < with_sinks for u in mine[:count]), at
                     assert count == passes + (cta < heavy), at
+
+
+def _cluster(units, u, sms=152, fit=(76, 36, 15), waves=0):
+    asked = ctypes.c_int(0)
+    n = units.cluster(*u, sms, (ctypes.c_int * 3)(*fit), ctypes.byref(asked), waves)
+    return n, asked.value
+
+
+FEW = (1, 127, 128, 9, 128)  # units with sinks, others, tiles of one of each, the fewest
+
+
+@pytest.mark.parametrize("waves", [0, 1])
+def test_clusters_that_can_run(units, waves):
+    def cluster(u, **kw):
+        return _cluster(units, u, waves=waves, **kw)
+
+    # 2 x 32 heads over 8, 4096 keys, window 1024: an SM has 131 tiles, nobody is asked
+    assert cluster((16, 496, 128, 36, 128)) == (1, 0)
+    assert cluster((320, 320, 10, 10, 10)) == (1, 0)
+    assert cluster(FEW)[0] == 8
+    # a size that cannot run is not chosen: a smaller one, or none
+    assert cluster(FEW, fit=(76, 36, 0))[0] == 4
+    assert cluster(FEW, fit=(76, 0, 0))[0] == 2
+    assert cluster(FEW, fit=(0, 36, 15))[0] == 1
+    # none larger than the fewest tiles of a unit
+    assert cluster((1, 5, 40, 2, 3))[0] == 2
+    assert cluster((1, 5, 40, 2, 1))[0] == 1
+    # nothing but units with sinks
+    assert cluster((9, 0, 72, 0, 8))[0] == 8
+
+
+def test_rounds_of_clusters(units):
+    # 16 units: clusters of 8 run 15 at a time, so they would take two rounds
+    assert _cluster(units, (16, 624, 1024, 8, 1000))[0] == 4
+    assert _cluster(units, (16, 624, 1024, 8, 1000), fit=(76, 36, 16))[0] == 8
