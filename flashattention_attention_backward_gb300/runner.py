@@ -117,10 +117,10 @@ def forward(q, k, v, scale, causal, softcap=0.0, stream=None, impl="tc", dropout
     runs attn_fwd_dropout or attn_fwd_ref_dropout; window = (left, right) runs
     attn_fwd_local or attn_fwd_ref_local, with sinks = n (the first n keys stay
     visible to the left of the window) attn_fwd_sinks or attn_fwd_ref_sinks."""
+    window, sinks = _check_sinks(sinks, window, dropout)
     B, H, H_kv, N, d = _dims(q, k, v)
     if v.shape != k.shape:
         raise ValueError("v must have the shape of k")
-    window, sinks = _check_sinks(sinks, window, dropout)
     args = (B, H, H_kv, N, d, scale, causal, softcap)
     if dropout is not None:
         fn = {"tc": attn_fwd_dropout, "ref": attn_fwd_ref_dropout}[impl]
@@ -193,6 +193,9 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
     then the gradients of what went into it, each rounded once
     (attn_bwd_finalize_rotary in place of attn_bwd_finalize, and behind
     attn_bwd_sum_partials in the deterministic form)."""
+    if sinks and deterministic:
+        raise ValueError("sinks have no deterministic variant")
+    window, sinks = _check_sinks(sinks, window, dropout)
     B, H, H_kv, N, d = _dims(q, k, v, o, do)
     if v.shape != k.shape or o.shape != q.shape or do.shape != q.shape:
         raise ValueError("v must have the shape of k, and o, dO that of q")
@@ -201,7 +204,6 @@ def backward(q, k, v, o, do, lse, scale, causal, softcap=0.0, stream=None, bufs=
         positions, pos_stride = _check_rotary(rotary, positions, B, N, d, q.device)
     elif positions is not None:
         raise ValueError("positions are those of a rotary")
-    window, sinks = _check_sinks(sinks, window, dropout)
     if dropout is None and window is not None and deterministic:
         raise ValueError("the local window has no deterministic variant")
     with _On(stream, q.device) as on:
