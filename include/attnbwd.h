@@ -34,7 +34,9 @@
  *  * `scale` is tau (usually 1/sqrt(d)); the logit is tau * q.k.
  *  * `softcap` > 0 enables the softcap: logit = c * tanh(tau q.k / c), whose
  *    derivative (1 - tanh^2) multiplies dS ([bwd-detail] §2.1(3)).
- *    softcap <= 0 disables it.
+ *    softcap <= 0 disables it. The backward's tanh is off by up to 2^-22, its
+ *    logits by up to 2^-22 c, so that a cap of 10^5 and more costs P digits that
+ *    bf16 would hold; so is the forward's shift, which is of no matter below 10^7.
  *  * `causal` != 0 applies the lower-triangular mask: key j is visible to
  *    query i iff j <= i (queries and keys share the length N).
  *  * `stream` is a cudaStream_t passed as void* (NULL = legacy default
@@ -62,7 +64,7 @@ extern "C" {
 #define ATTN_ERR_DEVICE_TIMEOUT (-6) /* a kernel gave up waiting (device status) */
 #define ATTN_ERR_DEVICE (-7)         /* a kernel detected an internal fault */
 #define ATTN_ERR_TOO_LARGE (-8)      /* a size exceeds what the kernels index */
-#define ATTN_ERR_PAGE (-9)           /* a slot outside the page table or the cache (device status) */
+#define ATTN_ERR_PAGE (-9)           /* a slot outside page table or cache (device status) */
 
 /*
  * attn_fwd_ref: simple GPU forward producing the tensors the backward needs
@@ -372,8 +374,8 @@ int attn_rotary(const void* q, const void* k, void* q_out, void* k_out,
  * came out of attn_rotary, with the adjoint of that call, in one launch:
  *   dq = bf16(R^T (scale * dq_accum)),  dk_out = bf16(R^T dk).
  * In:  dq_accum [B,H,N,d] fp32 (from attn_bwd and its forms, or from
- *      attn_bwd_sum_partials), dk [B,H_kv,N,d] bf16, both contiguous; turns, positions, pos_stride, rot, magnitude,
- *      interleaved as given to attn_rotary.
+ *      attn_bwd_sum_partials), dk [B,H_kv,N,d] bf16, both contiguous; turns,
+ *      positions, pos_stride, rot, magnitude, interleaved as given to attn_rotary.
  * Out: dq, dk_out bf16; dk_out may be dk if it is contiguous. strides: HOST
  *      array of 6 element strides, (batch, head, row) of dq and dk_out; NULL:
  *      contiguous.
@@ -470,8 +472,9 @@ int attn_dropout_add_norm_bwd(const void* dy, const void* dz_in, const void* z, 
  * new tokens of B sequences one behind another, as rows of [T, heads, d]:
  *   starts  [B + 1] int32: sequence b's rows are starts[b] .. starts[b + 1] - 1
  *           (none if equal; starts never fall). Rows outside
- *           starts[0] .. starts[B] - 1 belong to none: they are not read, and
- *           what the calls would write for them stays as it was.
+ *           starts[0] .. starts[B] - 1 belong to none: what they hold changes no
+ *           result (the attention may read such rows of q), and what the calls
+ *           would write for them stays as it was.
  *   lengths [B] int32: positions of sequence b, its new tokens the last of
  *           them: row starts[b] + i stands at position
  *           lengths[b] - (starts[b + 1] - starts[b]) + i.
@@ -517,8 +520,15 @@ int attn_cache_append(const void* q, const void* k, const void* v, void* q_out, 
  * In:  q [T,H,d]. Out: o [T,H,d], lse [T,H] fp32 contiguous (may be NULL); they
  *      overlap neither q nor the cache. Positions stay below 2^30.
  * Values in slots that no query of a sequence's call sees are never used,
- * whatever they hold (NaN too). Pages behind the window and past the sinks may
- * have been given away: their table entries are not read.
+ * whatever they hold (NaN too). Where some of a chunk's queries see a slot and
+ * others do not, a NaN or an infinity among its values may make NaN of the others'
+ * O as well (their weight of it is 0, and 0 times it NaN), as in attn_fwd. Pages
+ * behind the window and past the sinks may have been given away: their table entries
+ * are not read.
+ * Weights enter the second product in the cache's type: off by half a step of it, and
+ * with fp16 also by up to 2^-34 of the row's largest. Under a softcap a logit is off
+ * by up to 2^-20 of itself where no logit of the tokens computed together reaches
+ * three quarters of the cap, else by up to 2^-22 of the cap.
  * strides: HOST array of 10 element strides: (token, head) of q and o, (page,
  *      slot, head) of k_cache and v_cache; NULL: all contiguous. Positive
  *      multiples of 8 elements (ATTN_ERR_ALIGN; but for dimensions of one
@@ -527,7 +537,9 @@ int attn_cache_append(const void* q, const void* k, const void* v, void* q_out, 
  * (ATTN_ERR_UNSUPPORTED otherwise); scale > 0, sinks >= 0.
  * workspace: attn_cache_fwd_workspace_bytes(T, B, H, H_kv, d) bytes (an
  *      ATTN_ERR_* code, negative, for sizes that a call refuses) of device
- *      memory, whose contents need no preparation and mean nothing after.
+ *      memory, whose contents need no preparation and mean nothing after: 13, 26
+ *      or 51 MB at d = 64, 128 or 256, whatever the other sizes (how many parts
+ *      the work is cut into follows from the lengths, which only the device knows).
  *      Calls that may run at the same time (two streams, two captured graphs)
  *      need one each, and a captured call's lives as long as its graph.
  * The same call on the same lengths gives the same bits every time.
