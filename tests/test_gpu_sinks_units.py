@@ -42,3 +42,13 @@ def test_as_many_units_with_sinks_as_sms():
 ], ids=["2500", "1700", "900"])
 def test_more_clusters_than_run_at_once(w, win, sinks):
     _check(w, win, sinks)
+
+
+@pytest.mark.parametrize("w,win,sinks", [
+    (_w(1, 4, 2, 500, 128, False), (30, -1), 70),
+    (_w(1, 2, 1, 700, 64, False, 4.0, 2.0), (0, -1), 200),
+    (_w(1, 2, 2, 400, 256, False), (60, -1), 3),
+], ids=["128", "64", "256"])
+def test_no_right_bound(w, win, sinks):
+    """Every key from the window's start on, and the first ones."""
+    _check(w, win, sinks)
