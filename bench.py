@@ -43,6 +43,7 @@ UNIT = "TFLOPS"
 PEAK_FALLBACK = {"bf16_tflops": 1890.0, "hbm_gbs": 6800.0, "source": "fallback"}
 KERNEL_SOURCES = ["flashattention_attention_backward_gb300/csrc/attn_bwd.cu",
                   "flashattention_attention_backward_gb300/csrc/attn_bwd_kernel.cuh",
+                  "flashattention_attention_backward_gb300/csrc/sink_units.cuh",
                   "flashattention_attention_backward_gb300/csrc/sm103_ptx.cuh"]
 TRAFFIC_PROFILE = os.path.join(ROOT, "profiles", "attn_bwd_causal_gqa_traffic.json")
 

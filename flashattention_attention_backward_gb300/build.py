@@ -17,10 +17,10 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libattnbwd.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["attn_bwd.cu", "attn_bwd_sinks.cu", "attn_bwd256.cu", "attn_fwd.cu", "attn_fwd_ref.cu", "attn_prepost.cu",
-           "attn_noalloc.cu", "attn_rotary.cu", "attn_cache_append.cu", "attn_cache_fwd.cu",
-           "attn_norm.cu",
-           "attn_norm_bf16.cu", "attn_norm_fp16.cu", "attn_norm_fp32.cu"]
+SOURCES = ["attn_bwd.cu", "attn_bwd_sinks.cu", "attn_bwd256.cu", "attn_fwd.cu",
+           "attn_fwd_ref.cu", "attn_prepost.cu", "attn_noalloc.cu", "attn_rotary.cu",
+           "attn_cache_append.cu", "attn_cache_fwd.cu", "attn_norm.cu", "attn_norm_bf16.cu",
+           "attn_norm_fp16.cu", "attn_norm_fp32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fno-strict-aliasing"]

@@ -684,8 +684,8 @@ __device__ __forceinline__ void join_sums(const SplitParams& p, const Work& w, u
 
 template <bool DET, bool SPLIT>
 __device__ void drain_role(const Ctx& c, const Params& p, const Work& w, uint8_t* smem,
-                           uint32_t sbase, uint32_t tmem, const CUtensorMap* tm_dq, const CUtensorMap* tm_dk,
-                           const CUtensorMap* tm_dv) {
+                           uint32_t sbase, uint32_t tmem, const CUtensorMap* tm_dq,
+                           const CUtensorMap* tm_dk, const CUtensorMap* tm_dv) {
   using L = Layout;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;

@@ -156,7 +156,7 @@ struct Params {
 
 // What the kernels with sinks need besides. The others take Params alone: a few
 // words more made the compiler spill 344 bytes a thread of the dropout form's
-// softmax, not 110, for 2 % of its time.
+// softmax at d = 128, not 128, for 2 % of its time.
 struct SinkParams : Params {
   int sinks;       // the first keys, visible to the left of the band too
   int first_unit;  // the first unit of this launch
@@ -774,11 +774,11 @@ __device__ void softmax_role(const Ctx& c, const Params& p, uint8_t* smem, uint3
       const int dsbuf = (tl == 0 && ur > 0) ? ((ur - 1) & 1) : -1;
       const uint32_t bh = static_cast<uint32_t>(w.b * p.H + h);
       if (masked)
-        ok = softmax_tile<D, SOFTCAP, CAUSAL, true, DROP, SINKS>(c, p, smem, sbase, tmem, t, half, r,
-                                                          key, m0, dsbuf, bh);
+        ok = softmax_tile<D, SOFTCAP, CAUSAL, true, DROP, SINKS>(c, p, smem, sbase, tmem, t, half,
+                                                                 r, key, m0, dsbuf, bh);
       else
-        ok = softmax_tile<D, SOFTCAP, CAUSAL, false, DROP, SINKS>(c, p, smem, sbase, tmem, t, half, r,
-                                                           key, m0, dsbuf, bh);
+        ok = softmax_tile<D, SOFTCAP, CAUSAL, false, DROP, SINKS>(c, p, smem, sbase, tmem, t, half,
+                                                                  r, key, m0, dsbuf, bh);
     }
     tg += w.T;
   }
@@ -898,8 +898,9 @@ __device__ void dq_role(const Ctx& c, const Params& p, uint8_t* smem, uint32_t s
   const int G = p.H / p.H_kv;
   for (int ur = 0, tl = 0; ok; ++tl) {
     if (tl == T) {  // unit boundary: epilogue of the finished unit, then the next unit
-      if (!SPLIT && ur > 0 && !(ok = dq_epilogue<D>(c, p, kvh, row0, sbase, tmem, stage, part, r, ur - 1,
-                                          leader, tm_dk, tm_dv)))
+      if (!SPLIT && ur > 0 &&
+          !(ok = dq_epilogue<D>(c, p, kvh, row0, sbase, tmem, stage, part, r, ur - 1, leader,
+                                tm_dk, tm_dv)))
         break;
       tg += T;
       tl = 0;

@@ -405,10 +405,10 @@ __device__ __forceinline__ void mask_scores(uint32_t (&raw)[64], uint2 visible) 
     if (!bit_of(visible, e)) raw[e] = 0xff800000u;  // -inf
 }
 
-// P = 2^(x - shift) of 64 keys (S columns src .. src + 63) as bf16 pairs in columns dst .. dst + 31; returns their sum of P (fp32,
-// before rounding and before dropout). With DROP the bf16 values are
-// P o Z / (1 - p), Z the keep mask whose bit j of kb0 (kb1) belongs to key
-// key0 + j (key0 + 32 + j): the exponent carries log2(1 / (1 - p)), so exp2
+// P = 2^(x - shift) of 64 keys, raw their scores, as bf16 pairs in columns dst ..
+// dst + 31; returns their sum of P (fp32, before rounding and before dropout). With DROP
+// the bf16 values are P o Z / (1 - p), Z the keep mask whose bit j of kb0 (kb1) belongs
+// to the group's key j (32 + j): the exponent carries log2(1 / (1 - p)), so exp2
 // gives P / (1 - p), and the sum returned is that of P / (1 - p) over every
 // key (the caller multiplies the row sum by 1 - p at the end). dst may
 // overlap src: every S value of the chunk is read before the first P is
