@@ -715,8 +715,8 @@ struct Factors {
 // three forms of tanh. Up to 1/4 its Taylor sum to u^7, multiplied into the logit at
 // once: the first term left out is 62/2835 u^9, 8.4e-8 or less, the polynomial's error;
 // both shrink with u, so that a logit far below the cap is off by 2^-20 of itself. The
-// form through exp2 is off by 1e-7 of the cap: only for scores beyond the others, where
-// the logit is three quarters of the cap or more.
+// form through exp2 is off by 1e-7 of the cap: it serves warps that have a score beyond
+// 1, whose logit is three quarters of the cap or more.
 enum { kTanhMufu = 0, kTanhPoly = 1, kTanhTaylor = 2 };
 constexpr float kTaylorMax = 0.25f;
 template <int FORM>
@@ -1112,8 +1112,7 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         ok = named_bar_and(kBarBoth, 256, ok && got);
         if (!ok) break;
         const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
-        const float shift =
-            take_max<T, D, SOFTCAP>(c, x, smax, fac, t > 0, gb, tO, ok);
+        const float shift = take_max<T, D, SOFTCAP>(c, x, smax, fac, t > 0, gb, tO, ok);
         // P of the warp's 16 keys; 0 for the keys of the other quadrants: of the
         // 64 pair columns (0 .. 31 and 64 .. 95), in groups of 8 (16 keys),
         // warpgroup h writes groups h, 2 + h, 4 + h, 6 + h, its keys' one among them
@@ -1191,10 +1190,9 @@ __device__ void softmax_role(const Ctx& c, const Params& p, const Part& part, ui
         if (!ok) break;
         if (!idle) {
           const float smax = fmaxf(hmax, slot[(1 - h) * 128 + r]);
-          const float shift =
-              take_max<T, D, SOFTCAP>(c, x, smax, fac, t > 0, gb, tO, ok);
-          x.l += chunk_p<T, SOFTCAP>(fac, raw, tS + 64 * h, masked, visible, shift,
-                                     r < rows);
+          const float shift = take_max<T, D, SOFTCAP>(c, x, smax, fac, t > 0, gb, tO, ok);
+          x.l +=
+              chunk_p<T, SOFTCAP>(fac, raw, tS + 64 * h, masked, visible, shift, r < rows);
           tmem_wait_st();
         }
         tc_fence_before();

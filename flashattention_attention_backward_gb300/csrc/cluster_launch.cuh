@@ -30,7 +30,10 @@ struct Clusters {
   static int at_once(int ctas) {
     static std::atomic<int> known[kMaxTrackedDevices][3];
     static std::atomic<bool> configured[kMaxTrackedDevices];
-    if (!set_smem_limit_once(K::kern, K::kSmem, configured)) return 0;
+    if (!set_smem_limit_once(K::kern, K::kSmem, configured)) {
+      cudaGetLastError();  // not for the launch that does without clusters to report
+      return 0;
+    }
     const int s = ctas == 2 ? 0 : ctas == 4 ? 1 : 2;
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
